@@ -22,9 +22,6 @@ import torch
 
 own = False
 
-if own:
-    import mixed_precision_w4a16_repack_amd as w4
-
 DEV = "cuda"
 EPS = 1e-5
 DTYPES = {"f16": torch.float16, "bf16": torch.bfloat16}
@@ -306,6 +303,8 @@ def _plain(st):
 
 
 def _own(st):
+    import mixed_precision_w4a16_repack_amd as w4
+
     case = st["case"]
     dt = DTYPES[case["dtype"]]
     if case["op"] in ("norm", "act"):
