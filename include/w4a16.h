@@ -316,6 +316,127 @@ w4a16_status w4a8_gemm(const int8_t *qa, const float *xs, int64_t M, int64_t ldq
                        int64_t K, int32_t group_size, int32_t dtype, const void *bias, void *C, int64_t ldc,
                        void *workspace, size_t workspace_bytes, hipStream_t stream);
 
+/* ---- The operators between a decoder layer's GEMMs: norm, gate, key/value
+ * cache and the attention of single tokens. Conventions as above; act dtype
+ * rows need only 2-byte alignment, any stride and any width unless a call
+ * says otherwise; strides are in elements; every statistic, sum and scale is
+ * fp32 and each output is rounded once. */
+
+/* RMS norm of rows, with the residual's addition:
+ *   h = x (+ residual)                        (fp32, not rounded)
+ *   y[m, k] = h[m, k] / sqrt(mean_k(h[m, :]^2) + eps) * weight[k]
+ *   residual_out = h rounded to the act dtype
+ *   x            [M, ldx] act dtype, ldx >= K;  weight [K] act dtype
+ *   residual     [M, ldr] act dtype, ldr >= K, or NULL
+ *   residual_out [M, ldro] act dtype, ldro >= K, or NULL (not written); may
+ *                be the residual or x itself (same pointer and stride)
+ *   y            [M, ldy] act dtype, ldy >= K; may be x itself if
+ *                residual_out is not
+ * eps >= 0 and finite. M == 0 is a no-op. A row whose sum of squares passes
+ * the fp32 range, or that holds a NaN, has no defined values. */
+w4a16_status w4a16_rmsnorm(const void *x, int64_t M, int64_t K, int64_t ldx, int32_t dtype, const void *weight,
+                           float eps, const void *residual, int64_t ldr, void *residual_out, int64_t ldro, void *y,
+                           int64_t ldy, hipStream_t stream);
+
+/* The same norm with y as the input of w4a8_gemm: codes and a scale per row,
+ * quantised from the fp32 values,
+ *   xs[m] = max_k |y[m, k]| / 127,  qa[m, k] = rint(y[m, k] / xs[m])
+ * with w4a8_quantize's order of codes, row of zeros and rules for K, qa, ldq
+ * and xs. A quotient within fp32's rounding of a tie may go to either code. */
+w4a16_status w4a8_rmsnorm(const void *x, int64_t M, int64_t K, int64_t ldx, int32_t dtype, const void *weight,
+                          float eps, const void *residual, int64_t ldr, void *residual_out, int64_t ldro, int8_t *qa,
+                          int64_t ldq, float *xs, hipStream_t stream);
+
+/* The gate of a fused gate/up product: x [M, ldx] act dtype, ldx >= 2 K, holds
+ * the gate in columns 0 .. K - 1 and the up projection in K .. 2 K - 1;
+ *   y[m, k] = silu(x[m, k]) * x[m, K + k],  silu(g) = g / (1 + exp(-g))
+ * y [M, ldy] act dtype, ldy >= K; must not overlap x. M == 0 is a no-op. */
+w4a16_status w4a16_silu_mul(const void *x, int64_t M, int64_t K, int64_t ldx, int32_t dtype, void *y, int64_t ldy,
+                            hipStream_t stream);
+
+/* The same with codes and a scale per row, as w4a8_rmsnorm writes them. */
+w4a16_status w4a8_silu_mul(const void *x, int64_t M, int64_t K, int64_t ldx, int32_t dtype, int8_t *qa, int64_t ldq,
+                           float *xs, hipStream_t stream);
+
+/* Paged key/value cache. A cache is `pages` pages of page_size tokens for
+ * kv_heads heads of head_dim; token `offset` of page `page` has the slot
+ * page * page_size + offset. head_dim is 64, 128, 192 or 256, page_size a
+ * multiple of 32. `kind` is a w4a16_kv_kind: 16-bit values in the act dtype,
+ * or int8 codes with one fp32 scale per token and head for the key and one
+ * for the value (scale = max_d |x| / 127, code = rint(x / scale), a row of
+ * zeros has scale 0).
+ *
+ * Layout: page p, head h is a record of R bytes at (p * kv_heads + h) * R,
+ * where D = head_dim, P = page_size, R = 4 P D (16 bit) or 2 P D + 8 P (int8):
+ * keys, then values, then (int8) P key scales and P value scales. Keys and
+ * values are 1024-byte tiles, each one 16-byte load per lane of a wavefront
+ * and an operand of the matrix instructions as it stands:
+ *   key (t, d), 16 bit: tile (t / 16) * (D / 32) + d / 32, 16-byte unit
+ *     16 * (d % 32 / 8) + t % 16, value d % 8 of the unit;
+ *   key (t, d), int8: tile (t / 16) * (D / 64) + d / 64, the same unit, byte
+ *     8 * (d % 64 / 32) + d % 8;
+ *   value (t, d), 16 bit: tile (t / 32) * (D / 16) + d / 16, unit
+ *     16 * (t % 16 / 4) + d % 16, value 4 * (t % 32 / 16) + t % 4;
+ *   value (t, d), int8: tile (t / 32) * (D / 32) + d / 32, the same unit, byte
+ *     8 * (d % 32 / 16) + 4 * (t % 32 / 16) + t % 4.
+ * The caller owns the cache (16-byte aligned) and the assignment of pages;
+ * a cache need not be cleared before its first use. */
+typedef enum { W4A16_KV_ACT = 0, W4A16_KV_INT8 = 1 } w4a16_kv_kind;
+
+/* Bytes of a cache. out_bytes is a host pointer. */
+w4a16_status w4a16_kv_cache_size(int64_t pages, int32_t kv_heads, int32_t head_dim, int32_t page_size, int32_t kind,
+                                 size_t *out_bytes);
+
+/* Writes T tokens' keys and values to their slots:
+ *   k, v   element (token, head, d) at token * ts + head * hs + d, act dtype
+ *   slots  [T] int64 (device); a token whose slot is outside
+ *          [0, pages * page_size) is skipped (padding: -1). Two tokens of one
+ *          call must not have the same slot.
+ * No other slot's bytes change. T == 0 is a no-op. W4A16_ERR_SIZE if
+ * cache_bytes is less than w4a16_kv_cache_size(). */
+w4a16_status w4a16_kv_write(const void *k, int64_t k_ts, int64_t k_hs, const void *v, int64_t v_ts, int64_t v_hs,
+                            int64_t T, const int64_t *slots, void *cache, size_t cache_bytes, int64_t pages,
+                            int32_t kv_heads, int32_t head_dim, int32_t page_size, int32_t kind, int32_t dtype,
+                            hipStream_t stream);
+
+/* Reads slots back to rows of the same form as w4a16_kv_write's, in the act
+ * dtype (int8: code * scale, rounded once). The rows of a slot outside the
+ * cache are zeros. The rows of k and v must not overlap. */
+w4a16_status w4a16_kv_read(const int64_t *slots, int64_t T, const void *cache, size_t cache_bytes, int64_t pages,
+                           int32_t kv_heads, int32_t head_dim, int32_t page_size, int32_t kind, int32_t dtype, void *k,
+                           int64_t k_ts, int64_t k_hs, void *v, int64_t v_ts, int64_t v_hs, hipStream_t stream);
+
+/* Bytes of device workspace w4a16_attention needs for these arguments (0 if
+ * none). It starts with the counter region of w4a16_workspace_size(), with
+ * the same rule: w4a16_workspace_counter_bytes() zero bytes before the first
+ * use, left zero by every completed call. Calls that share a workspace must
+ * be ordered. out_bytes is a host pointer. */
+w4a16_status w4a16_attention_workspace_size(int64_t B, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
+                                            int32_t page_size, int64_t table_width, int64_t window, int32_t kind,
+                                            size_t *out_bytes);
+
+/* Attention of one new token per sequence over the cache:
+ *   out[b, i] = sum_t p_t v_t,  p = softmax_t(scale * q[b, i] . k_t)
+ * where query head i reads kv head i / (q_heads / kv_heads) and t runs over
+ * the sequence's tokens max(0, n - window) .. n - 1 (window 0: all), n =
+ * lengths[b] clamped to [0, table_width * page_size]. Token t lies in page
+ * table[b * table_ld + t / page_size] at offset t % page_size; tokens of a
+ * page number outside [0, pages) are not seen, nor is anything read from
+ * them. Memory of unseen tokens may hold anything, NaN included. A sequence
+ * that sees nothing, or only scores of -infinity, gives zeros.
+ *   q, out  element (b, head, d) at b * bs + head * hs + d, act dtype
+ *   table   [B, table_ld] int32, table_ld >= table_width (device)
+ *   lengths [B] int32 (device)
+ * q_heads must be a multiple of kv_heads; scale finite; B == 0 is a no-op. The
+ * result does not depend on the workspace's contents or on earlier calls
+ * (no float atomics: the order of every sum is fixed). W4A16_ERR_SIZE if the
+ * cache or the workspace is too small. */
+w4a16_status w4a16_attention(const void *q, int64_t q_bs, int64_t q_hs, int64_t B, int32_t q_heads, const void *cache,
+                             size_t cache_bytes, int64_t pages, int32_t kv_heads, int32_t head_dim, int32_t page_size,
+                             int32_t kind, int32_t dtype, const int32_t *table, int64_t table_width, int64_t table_ld,
+                             const int32_t *lengths, int64_t window, float scale, void *out, int64_t o_bs, int64_t o_hs,
+                             void *workspace, size_t workspace_bytes, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

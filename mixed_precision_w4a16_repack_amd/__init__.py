@@ -8,8 +8,11 @@ library's message on any non-zero status. It never falls back to another
 implementation: without the built library every call raises.
 
 Names follow the C ABI (include/w4a16.h): ``packed_size``, ``repack``,
-``unpack``, ``workspace_size``, ``select_path``, ``gemm``, and the dense
-prefill variant ``dequant`` and ``gemm_dense``.
+``unpack``, ``workspace_size``, ``select_path``, ``gemm``, the dense
+prefill variant ``dequant`` and ``gemm_dense``, and the operators between a
+decoder layer's GEMMs: ``rmsnorm``, ``silu_mul`` (and their int8 forms
+``rmsnorm_a8``, ``silu_mul_a8``), ``kv_cache_size``, ``kv_write``,
+``kv_read`` and ``attention``.
 """
 
 from __future__ import annotations
@@ -31,10 +34,13 @@ PATH_AUTO = 0
 PATH_SKINNY = 1
 PATH_MFMA = 2
 
+KV_ACT = 0
+KV_INT8 = 1
+
 _DTYPE_CODE = {torch.float16: F16, torch.bfloat16: BF16}
 
 # C ABI function signatures: name -> (restype, argtypes)
-_P, _I64, _I32, _SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_size_t
+_P, _I64, _I32, _SZ, _F32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_size_t, ctypes.c_float
 SIGNATURES = {
     "w4a16_abi_version": (_I32, []),
     "w4a16_last_error": (ctypes.c_char_p, []),
@@ -60,6 +66,26 @@ SIGNATURES = {
     "w4a16_gemm_dense": (
         ctypes.c_int,
         [_P, _I64, _I64, _P, _I64, _I64, _I64, _I32, _P, _P, _I64, _P, _SZ, _P],
+    ),
+    "w4a16_rmsnorm": (ctypes.c_int, [_P, _I64, _I64, _I64, _I32, _P, _F32, _P, _I64, _P, _I64, _P, _I64, _P]),
+    "w4a8_rmsnorm": (ctypes.c_int, [_P, _I64, _I64, _I64, _I32, _P, _F32, _P, _I64, _P, _I64, _P, _I64, _P, _P]),
+    "w4a16_silu_mul": (ctypes.c_int, [_P, _I64, _I64, _I64, _I32, _P, _I64, _P]),
+    "w4a8_silu_mul": (ctypes.c_int, [_P, _I64, _I64, _I64, _I32, _P, _I64, _P, _P]),
+    "w4a16_kv_cache_size": (ctypes.c_int, [_I64, _I32, _I32, _I32, _I32, ctypes.POINTER(_SZ)]),
+    "w4a16_kv_write": (
+        ctypes.c_int,
+        [_P, _I64, _I64, _P, _I64, _I64, _I64, _P, _P, _SZ, _I64, _I32, _I32, _I32, _I32, _I32, _P],
+    ),
+    "w4a16_kv_read": (
+        ctypes.c_int,
+        [_P, _I64, _P, _SZ, _I64, _I32, _I32, _I32, _I32, _I32, _P, _I64, _I64, _P, _I64, _I64, _P],
+    ),
+    "w4a16_attention_workspace_size": (
+        ctypes.c_int, [_I64, _I32, _I32, _I32, _I32, _I64, _I64, _I32, ctypes.POINTER(_SZ)]),
+    "w4a16_attention": (
+        ctypes.c_int,
+        [_P, _I64, _I64, _I64, _I32, _P, _SZ, _I64, _I32, _I32, _I32, _I32, _I32, _P, _I64, _I64, _P, _I64, _F32,
+         _P, _I64, _I64, _P, _SZ, _P],
     ),
 }
 
@@ -398,4 +424,216 @@ def gemm_dense(A: torch.Tensor, W: torch.Tensor, bias: torch.Tensor | None = Non
         _ptr(A), M, A.stride(0), _ptr(W), N, K, W.stride(0), _DTYPE_CODE[A.dtype], _ptr(bias), _ptr(out),
         out.stride(0), _ptr(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size(),
         _stream(A)))
+    return out
+
+
+def _same_device(first: torch.Tensor, **others: torch.Tensor | None):
+    for name, t in others.items():
+        if t is not None and t.device != first.device:
+            raise ValueError(f"{name} is on {t.device}, expected {first.device}")
+
+
+def _rows(name: str, t: torch.Tensor | None, M: int, K: int, dtype):
+    if t is None:
+        return
+    _need_cuda(name, t, dtype)
+    if tuple(t.shape) != (M, K) or t.stride(1) != 1:
+        raise ValueError(f"{name} must be [M={M}, K={K}] with unit column stride, got {tuple(t.shape)} {t.stride()}")
+
+
+def _ld(t: torch.Tensor | None) -> int:
+    """Row stride of [M, K] rows (torch gives a single row any stride)."""
+    if t is None:
+        return 0
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+
+
+def _codes_out(out, M: int, K: int, device):
+    if out is None:
+        return (torch.empty((M, K), dtype=torch.int8, device=device),
+                torch.empty((M,), dtype=torch.float32, device=device))
+    qa, xs = out
+    _need_cuda("qa", qa, torch.int8)
+    _need_cuda("xs", xs, torch.float32)
+    if tuple(qa.shape) != (M, K) or qa.stride(1) != 1 or xs.shape != (M,) or not xs.is_contiguous():
+        raise ValueError(f"out must be (qa [M={M}, K={K}] with unit column stride, contiguous xs [M={M}])")
+    return qa, xs
+
+
+def _norm_args(x, weight, residual, residual_out):
+    _need_cuda("x", x, (torch.float16, torch.bfloat16))
+    if x.dim() != 2 or x.stride(1) != 1:
+        raise ValueError("x must be 2-D with unit column stride")
+    M, K = x.shape
+    _need_cuda("weight", weight, x.dtype)
+    if tuple(weight.shape) != (K,) or not weight.is_contiguous():
+        raise ValueError(f"weight must be a contiguous [K={K}] tensor")
+    _rows("residual", residual, M, K, x.dtype)
+    _rows("residual_out", residual_out, M, K, x.dtype)
+    _same_device(x, weight=weight, residual=residual, residual_out=residual_out)
+    return M, K
+
+
+def rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-5, residual: torch.Tensor | None = None,
+            residual_out: torch.Tensor | None = None, out: torch.Tensor | None = None) -> torch.Tensor:
+    """y = h / sqrt(mean(h^2) + eps) * weight per row of h = x (+ residual).
+
+    ``residual_out`` (which may be ``residual`` itself) receives h."""
+    M, K = _norm_args(x, weight, residual, residual_out)
+    if out is None:
+        out = torch.empty((M, K), dtype=x.dtype, device=x.device)
+    _rows("out", out, M, K, x.dtype)
+    _same_device(x, out=out)
+    _check(load_library().w4a16_rmsnorm(
+        _ptr(x), M, K, _ld(x), _DTYPE_CODE[x.dtype], _ptr(weight), eps, _ptr(residual), _ld(residual),
+        _ptr(residual_out), _ld(residual_out), _ptr(out), _ld(out), _stream(x)))
+    return out
+
+
+def rmsnorm_a8(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-5, residual: torch.Tensor | None = None,
+               residual_out: torch.Tensor | None = None, out: tuple[torch.Tensor, torch.Tensor] | None = None):
+    """``rmsnorm`` as the input of ``gemm_w4a8``: (qa [M, K] int8, xs [M] fp32), as ``quantize_a8`` stores them."""
+    M, K = _norm_args(x, weight, residual, residual_out)
+    qa, xs = _codes_out(out, M, K, x.device)
+    _same_device(x, qa=qa, xs=xs)
+    _check(load_library().w4a8_rmsnorm(
+        _ptr(x), M, K, _ld(x), _DTYPE_CODE[x.dtype], _ptr(weight), eps, _ptr(residual), _ld(residual),
+        _ptr(residual_out), _ld(residual_out), _ptr(qa), _ld(qa), _ptr(xs), _stream(x)))
+    return qa, xs
+
+
+def _gate_args(x):
+    _need_cuda("x", x, (torch.float16, torch.bfloat16))
+    if x.dim() != 2 or x.stride(1) != 1 or x.shape[1] % 2:
+        raise ValueError(f"x must be [M, 2*K] with unit column stride, got {tuple(x.shape)} {x.stride()}")
+    return x.shape[0], x.shape[1] // 2
+
+
+def silu_mul(x: torch.Tensor, out: torch.Tensor | None = None) -> torch.Tensor:
+    """silu(g) * u of x [M, 2K] = [g | u] (a fused gate/up product)."""
+    M, K = _gate_args(x)
+    if out is None:
+        out = torch.empty((M, K), dtype=x.dtype, device=x.device)
+    _rows("out", out, M, K, x.dtype)
+    _same_device(x, out=out)
+    _check(load_library().w4a16_silu_mul(_ptr(x), M, K, _ld(x), _DTYPE_CODE[x.dtype], _ptr(out), _ld(out), _stream(x)))
+    return out
+
+
+def silu_mul_a8(x: torch.Tensor, out: tuple[torch.Tensor, torch.Tensor] | None = None):
+    """``silu_mul`` as the input of ``gemm_w4a8``: (qa [M, K] int8, xs [M] fp32)."""
+    M, K = _gate_args(x)
+    qa, xs = _codes_out(out, M, K, x.device)
+    _same_device(x, qa=qa, xs=xs)
+    _check(load_library().w4a8_silu_mul(_ptr(x), M, K, _ld(x), _DTYPE_CODE[x.dtype], _ptr(qa), _ld(qa), _ptr(xs),
+                                        _stream(x)))
+    return qa, xs
+
+
+def kv_cache_size(pages: int, kv_heads: int, head_dim: int, page_size: int, kind: int) -> int:
+    """Bytes of a paged key/value cache (allocate them as uint8)."""
+    out = _SZ(0)
+    _check(load_library().w4a16_kv_cache_size(pages, kv_heads, head_dim, page_size, kind, ctypes.byref(out)))
+    return int(out.value)
+
+
+def _heads(name: str, t: torch.Tensor, shape, dtype):
+    _need_cuda(name, t, dtype)
+    if t.dim() != 3 or tuple(t.shape) != tuple(shape) or t.stride(2) != 1:
+        raise ValueError(f"{name} must be {list(shape)} with unit stride in its last dimension, "
+                         f"got {tuple(t.shape)} {t.stride()}")
+
+
+def _cache_bytes(cache: torch.Tensor) -> int:
+    _need_cuda("cache", cache)
+    if not cache.is_contiguous():
+        raise ValueError("cache must be contiguous")
+    return cache.numel() * cache.element_size()
+
+
+def _slots(slots: torch.Tensor) -> int:
+    _need_cuda("slots", slots, torch.int64)
+    if slots.dim() != 1 or not slots.is_contiguous():
+        raise ValueError("slots must be a contiguous [T] tensor")
+    return slots.shape[0]
+
+
+def kv_write(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, cache: torch.Tensor, pages: int, page_size: int,
+             kind: int) -> None:
+    """Writes keys and values [T, kv_heads, head_dim] to their slots (page * page_size + offset; -1: not written).
+
+    Any token and head strides; ``kind`` is ``KV_ACT`` (values in k's dtype) or ``KV_INT8``."""
+    _need_cuda("k", k, (torch.float16, torch.bfloat16))
+    T = _slots(slots)
+    if k.dim() != 3:
+        raise ValueError("k must be [T, kv_heads, head_dim]")
+    H, D = k.shape[1:]
+    _heads("k", k, (T, H, D), k.dtype)
+    _heads("v", v, (T, H, D), k.dtype)
+    nbytes = _cache_bytes(cache)
+    _same_device(k, v=v, slots=slots, cache=cache)
+    _check(load_library().w4a16_kv_write(
+        _ptr(k), k.stride(0), k.stride(1), _ptr(v), v.stride(0), v.stride(1), T, _ptr(slots), _ptr(cache), nbytes,
+        pages, H, D, page_size, kind, _DTYPE_CODE[k.dtype], _stream(k)))
+
+
+def kv_read(slots: torch.Tensor, cache: torch.Tensor, pages: int, kv_heads: int, head_dim: int, page_size: int,
+            kind: int, dtype: torch.dtype, out: tuple[torch.Tensor, torch.Tensor] | None = None):
+    """The keys and values [T, kv_heads, head_dim] of slots, in ``dtype`` (zeros for a slot outside the cache)."""
+    T = _slots(slots)
+    if dtype not in _DTYPE_CODE:
+        raise ValueError(f"dtype {dtype} is not fp16 or bf16")
+    shape = (T, kv_heads, head_dim)
+    if out is None:
+        out = (torch.empty(shape, dtype=dtype, device=slots.device), torch.empty(shape, dtype=dtype, device=slots.device))
+    k, v = out
+    _heads("k", k, shape, dtype)
+    _heads("v", v, shape, dtype)
+    nbytes = _cache_bytes(cache)
+    _same_device(slots, k=k, v=v, cache=cache)
+    _check(load_library().w4a16_kv_read(
+        _ptr(slots), T, _ptr(cache), nbytes, pages, kv_heads, head_dim, page_size, kind, _DTYPE_CODE[dtype],
+        _ptr(k), k.stride(0), k.stride(1), _ptr(v), v.stride(0), v.stride(1), _stream(slots)))
+    return k, v
+
+
+def attention_workspace_size(B: int, q_heads: int, kv_heads: int, head_dim: int, page_size: int, table_width: int,
+                             window: int, kind: int) -> int:
+    out = _SZ(0)
+    _check(load_library().w4a16_attention_workspace_size(B, q_heads, kv_heads, head_dim, page_size, table_width,
+                                                         window, kind, ctypes.byref(out)))
+    return int(out.value)
+
+
+def attention(q: torch.Tensor, cache: torch.Tensor, table: torch.Tensor, lengths: torch.Tensor, pages: int,
+              kv_heads: int, page_size: int, kind: int, window: int = 0, scale: float | None = None,
+              out: torch.Tensor | None = None, workspace: Workspace | None = None) -> torch.Tensor:
+    """Attention of one new token per sequence over the cache: q [B, q_heads, head_dim] -> the same shape.
+
+    ``table`` [B, width] int32 holds each sequence's pages, ``lengths`` [B] int32 its tokens (the new one
+    included); ``window`` > 0 sees only the last tokens; ``scale`` defaults to head_dim ** -0.5."""
+    _need_cuda("q", q, (torch.float16, torch.bfloat16))
+    if q.dim() != 3:
+        raise ValueError("q must be [B, q_heads, head_dim]")
+    B, Hq, D = q.shape
+    _heads("q", q, (B, Hq, D), q.dtype)
+    if out is None:
+        out = torch.empty((B, Hq, D), dtype=q.dtype, device=q.device)
+    _heads("out", out, (B, Hq, D), q.dtype)
+    _need_cuda("table", table, torch.int32)
+    _need_cuda("lengths", lengths, torch.int32)
+    if table.dim() != 2 or table.shape[0] != B or (table.shape[1] > 1 and table.stride(1) != 1):
+        raise ValueError(f"table must be [B={B}, width] with unit column stride")
+    if tuple(lengths.shape) != (B,) or not lengths.is_contiguous():
+        raise ValueError(f"lengths must be a contiguous [B={B}] tensor")
+    nbytes = _cache_bytes(cache)
+    _same_device(q, cache=cache, table=table, lengths=lengths, out=out)
+    width = table.shape[1]
+    ws_bytes = attention_workspace_size(B, Hq, kv_heads, D, page_size, width, window, kind) if B > 0 else 0
+    ws = (workspace or _default_workspace(q.device, "attention")).get(ws_bytes)
+    _check(load_library().w4a16_attention(
+        _ptr(q), q.stride(0), q.stride(1), B, Hq, _ptr(cache), nbytes, pages, kv_heads, D, page_size, kind,
+        _DTYPE_CODE[q.dtype], _ptr(table), width, _ld(table), _ptr(lengths), window,
+        D ** -0.5 if scale is None else scale, _ptr(out), out.stride(0), out.stride(1),
+        _ptr(ws) if ws_bytes else None, ws.numel() if (ws is not None and ws_bytes) else 0, _stream(q)))
     return out

@@ -26,7 +26,8 @@ LIB = os.path.join(PKG, "libw4a16.so")
 # benchmark only (the HBM read ceiling of one launch); not part of the path.
 CEILING_SRC = "ceiling.hip"
 CEILING_LIB = os.path.join(PKG, "libw4a16_ceiling.so")
-SOURCES = ["w4a16_api.cpp", "repack.hip", "skinny.hip", "mfma.hip", "dense.hip", "w4a8.hip", "scratch.hip"]
+SOURCES = ["w4a16_api.cpp", "repack.hip", "skinny.hip", "mfma.hip", "dense.hip", "w4a8.hip", "scratch.hip",
+           "row_ops.hip", "kv_cache.hip", "attention.hip"]
 STAGED = ["mfma.hip", "w4a8.hip"]  # kernels with hand-counted waits (wait_check)
 ASSEMBLED = STAGED + ["skinny.hip"]  # every source with MFMA kernels (operand hazard check)
 

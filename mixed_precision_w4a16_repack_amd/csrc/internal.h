@@ -143,4 +143,59 @@ int dense_gemm(const void* A, int64_t M, int64_t lda, const void* W, int64_t N, 
                const void* bias, void* C, int64_t ldc, void* workspace, size_t workspace_bytes, hipStream_t stream,
                const char** what);
 
+// ---- operators around the GEMMs: row_ops.hip, kv_cache.hip, attention.hip.
+// Strides are in elements; optional tensors are nullptr.
+struct NormArgs {
+    const uint16_t* x = nullptr;
+    const uint16_t* weight = nullptr;
+    const uint16_t* residual = nullptr;  // optional
+    uint16_t* residual_out = nullptr;    // optional
+    uint16_t* y = nullptr;               // 16-bit output, or ...
+    int8_t* q = nullptr;                 // ... codes and scales
+    float* xs = nullptr;
+    int64_t M = 0, K = 0, ldx = 0, ldr = 0, ldro = 0, ldy = 0, ldq = 0;
+    float eps = 0.0f;
+};
+hipError_t launch_norm(const NormArgs& a, int dtype, hipStream_t stream);
+
+struct GateArgs {
+    const uint16_t* x = nullptr;  // [M, 2K], the gate's columns first
+    uint16_t* y = nullptr;        // 16-bit output, or ...
+    int8_t* q = nullptr;          // ... codes and scales
+    float* xs = nullptr;
+    int64_t M = 0, K = 0, ldx = 0, ldy = 0, ldq = 0;
+};
+int64_t gate_workgroups(int64_t M, int64_t K, bool out8);  // of launch_gate
+hipError_t launch_gate(const GateArgs& a, int dtype, hipStream_t stream);
+
+struct KvArgs {
+    const uint16_t* k = nullptr;  // rows to write ...
+    const uint16_t* v = nullptr;
+    uint16_t* k_out = nullptr;    // ... or read
+    uint16_t* v_out = nullptr;
+    int64_t T = 0, k_ts = 0, k_hs = 0, v_ts = 0, v_hs = 0;  // tokens; token and head strides
+    const int64_t* slots = nullptr;
+    unsigned char* cache = nullptr;
+    int64_t pages = 0;
+    int H = 0, D = 0, P = 0;  // kv heads, head size, tokens per page
+};
+int64_t kv_workgroups(int64_t T, int64_t H);  // of launch_kv_write and launch_kv_read
+hipError_t launch_kv_write(const KvArgs& a, int kind, int dtype, hipStream_t stream);
+hipError_t launch_kv_read(const KvArgs& a, int kind, int dtype, hipStream_t stream);
+
+struct AttentionArgs {
+    const uint16_t* q = nullptr;
+    uint16_t* out = nullptr;
+    int64_t B = 0, q_ts = 0, q_hs = 0, o_ts = 0, o_hs = 0;  // sequences; sequence and head strides
+    const unsigned char* cache = nullptr;
+    int64_t pages = 0;
+    const int32_t* table = nullptr;  // [B, width], rows table_ld apart
+    int64_t width = 0, table_ld = 0;
+    const int32_t* lengths = nullptr;
+    int64_t window = 0;
+    int Hq = 0, H = 0, D = 0, P = 0;
+    float scale = 0.0f;
+};
+hipError_t launch_attention(const AttentionArgs& a, int kind, int dtype, hipStream_t stream);
+
 }  // namespace w4a16

@@ -1,0 +1,333 @@
+// row_ops.hip -- the element-wise work between a decoder layer's GEMMs, one
+// pass over each row:
+//   norm:  h = x (+ residual),  y = h * rsqrt(mean(h^2) + eps) * weight
+//   gate:  y = silu(g) * u = g / (1 + exp(-g)) * u  of a row [g | u]
+// each with y in the activation dtype, or as int8 codes with one fp32 scale
+// per row: the input of the W4A8 GEMM, which a separate quantiser would have
+// to read back. Statistics, products and the scale are fp32; y is rounded
+// once (to 16 bits, or to a code).
+//
+// Rows need no alignment beyond their element's: 16-byte accesses are made
+// on any 2-byte address (global memory takes them), and the up to 7 elements
+// of a row's end are moved one by one.
+#include "device_common.h"
+#include "internal.h"
+
+namespace w4a16 {
+namespace {
+
+typedef u32x4 u32x4_any __attribute__((aligned(2)));
+
+// Eight elements of a row from c (n of them inside the row, 1 .. 8; the rest 0).
+__device__ __forceinline__ u32x4 load8(const uint16_t* p, int64_t n) {
+    if (n >= 8) return *reinterpret_cast<const u32x4_any*>(p);
+    u32x4 v{0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int e = 0; e < 7; ++e)
+        if (e < n) v[e >> 1] |= (uint32_t)p[e] << (16 * (e & 1));
+    return v;
+}
+
+__device__ __forceinline__ void store8(uint16_t* p, int64_t n, const u32x4& v) {
+    if (n >= 8) {
+        *reinterpret_cast<u32x4_any*>(p) = v;
+        return;
+    }
+#pragma unroll
+    for (int e = 0; e < 7; ++e)
+        if (e < n) p[e] = (uint16_t)(v[e >> 1] >> (16 * (e & 1)));
+}
+
+template <int DT>
+__device__ __forceinline__ float elem(const u32x4& v, int e) {
+    return act_to_float<DT>((uint16_t)(v[e >> 1] >> (16 * (e & 1))));
+}
+
+template <int DT>
+__device__ __forceinline__ u32x4 pack8(const float* y) {
+    u32x4 v;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = (uint32_t)to_act_bits<DT>(y[2 * e]) | (uint32_t)to_act_bits<DT>(y[2 * e + 1]) << 16;
+    return v;
+}
+
+// |y| as its bit pattern: ordered as unsigned integers with NaN above
+// infinity, so a maximum over it keeps a NaN instead of dropping it.
+__device__ __forceinline__ uint32_t abs_bits(float y) { return __builtin_bit_cast(uint32_t, y) & 0x7FFFFFFFu; }
+
+// The codes of a row whose largest magnitude is amax: rint(y * (127 / amax)),
+// within [-127, 127] because amax * fp32(127 / amax) rounds to 127 at most.
+// `pre` lifts rows below 1e-30, whose quotient would overflow; a row of zeros
+// has factor 0.
+struct CodeScale {
+    float pre, inv;
+    __device__ __forceinline__ explicit CodeScale(float amax) {
+        pre = amax < 1e-30f ? 0x1p100f : 1.0f;
+        inv = amax > 0.0f ? 127.0f / (amax * pre) : 0.0f;
+    }
+    __device__ __forceinline__ int code(float y) const { return (int)__builtin_rintf(y * pre * inv); }
+};
+
+// Eight codes in the stored order 0,4,1,5,2,6,3,7 (the packed weight's).
+__device__ __forceinline__ uint2 codes8(const float* y, const CodeScale& s) {
+    uint32_t out[2] = {0u, 0u};
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const int pos = e < 4 ? 2 * e : 2 * e - 7;
+        out[pos >> 2] |= ((uint32_t)s.code(y[e]) & 0xFFu) << (8 * (pos & 3));
+    }
+    return make_uint2(out[0], out[1]);
+}
+
+// Sum and maximum over the TPR threads of a row (TPR 64: one wave, no LDS).
+template <int TPR>
+__device__ __forceinline__ void row_reduce(float& sum, uint32_t& amax) {
+#pragma unroll
+    for (int off = 32; off >= 1; off >>= 1) {
+        sum += __shfl_xor(sum, off);
+        const uint32_t o = __shfl_xor(amax, off);
+        amax = o > amax ? o : amax;
+    }
+    if constexpr (TPR > 64) {
+        constexpr int W = TPR / 64;
+        __shared__ float s_sum[W];
+        __shared__ uint32_t s_max[W];
+        if ((threadIdx.x & 63) == 0) {
+            s_sum[threadIdx.x >> 6] = sum;
+            s_max[threadIdx.x >> 6] = amax;
+        }
+        __syncthreads();
+        sum = 0.0f;
+        amax = 0u;
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+            sum += s_sum[w];
+            amax = s_max[w] > amax ? s_max[w] : amax;
+        }
+    }
+}
+
+// One row on TPR threads. CPT > 0: the row (K <= 8 * TPR * CPT) stays in
+// registers between the reduction and the output, so memory is read once.
+// CPT == 0: any K, the row is read twice (residual_out is written in the
+// second pass only: it may be the residual or x itself).
+template <int DT, int TPR, int CPT, bool OUT8>
+__global__ __launch_bounds__(256) void norm_kernel(NormArgs a) {
+    const int64_t m = (int64_t)blockIdx.x * (256 / TPR) + threadIdx.x / TPR;
+    if (TPR == 64 && m >= a.M) return;  // TPR 64 has no barrier
+    const int t = threadIdx.x % TPR;
+    const uint16_t* x = a.x + m * a.ldx;
+    const uint16_t* r = a.residual + m * a.ldr;
+    uint16_t* ro = a.residual_out + m * a.ldro;
+    const int64_t chunks = (a.K + 7) / 8;
+    constexpr int R = CPT > 0 ? CPT : 1;
+    float h[R][8];
+    u32x4 w[R];
+    float sum = 0.0f;
+    uint32_t amax = 0u;
+
+    auto load = [&](int64_t c, float* hc, u32x4& wc) {
+        const int64_t n = a.K - 8 * c;
+        const u32x4 vx = load8(x + 8 * c, n);
+        wc = load8(a.weight + 8 * c, n);
+        if (a.residual != nullptr) {
+            const u32x4 vr = load8(r + 8 * c, n);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) hc[e] = elem<DT>(vx, e) + elem<DT>(vr, e);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) hc[e] = elem<DT>(vx, e);
+        }
+    };
+    auto reduce = [&](float* hc, const u32x4& wc) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            sum += hc[e] * hc[e];
+            if constexpr (OUT8) {
+                const uint32_t b = abs_bits(hc[e] * elem<DT>(wc, e));
+                amax = b > amax ? b : amax;
+            }
+        }
+    };
+    auto finish = [&](int64_t c, float* hc, const u32x4& wc, float rs, const CodeScale& cs) {
+        const int64_t n = a.K - 8 * c;
+        if (a.residual_out != nullptr) store8(ro + 8 * c, n, pack8<DT>(hc));
+        float y[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] = (OUT8 ? hc[e] : hc[e] * rs) * elem<DT>(wc, e);
+        if constexpr (OUT8) {
+            *reinterpret_cast<uint2*>(a.q + m * a.ldq + 8 * c) = codes8(y, cs);
+        } else {
+            store8(a.y + m * a.ldy + 8 * c, n, pack8<DT>(y));
+        }
+    };
+
+    if constexpr (CPT > 0) {
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            const int64_t c = t + (int64_t)TPR * i;
+            if (c < chunks) {
+                load(c, h[i], w[i]);
+            } else {
+                w[i] = u32x4{0u, 0u, 0u, 0u};
+#pragma unroll
+                for (int e = 0; e < 8; ++e) h[i][e] = 0.0f;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < R; ++i) reduce(h[i], w[i]);
+    } else {
+        for (int64_t c = t; c < chunks; c += TPR) {
+            load(c, h[0], w[0]);
+            reduce(h[0], w[0]);
+        }
+    }
+    row_reduce<TPR>(sum, amax);
+    const float rs = 1.0f / sqrtf(sum / (float)a.K + a.eps);
+    // The codes do not depend on rs: it scales the row and its maximum alike.
+    const float top = __builtin_bit_cast(float, amax);
+    const CodeScale cs(top);
+    if (OUT8 && t == 0) a.xs[m] = top * rs / 127.0f;
+    if constexpr (CPT > 0) {
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            const int64_t c = t + (int64_t)TPR * i;
+            if (c < chunks) finish(c, h[i], w[i], rs, cs);
+        }
+    } else {
+        for (int64_t c = t; c < chunks; c += TPR) {
+            load(c, h[0], w[0]);
+            finish(c, h[0], w[0], rs, cs);
+        }
+    }
+}
+
+template <int DT>
+__device__ __forceinline__ void gate8(const u32x4& g, const u32x4& u, float* y) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const float gf = elem<DT>(g, e);
+        y[e] = gf * __builtin_amdgcn_rcpf(1.0f + __expf(-gf)) * elem<DT>(u, e);
+    }
+}
+
+// 16-bit output: chunks of 8 columns, 256 per workgroup.
+template <int DT>
+__global__ __launch_bounds__(256) void gate_kernel(GateArgs a, int64_t blocks_per_row) {
+    const int64_t m = blockIdx.x / blocks_per_row;
+    const int64_t c = (blockIdx.x % blocks_per_row) * 256 + threadIdx.x;
+    const int64_t n = a.K - 8 * c;
+    if (n <= 0) return;
+    const uint16_t* x = a.x + m * a.ldx + 8 * c;
+    const u32x4 g = load8(x, n), u = load8(x + a.K, n);
+    float y[8];
+    gate8<DT>(g, u, y);
+    store8(a.y + m * a.ldy + 8 * c, n, pack8<DT>(y));
+}
+
+// Codes: one row on TPR threads, held in registers (CPT > 0) or computed
+// twice (CPT == 0, any K).
+template <int DT, int TPR, int CPT>
+__global__ __launch_bounds__(256) void gate8_kernel(GateArgs a) {
+    const int64_t m = (int64_t)blockIdx.x * (256 / TPR) + threadIdx.x / TPR;
+    if (TPR == 64 && m >= a.M) return;
+    const int t = threadIdx.x % TPR;
+    const uint16_t* x = a.x + m * a.ldx;
+    const int64_t chunks = a.K / 8;
+    constexpr int R = CPT > 0 ? CPT : 1;
+    float y[R][8];
+    float unused = 0.0f;
+    uint32_t amax = 0u;
+    auto load = [&](int64_t c, float* yc) { gate8<DT>(load8(x + 8 * c, 8), load8(x + a.K + 8 * c, 8), yc); };
+    auto reduce = [&](const float* yc) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) amax = abs_bits(yc[e]) > amax ? abs_bits(yc[e]) : amax;
+    };
+    if constexpr (CPT > 0) {
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            const int64_t c = t + (int64_t)TPR * i;
+            if (c < chunks) {
+                load(c, y[i]);
+                reduce(y[i]);
+            }
+        }
+    } else {
+        for (int64_t c = t; c < chunks; c += TPR) {
+            load(c, y[0]);
+            reduce(y[0]);
+        }
+    }
+    row_reduce<TPR>(unused, amax);
+    const float top = __builtin_bit_cast(float, amax);
+    const CodeScale cs(top);
+    if (t == 0) a.xs[m] = top / 127.0f;
+    if constexpr (CPT > 0) {
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            const int64_t c = t + (int64_t)TPR * i;
+            if (c < chunks) *reinterpret_cast<uint2*>(a.q + m * a.ldq + 8 * c) = codes8(y[i], cs);
+        }
+    } else {
+        for (int64_t c = t; c < chunks; c += TPR) {
+            load(c, y[0]);
+            *reinterpret_cast<uint2*>(a.q + m * a.ldq + 8 * c) = codes8(y[0], cs);
+        }
+    }
+}
+
+// Calls f with the threads per row and register chunks per thread of a width.
+template <class F>
+void by_width(int64_t K, F&& f) {
+    using std::integral_constant;
+    const int64_t c = (K + 7) / 8;
+    if (c <= 64) f(integral_constant<int, 64>{}, integral_constant<int, 1>{});
+    else if (c <= 128) f(integral_constant<int, 64>{}, integral_constant<int, 2>{});
+    else if (c <= 256) f(integral_constant<int, 256>{}, integral_constant<int, 1>{});
+    else if (c <= 512) f(integral_constant<int, 256>{}, integral_constant<int, 2>{});
+    else if (c <= 1024) f(integral_constant<int, 256>{}, integral_constant<int, 4>{});
+    else if (c <= 2048) f(integral_constant<int, 256>{}, integral_constant<int, 8>{});
+    else f(integral_constant<int, 256>{}, integral_constant<int, 0>{});
+}
+
+template <int DT>
+void norm_dispatch(const NormArgs& a, hipStream_t stream) {
+    by_width(a.K, [&](auto tpr, auto cpt) {
+        const dim3 grid((unsigned)((a.M * decltype(tpr)::value + 255) / 256));
+        if (a.q != nullptr)
+            hipLaunchKernelGGL((norm_kernel<DT, decltype(tpr)::value, decltype(cpt)::value, true>), grid, dim3(256), 0, stream, a);
+        else
+            hipLaunchKernelGGL((norm_kernel<DT, decltype(tpr)::value, decltype(cpt)::value, false>), grid, dim3(256), 0, stream, a);
+    });
+}
+
+template <int DT>
+void gate_dispatch(const GateArgs& a, hipStream_t stream) {
+    if (a.q == nullptr) {
+        const int64_t bpr = (a.K + 2047) / 2048;
+        hipLaunchKernelGGL((gate_kernel<DT>), dim3((unsigned)(a.M * bpr)), dim3(256), 0, stream, a, bpr);
+        return;
+    }
+    by_width(a.K, [&](auto tpr, auto cpt) {
+        const dim3 grid((unsigned)((a.M * decltype(tpr)::value + 255) / 256));
+        hipLaunchKernelGGL((gate8_kernel<DT, decltype(tpr)::value, decltype(cpt)::value>), grid, dim3(256), 0, stream, a);
+    });
+}
+
+}  // namespace
+
+int64_t gate_workgroups(int64_t M, int64_t K, bool out8) { return out8 ? M : M * ((K + 2047) / 2048); }
+
+hipError_t launch_norm(const NormArgs& a, int dtype, hipStream_t stream) {
+    if (dtype == 0) norm_dispatch<0>(a, stream);
+    else norm_dispatch<1>(a, stream);
+    return hipGetLastError();
+}
+
+hipError_t launch_gate(const GateArgs& a, int dtype, hipStream_t stream) {
+    if (dtype == 0) gate_dispatch<0>(a, stream);
+    else gate_dispatch<1>(a, stream);
+    return hipGetLastError();
+}
+
+}  // namespace w4a16

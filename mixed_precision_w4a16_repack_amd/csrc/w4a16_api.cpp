@@ -477,3 +477,297 @@ w4a16_status w4a16_gemm_dense(const void* A, int64_t M, int64_t lda, const void*
 }
 
 }  // extern "C"
+
+namespace w4a16 {
+namespace {
+
+// Workgroups of one launch are counted in 32 bits.
+constexpr int64_t kMaxWorkgroups = ((int64_t)1 << 31) - 1;
+
+bool aligned_to(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+w4a16_status check_dtype(int32_t dtype) {
+    if (dtype != W4A16_F16 && dtype != W4A16_BF16)
+        return fail(W4A16_ERR_INVALID_ARG, "dtype=%d is not a w4a16_dtype (0 fp16, 1 bf16)", dtype);
+    return W4A16_OK;
+}
+
+w4a16_status check_row_stride(const char* name, int64_t ld, const char* width, int64_t least) {
+    if (ld < least) return fail(W4A16_ERR_INVALID_ARG, "%s=%lld must be >= %s=%lld", name, (long long)ld, width, (long long)least);
+    return check_stride(name, ld);
+}
+
+// M rows of K elements for a kernel of at most one workgroup per row (norm)
+// or per 2048 columns (gate).
+w4a16_status check_rows(int64_t M, int64_t K, int32_t dtype, bool out8) {
+    if (M < 0) return fail(W4A16_ERR_INVALID_ARG, "M=%lld must be >= 0", (long long)M);
+    if (K <= 0) return fail(W4A16_ERR_INVALID_ARG, "K=%lld must be positive", (long long)K);
+    w4a16_status st = check_dtype(dtype);
+    if (st != W4A16_OK) return st;
+    if (K > kMaxDim) return fail(W4A16_ERR_UNSUPPORTED, "K=%lld must be at most 2^32", (long long)K);
+    if (out8 && K % 8 != 0) return fail(W4A16_ERR_UNSUPPORTED, "K=%lld must be divisible by 8", (long long)K);
+    if (M > kMaxWorkgroups) return fail(W4A16_ERR_UNSUPPORTED, "M=%lld is too large for one launch", (long long)M);
+    return W4A16_OK;
+}
+
+w4a16_status check_codes(const int8_t* qa, int64_t ldq, const float* xs) {
+    if (!aligned_to(qa, 8) || ldq % 8 != 0)
+        return fail(W4A16_ERR_UNSUPPORTED, "qa must be 8-byte aligned with ldq %% 8 == 0 (ldq=%lld)", (long long)ldq);
+    if (!aligned_to(xs, 4)) return fail(W4A16_ERR_INVALID_ARG, "xs must be 4-byte aligned");
+    return W4A16_OK;
+}
+
+w4a16_status norm_impl(const void* x, int64_t M, int64_t K, int64_t ldx, int32_t dtype, const void* weight, float eps,
+                       const void* residual, int64_t ldr, void* residual_out, int64_t ldro, void* y, int64_t ldy,
+                       int8_t* qa, int64_t ldq, float* xs, bool out8, hipStream_t stream) {
+    w4a16_status st = check_rows(M, K, dtype, out8);
+    if (st != W4A16_OK || (st = check_row_stride("ldx", ldx, "K", K)) != W4A16_OK) return st;
+    if (out8 ? (st = check_row_stride("ldq", ldq, "K", K)) != W4A16_OK : (st = check_row_stride("ldy", ldy, "K", K)) != W4A16_OK)
+        return st;
+    if (residual != nullptr && (st = check_row_stride("ldr", ldr, "K", K)) != W4A16_OK) return st;
+    if (residual_out != nullptr && (st = check_row_stride("ldro", ldro, "K", K)) != W4A16_OK) return st;
+    if (!(eps >= 0.0f && eps <= 3.4e38f)) return fail(W4A16_ERR_INVALID_ARG, "eps=%g must be finite and >= 0", (double)eps);
+    if (M == 0) return W4A16_OK;
+    if (x == nullptr || weight == nullptr) return fail(W4A16_ERR_INVALID_ARG, "x and weight must not be NULL");
+    if (out8 ? (qa == nullptr || xs == nullptr) : y == nullptr)
+        return fail(W4A16_ERR_INVALID_ARG, out8 ? "qa and xs must not be NULL" : "y must not be NULL");
+    if (!aligned_to(x, 2) || !aligned_to(weight, 2) || !aligned_to(residual, 2) || !aligned_to(residual_out, 2) ||
+        !aligned_to(y, 2))
+        return fail(W4A16_ERR_INVALID_ARG, "x, weight, residual, residual_out and y must be 2-byte aligned");
+    if (out8 && (st = check_codes(qa, ldq, xs)) != W4A16_OK) return st;
+    NormArgs a;
+    a.x = static_cast<const uint16_t*>(x);
+    a.weight = static_cast<const uint16_t*>(weight);
+    a.residual = static_cast<const uint16_t*>(residual);
+    a.residual_out = static_cast<uint16_t*>(residual_out);
+    a.y = static_cast<uint16_t*>(y);
+    a.q = out8 ? qa : nullptr;
+    a.xs = xs;
+    a.M = M, a.K = K, a.ldx = ldx, a.ldr = ldr, a.ldro = ldro, a.ldy = ldy, a.ldq = ldq;
+    a.eps = eps;
+    hipError_t e = launch_norm(a, dtype, stream);
+    if (e != hipSuccess) return hip_fail("rmsnorm kernel launch", e);
+    return W4A16_OK;
+}
+
+w4a16_status gate_impl(const void* x, int64_t M, int64_t K, int64_t ldx, int32_t dtype, void* y, int64_t ldy,
+                       int8_t* qa, int64_t ldq, float* xs, bool out8, hipStream_t stream) {
+    w4a16_status st = check_rows(M, K, dtype, out8);
+    if (st != W4A16_OK || (st = check_row_stride("ldx", ldx, "2*K", 2 * K)) != W4A16_OK) return st;
+    if (out8 ? (st = check_row_stride("ldq", ldq, "K", K)) != W4A16_OK : (st = check_row_stride("ldy", ldy, "K", K)) != W4A16_OK)
+        return st;
+    if (M == 0) return W4A16_OK;
+    if (gate_workgroups(M, K, out8) > kMaxWorkgroups)
+        return fail(W4A16_ERR_UNSUPPORTED, "M=%lld rows of K=%lld are too large for one launch", (long long)M, (long long)K);
+    if (x == nullptr) return fail(W4A16_ERR_INVALID_ARG, "x must not be NULL");
+    if (out8 ? (qa == nullptr || xs == nullptr) : y == nullptr)
+        return fail(W4A16_ERR_INVALID_ARG, out8 ? "qa and xs must not be NULL" : "y must not be NULL");
+    if (!aligned_to(x, 2) || !aligned_to(y, 2)) return fail(W4A16_ERR_INVALID_ARG, "x and y must be 2-byte aligned");
+    if (out8 && (st = check_codes(qa, ldq, xs)) != W4A16_OK) return st;
+    GateArgs a;
+    a.x = static_cast<const uint16_t*>(x);
+    a.y = static_cast<uint16_t*>(y);
+    a.q = out8 ? qa : nullptr;
+    a.xs = xs;
+    a.M = M, a.K = K, a.ldx = ldx, a.ldy = ldy, a.ldq = ldq;
+    hipError_t e = launch_gate(a, dtype, stream);
+    if (e != hipSuccess) return hip_fail("silu_mul kernel launch", e);
+    return W4A16_OK;
+}
+
+// Geometry rules of a paged cache; *bytes is its size.
+w4a16_status check_cache(int64_t pages, int32_t kv_heads, int32_t head_dim, int32_t page_size, int32_t kind, size_t* bytes) {
+    if (kind != W4A16_KV_ACT && kind != W4A16_KV_INT8)
+        return fail(W4A16_ERR_INVALID_ARG, "kind=%d is not a w4a16_kv_kind (0 act dtype, 1 int8)", kind);
+    if (pages < 0) return fail(W4A16_ERR_INVALID_ARG, "pages=%lld must be >= 0", (long long)pages);
+    if (kv_heads <= 0) return fail(W4A16_ERR_INVALID_ARG, "kv_heads=%d must be positive", kv_heads);
+    if (head_dim != 64 && head_dim != 128 && head_dim != 192 && head_dim != 256)
+        return fail(W4A16_ERR_UNSUPPORTED, "head_dim=%d not supported; supported: 64, 128, 192, 256", head_dim);
+    if (page_size <= 0 || page_size % 32 != 0)
+        return fail(W4A16_ERR_UNSUPPORTED, "page_size=%d must be a positive multiple of 32", page_size);
+    // Together these keep a cache below 2^62 bytes, and a record's offsets in 31 bits.
+    if (page_size > (1 << 16) || kv_heads > (1 << 16) || pages > ((int64_t)1 << 31) - 1)
+        return fail(W4A16_ERR_UNSUPPORTED, "page_size and kv_heads must be at most 2^16, pages below 2^31");
+    const int64_t values = (int64_t)page_size * head_dim;
+    const int64_t record = kind == W4A16_KV_ACT ? 4 * values : 2 * values + 8 * (int64_t)page_size;
+    if (__builtin_mul_overflow(record * kv_heads, pages, reinterpret_cast<int64_t*>(bytes)) || (int64_t)*bytes > ((int64_t)1 << 50))
+        return fail(W4A16_ERR_UNSUPPORTED, "a cache must be at most 2^50 bytes");
+    return W4A16_OK;
+}
+
+w4a16_status check_cache_buffer(const void* cache, size_t cache_bytes, size_t need) {
+    if (need > 0 && cache == nullptr) return fail(W4A16_ERR_INVALID_ARG, "cache must not be NULL");
+    if (!aligned16(cache)) return fail(W4A16_ERR_INVALID_ARG, "cache must be 16-byte aligned");
+    if (cache_bytes < need)
+        return fail(W4A16_ERR_SIZE, "cache_bytes=%zu is smaller than the %zu bytes of the cache", cache_bytes, need);
+    return W4A16_OK;
+}
+
+// Strides of a [rows, heads, head_dim] tensor: any in [0, 2^40], negative ones excluded.
+w4a16_status check_head_strides(const char* name, int64_t rs, int64_t hs) {
+    if (rs < 0 || hs < 0) return fail(W4A16_ERR_INVALID_ARG, "%s strides must be >= 0", name);
+    if (rs > kMaxStride || hs > kMaxStride)
+        return fail(W4A16_ERR_UNSUPPORTED, "%s strides must be at most 2^40 elements", name);
+    return W4A16_OK;
+}
+
+w4a16_status kv_impl(bool write, const void* k, int64_t k_ts, int64_t k_hs, const void* v, int64_t v_ts, int64_t v_hs,
+                     int64_t T, const int64_t* slots, const void* cache, size_t cache_bytes, int64_t pages,
+                     int32_t kv_heads, int32_t head_dim, int32_t page_size, int32_t kind, int32_t dtype,
+                     hipStream_t stream) {
+    size_t need = 0;
+    w4a16_status st = check_cache(pages, kv_heads, head_dim, page_size, kind, &need);
+    if (st != W4A16_OK || (st = check_dtype(dtype)) != W4A16_OK) return st;
+    if (T < 0) return fail(W4A16_ERR_INVALID_ARG, "T=%lld must be >= 0", (long long)T);
+    if ((st = check_head_strides("k", k_ts, k_hs)) != W4A16_OK || (st = check_head_strides("v", v_ts, v_hs)) != W4A16_OK)
+        return st;
+    if (T == 0) return W4A16_OK;
+    if (T > kMaxDim || kv_workgroups(T, kv_heads) > kMaxWorkgroups)
+        return fail(W4A16_ERR_UNSUPPORTED, "T=%lld is too large for one launch", (long long)T);
+    if (k == nullptr || v == nullptr || slots == nullptr)
+        return fail(W4A16_ERR_INVALID_ARG, "k, v and slots must not be NULL");
+    if (!aligned_to(k, 2) || !aligned_to(v, 2)) return fail(W4A16_ERR_INVALID_ARG, "k and v must be 2-byte aligned");
+    if (!aligned_to(slots, 8)) return fail(W4A16_ERR_INVALID_ARG, "slots must be 8-byte aligned");
+    if ((st = check_cache_buffer(cache, cache_bytes, need)) != W4A16_OK) return st;
+    KvArgs a;
+    a.k = static_cast<const uint16_t*>(k);
+    a.v = static_cast<const uint16_t*>(v);
+    if (!write) {
+        a.k_out = const_cast<uint16_t*>(a.k);
+        a.v_out = const_cast<uint16_t*>(a.v);
+    }
+    a.T = T, a.k_ts = k_ts, a.k_hs = k_hs, a.v_ts = v_ts, a.v_hs = v_hs;
+    a.slots = slots;
+    a.cache = static_cast<unsigned char*>(const_cast<void*>(cache));
+    a.pages = pages, a.H = kv_heads, a.D = head_dim, a.P = page_size;
+    hipError_t e = write ? launch_kv_write(a, kind, dtype, stream) : launch_kv_read(a, kind, dtype, stream);
+    if (e != hipSuccess) return hip_fail(write ? "kv_write kernel launch" : "kv_read kernel launch", e);
+    return W4A16_OK;
+}
+
+// Shape rules of the attention calls.
+w4a16_status check_attention(int64_t B, int32_t q_heads, int32_t kv_heads, int32_t page_size, int64_t table_width, int64_t window) {
+    if (B < 0) return fail(W4A16_ERR_INVALID_ARG, "B=%lld must be >= 0", (long long)B);
+    if (q_heads <= 0 || q_heads % kv_heads != 0)
+        return fail(W4A16_ERR_INVALID_ARG, "q_heads=%d must be a positive multiple of kv_heads=%d", q_heads, kv_heads);
+    if (table_width < 0) return fail(W4A16_ERR_INVALID_ARG, "table_width=%lld must be >= 0", (long long)table_width);
+    if (window < 0) return fail(W4A16_ERR_INVALID_ARG, "window=%lld must be >= 0", (long long)window);
+    if (q_heads > (1 << 20) || B > (int64_t)1 << 31 || B * q_heads > kMaxWorkgroups)
+        return fail(W4A16_ERR_UNSUPPORTED, "B=%lld sequences of q_heads=%d are too large for one launch", (long long)B, q_heads);
+    if (table_width > (((int64_t)1 << 31) + page_size - 1) / page_size)
+        return fail(W4A16_ERR_UNSUPPORTED, "table_width=%lld pages hold more than 2^31 tokens", (long long)table_width);
+    return W4A16_OK;
+}
+
+}  // namespace
+}  // namespace w4a16
+
+extern "C" {
+
+w4a16_status w4a16_rmsnorm(const void* x, int64_t M, int64_t K, int64_t ldx, int32_t dtype, const void* weight,
+                           float eps, const void* residual, int64_t ldr, void* residual_out, int64_t ldro, void* y,
+                           int64_t ldy, hipStream_t stream) {
+    clear_error();
+    return norm_impl(x, M, K, ldx, dtype, weight, eps, residual, ldr, residual_out, ldro, y, ldy, nullptr, 0, nullptr,
+                     false, stream);
+}
+
+w4a16_status w4a8_rmsnorm(const void* x, int64_t M, int64_t K, int64_t ldx, int32_t dtype, const void* weight,
+                          float eps, const void* residual, int64_t ldr, void* residual_out, int64_t ldro, int8_t* qa,
+                          int64_t ldq, float* xs, hipStream_t stream) {
+    clear_error();
+    return norm_impl(x, M, K, ldx, dtype, weight, eps, residual, ldr, residual_out, ldro, nullptr, 0, qa, ldq, xs, true,
+                     stream);
+}
+
+w4a16_status w4a16_silu_mul(const void* x, int64_t M, int64_t K, int64_t ldx, int32_t dtype, void* y, int64_t ldy,
+                            hipStream_t stream) {
+    clear_error();
+    return gate_impl(x, M, K, ldx, dtype, y, ldy, nullptr, 0, nullptr, false, stream);
+}
+
+w4a16_status w4a8_silu_mul(const void* x, int64_t M, int64_t K, int64_t ldx, int32_t dtype, int8_t* qa, int64_t ldq,
+                           float* xs, hipStream_t stream) {
+    clear_error();
+    return gate_impl(x, M, K, ldx, dtype, nullptr, 0, qa, ldq, xs, true, stream);
+}
+
+w4a16_status w4a16_kv_cache_size(int64_t pages, int32_t kv_heads, int32_t head_dim, int32_t page_size, int32_t kind,
+                                 size_t* out_bytes) {
+    clear_error();
+    if (out_bytes == nullptr) return fail(W4A16_ERR_INVALID_ARG, "out_bytes is NULL");
+    size_t need = 0;
+    w4a16_status st = check_cache(pages, kv_heads, head_dim, page_size, kind, &need);
+    if (st == W4A16_OK) *out_bytes = need;
+    return st;
+}
+
+w4a16_status w4a16_kv_write(const void* k, int64_t k_ts, int64_t k_hs, const void* v, int64_t v_ts, int64_t v_hs,
+                            int64_t T, const int64_t* slots, void* cache, size_t cache_bytes, int64_t pages,
+                            int32_t kv_heads, int32_t head_dim, int32_t page_size, int32_t kind, int32_t dtype,
+                            hipStream_t stream) {
+    clear_error();
+    return kv_impl(true, k, k_ts, k_hs, v, v_ts, v_hs, T, slots, cache, cache_bytes, pages, kv_heads, head_dim,
+                   page_size, kind, dtype, stream);
+}
+
+w4a16_status w4a16_kv_read(const int64_t* slots, int64_t T, const void* cache, size_t cache_bytes, int64_t pages,
+                           int32_t kv_heads, int32_t head_dim, int32_t page_size, int32_t kind, int32_t dtype, void* k,
+                           int64_t k_ts, int64_t k_hs, void* v, int64_t v_ts, int64_t v_hs, hipStream_t stream) {
+    clear_error();
+    return kv_impl(false, k, k_ts, k_hs, v, v_ts, v_hs, T, slots, cache, cache_bytes, pages, kv_heads, head_dim,
+                   page_size, kind, dtype, stream);
+}
+
+w4a16_status w4a16_attention_workspace_size(int64_t B, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
+                                            int32_t page_size, int64_t table_width, int64_t window, int32_t kind,
+                                            size_t* out_bytes) {
+    clear_error();
+    if (out_bytes == nullptr) return fail(W4A16_ERR_INVALID_ARG, "out_bytes is NULL");
+    size_t unused = 0;
+    w4a16_status st = check_cache(0, kv_heads, head_dim, page_size, kind, &unused);
+    if (st != W4A16_OK || (st = check_attention(B, q_heads, kv_heads, page_size, table_width, window)) != W4A16_OK) return st;
+    *out_bytes = 0;
+    return W4A16_OK;
+}
+
+w4a16_status w4a16_attention(const void* q, int64_t q_bs, int64_t q_hs, int64_t B, int32_t q_heads, const void* cache,
+                             size_t cache_bytes, int64_t pages, int32_t kv_heads, int32_t head_dim, int32_t page_size,
+                             int32_t kind, int32_t dtype, const int32_t* table, int64_t table_width, int64_t table_ld,
+                             const int32_t* lengths, int64_t window, float scale, void* out, int64_t o_bs, int64_t o_hs,
+                             void* workspace, size_t workspace_bytes, hipStream_t stream) {
+    clear_error();
+    size_t need = 0;
+    w4a16_status st = check_cache(pages, kv_heads, head_dim, page_size, kind, &need);
+    if (st != W4A16_OK || (st = check_dtype(dtype)) != W4A16_OK ||
+        (st = check_attention(B, q_heads, kv_heads, page_size, table_width, window)) != W4A16_OK ||
+        (st = check_head_strides("q", q_bs, q_hs)) != W4A16_OK || (st = check_head_strides("out", o_bs, o_hs)) != W4A16_OK)
+        return st;
+    if ((st = check_row_stride("table_ld", table_ld, "table_width", table_width)) != W4A16_OK) return st;
+    if (!(scale >= -3.4e38f && scale <= 3.4e38f)) return fail(W4A16_ERR_INVALID_ARG, "scale=%g must be finite", (double)scale);
+    if (B == 0) return W4A16_OK;
+    if (q == nullptr || out == nullptr || lengths == nullptr || (table == nullptr && table_width > 0))
+        return fail(W4A16_ERR_INVALID_ARG, "q, table, lengths and out must not be NULL");
+    if (!aligned_to(q, 2) || !aligned_to(out, 2)) return fail(W4A16_ERR_INVALID_ARG, "q and out must be 2-byte aligned");
+    if (!aligned_to(table, 4) || !aligned_to(lengths, 4))
+        return fail(W4A16_ERR_INVALID_ARG, "table and lengths must be 4-byte aligned");
+    if ((st = check_cache_buffer(cache, cache_bytes, need)) != W4A16_OK) return st;
+    AttentionArgs a;
+    a.q = static_cast<const uint16_t*>(q);
+    a.out = static_cast<uint16_t*>(out);
+    a.B = B, a.q_ts = q_bs, a.q_hs = q_hs, a.o_ts = o_bs, a.o_hs = o_hs;
+    a.cache = static_cast<const unsigned char*>(cache);
+    a.pages = pages;
+    a.table = table;
+    a.width = table_width, a.table_ld = table_ld;
+    a.lengths = lengths;
+    a.window = window;
+    a.Hq = q_heads, a.H = kv_heads, a.D = head_dim, a.P = page_size;
+    a.scale = scale;
+    (void)workspace, (void)workspace_bytes;
+    hipError_t e = launch_attention(a, kind, dtype, stream);
+    if (e != hipSuccess) return hip_fail("attention kernel launch", e);
+    return W4A16_OK;
+}
+
+}  // extern "C"
