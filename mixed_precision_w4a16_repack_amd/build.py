@@ -29,7 +29,7 @@ CEILING_LIB = os.path.join(PKG, "libw4a16_ceiling.so")
 SOURCES = ["w4a16_api.cpp", "repack.hip", "skinny.hip", "mfma.hip", "dense.hip", "w4a8.hip", "scratch.hip",
            "row_ops.hip", "kv_cache.hip", "attention.hip"]
 STAGED = ["mfma.hip", "w4a8.hip"]  # kernels with hand-counted waits (wait_check)
-ASSEMBLED = STAGED + ["skinny.hip"]  # every source with MFMA kernels (operand hazard check)
+ASSEMBLED = STAGED + ["skinny.hip", "attention.hip"]  # every source with MFMA kernels (operand hazard check)
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

@@ -1,95 +1,751 @@
 // attention.hip -- attention of one new token per sequence over the paged
 // key/value cache (layout in include/w4a16.h, kv_layout.h):
 //   s_t = scale * q . k_t,  o = sum_t exp(s_t - m) v_t / sum_t exp(s_t - m),
-// over the tokens t a sequence sees, in one pass with a running maximum m.
+// over the tokens t a sequence sees, in one pass with a running reference m.
+//
+// Tiles of 32 tokens. A cache tile is an MFMA operand as it is stored, so
+// nothing is shuffled: S^T = K Q^T (16 tokens x 16 query heads of one kv
+// head), whose result already lies as the B operand of O^T += V^T P^T (the
+// value tiles hold their tokens in that order). Keys, values and results stay
+// in registers; a wave loads a tile's keys while it works on the one before.
+//
+// Scores are in base 2 (scale * log2(e) folded into one factor). The running
+// reference moves only when a score passes it by kHeadroom, which is rare
+// after the first tiles, so a tile usually costs no cross-lane step and no
+// rescaling of O. 16-bit probabilities carry a factor 2^13 in fp16, which
+// keeps them out of the subnormals down to 2^-27 of the largest (and not lost
+// above 2^-38); the sums take the unrounded fp32 ones.
+//
+// int8: codes become exact fp16 values (0x6400 | (code ^ 0x80) is 1152 + code),
+// the key's scale multiplies the score, and the value's scale its probability,
+// w = p * vs. Scales of any size must not leave fp16's range, so w has a
+// reference of its own, c >= log2(w): w is formed as p * vs * f with
+// f = 2^(13 - c + m). A bf16 query is moved by a power of two to the top of
+// fp16's range (its 8 bits are exact there; elements below 2^-29 of the
+// largest lose bits).
+//
+// What bounds it: the cache's bytes. Work is divided by tiles over a fixed
+// number of workgroups, computed on the device from the lengths (the host
+// does not know them): each takes an equal run of the list of all (sequence,
+// kv head, tile), whatever the lengths are. A (sequence, head) that several
+// workgroups share is joined by the last of them to arrive, in order of
+// position, so the result does not depend on the order of arrival.
 #include "device_common.h"
+#include "exchange.h"
 #include "internal.h"
 #include "kv_layout.h"
 
 namespace w4a16 {
 namespace {
 
-constexpr int kMaxD = 256;
+constexpr int kWaves = 4;
+constexpr int kTile = 32;              // tokens
+constexpr int kMinTiles = 16;          // least tiles per workgroup when a head is split
+constexpr int kFan = 16;               // partial results joined by one workgroup ...
+constexpr int kBatch = 8;              // ... with the loads of this many in flight
+constexpr float kLowest = -3.402823466e38f;
 
-// One workgroup per (sequence, query head); a wave takes every fourth token,
-// lanes over d; the four waves' results are joined in LDS.
-template <int DT, int KIND>
-__global__ __launch_bounds__(256) void attention_kernel(AttentionArgs a) {
-    using L = KvPlace<KIND>;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t b = blockIdx.x / a.Hq;
-    const int hq = (int)(blockIdx.x % a.Hq);
-    const int h = hq / (a.Hq / a.H);
-    int64_t n = a.lengths[b];
-    n = n < 0 ? 0 : (n > a.width * a.P ? a.width * a.P : n);
-    const int64_t first = a.window > 0 && n > a.window ? n - a.window : 0;
-    const uint16_t* q = a.q + b * a.q_ts + hq * a.q_hs;
-    float qv[kMaxD / 64], o[kMaxD / 64];
-    for (int i = 0; i < kMaxD / 64; ++i) {
-        qv[i] = 64 * i + lane < a.D ? act_to_float<DT>(q[64 * i + lane]) : 0.0f;
-        o[i] = 0.0f;
+typedef u32x4 u32x4_any __attribute__((aligned(2)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef u32x2 u32x2_any __attribute__((aligned(2)));
+
+// How many workgroups of each kernel share a CU (registers allow that many).
+template <int KIND, int D, int HT>
+constexpr int kPerCU = HT == 2 ? (D > 128 ? 1 : 2) : (KIND == 1 ? (D > 128 ? 2 : 3) : (D > 128 ? 1 : (D == 64 ? 3 : 2)));
+
+// What is left of the references in fp16 (2^13 * 2^2 < 65504).
+template <bool F16P>
+struct Prob {
+    static constexpr float kBias = F16P ? 13.0f : 0.0f;
+    static constexpr float kHeadroom = F16P ? 2.0f : 8.0f;
+};
+
+__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// Maximum, or sum, over the four lane groups of a column (lanes l, l + 16, ...).
+__device__ __forceinline__ float column_max(float v) {
+    v = fmaxf(v, __shfl_xor(v, 16));
+    return fmaxf(v, __shfl_xor(v, 32));
+}
+__device__ __forceinline__ float column_sum(float v) {
+    v += __shfl_xor(v, 16);
+    return v + __shfl_xor(v, 32);
+}
+
+// Four int8 codes (one word) as two words of exact fp16 pairs.
+__device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+    const uint32_t x = w ^ 0x80808080u;
+    const half2_t off{(_Float16)-1152.0f, (_Float16)-1152.0f};
+    const half2_t a = __builtin_bit_cast(half2_t, __builtin_amdgcn_perm(0x64646464u, x, 0x04010400u)) + off;
+    const half2_t b = __builtin_bit_cast(half2_t, __builtin_amdgcn_perm(0x64646464u, x, 0x04030402u)) + off;
+    lo = __builtin_bit_cast(uint32_t, a);
+    hi = __builtin_bit_cast(uint32_t, b);
+}
+__device__ __forceinline__ u32x4 codes8_to_f16(uint32_t w0, uint32_t w1) {
+    uint32_t a, b, c, d;
+    codes_to_f16(w0, a, b);
+    codes_to_f16(w1, c, d);
+    return u32x4{a, b, c, d};
+}
+
+__device__ __forceinline__ int64_t read_lane(int64_t v, int lane) {
+    const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)v, lane);
+    const uint32_t hi = __builtin_amdgcn_readlane((int)(uint32_t)(v >> 32), lane);
+    return (int64_t)((uint64_t)hi << 32 | lo);
+}
+
+__device__ __forceinline__ int64_t wave_scan(int64_t v, int lane) {
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+        const int64_t o = __shfl_up(v, d);
+        if (lane >= d) v += o;
     }
-    float m = -INFINITY, l = 0.0f;
-    for (int64_t tok = first + wave; tok < n; tok += 4) {
-        const int64_t page = a.table[b * a.table_ld + tok / a.P];
-        if (page < 0 || page >= a.pages) continue;
-        const int t = (int)(tok % a.P);
-        const unsigned char* rec = a.cache + (page * a.H + h) * L::record_bytes(a.D, a.P);
-        float s = 0.0f, v[kMaxD / 64];
-        for (int i = 0; i < kMaxD / 64; ++i) {
-            const int d = 64 * i + lane;
-            v[i] = 0.0f;
-            if (d >= a.D) continue;
-            if constexpr (KIND == 0) {
-                s += qv[i] * act_to_float<DT>(*reinterpret_cast<const uint16_t*>(rec + L::key(t, d, a.D)));
-                v[i] = act_to_float<DT>(*reinterpret_cast<const uint16_t*>(rec + L::value(t, d, a.D, a.P)));
-            } else {
-                s += qv[i] * (float)(int8_t)rec[L::key(t, d, a.D)];
-                v[i] = (float)(int8_t)rec[L::value(t, d, a.D, a.P)];
+    return v;
+}
+
+// a / b of non-negative numbers, mostly small.
+__device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {
+    if (((uint64_t)a | (uint64_t)b) >> 32 == 0) return (uint32_t)a / (uint32_t)b;
+    return a / b;
+}
+
+// What a sequence of a length sees: tokens lo .. n - 1, in the tiles
+// [first, first + count).
+struct Span {
+    int n, lo, first, count;
+    __device__ __forceinline__ Span(const AttentionArgs& a, int length) {
+        const int64_t most = a.width * a.P;
+        const int64_t len = length < 0 ? 0 : (length > most ? most : length);
+        n = (int)len;
+        lo = a.window > 0 && len > a.window ? (int)(len - a.window) : 0;
+        first = lo / kTile;
+        count = n > lo ? (n - 1) / kTile + 1 - first : 0;
+    }
+};
+
+template <int DT, int KIND, int D, int HT>
+struct Attend {
+    static constexpr bool kI8 = KIND == 1;
+    static constexpr bool kF16P = kI8 || DT == 0;
+    static constexpr int PDT = kF16P ? 0 : 1;             // operand type of both products
+    static constexpr int NL = D * (kI8 ? 1 : 2) / 32;     // 16-byte loads a lane for a tile's keys (and its values)
+    static constexpr int NQ = D / 32;                     // MFMAs along d
+    static constexpr int NO = D / 16;
+    static constexpr int kCols = 16 * HT;
+    static constexpr int kLd = D + 4;                     // floats between heads in LDS: spreads them over the banks
+    using L = KvPlace<KIND>;
+    using Pr = Prob<kF16P>;
+
+    const AttentionArgs& a;
+    const int lane, wave, g, col;
+    u32x4 q[HT][NQ];
+    float factor[HT];
+    u32x4 kb[NL], vb[NL];
+    floatx4 ks[2], vs[2];
+    floatx4 o[HT][NO];
+    float m[HT], l[HT], c[HT], f[HT];
+
+    __device__ __forceinline__ explicit Attend(const AttentionArgs& args)
+        : a(args), lane(threadIdx.x & 63), wave(__builtin_amdgcn_readfirstlane(threadIdx.x >> 6)), g(lane >> 4), col(lane & 15) {}
+
+    // The queries of sequence b, heads head0 .. head0 + heads - 1 (heads <= kCols) as B operands.
+    __device__ __forceinline__ void load_query(int64_t b, int head0, int heads) {
+#pragma unroll
+        for (int h = 0; h < HT; ++h) {
+            const bool in = 16 * h + col < heads;
+            const uint16_t* p = a.q + b * a.q_ts + (int64_t)(head0 + 16 * h + col) * a.q_hs + 8 * g;
+#pragma unroll
+            for (int i = 0; i < NQ; ++i) {
+                q[h][i] = u32x4{0u, 0u, 0u, 0u};
+                if (in) q[h][i] = *reinterpret_cast<const u32x4_any*>(p + 32 * i);
+            }
+            m[h] = kLowest;
+            c[h] = kLowest;
+            l[h] = 0.0f;
+            f[h] = 1.0f;
+#pragma unroll
+            for (int i = 0; i < NO; ++i) o[h][i] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+        }
+    }
+
+    __device__ __forceinline__ void convert_query() {
+#pragma unroll
+        for (int h = 0; h < HT; ++h) {
+            factor[h] = a.scale * 1.44269504088896341f;
+            if constexpr (kI8 && DT == 1) {
+                uint32_t top = 0u;
+#pragma unroll
+                for (int i = 0; i < NQ; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const uint32_t x = q[h][i][e] & 0x7FFFu, y = q[h][i][e] >> 16 & 0x7FFFu;
+                        top = x > top ? x : top;
+                        top = y > top ? y : top;
+                    }
+                uint32_t t = __shfl_xor(top, 16);
+                top = t > top ? t : top;
+                t = __shfl_xor(top, 32);
+                top = t > top ? t : top;
+                const int e = (int)(top >> 7);  // biased exponent of the head's largest element
+                const int up = e == 255 || top == 0u ? 0 : 14 + 127 - e;
+#pragma unroll
+                for (int i = 0; i < NQ; ++i)
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) {
+                        const uint32_t bits = q[h][i][w];
+                        const float x = __builtin_ldexpf(__builtin_bit_cast(float, bits << 16), up);
+                        const float y = __builtin_ldexpf(__builtin_bit_cast(float, bits & 0xFFFF0000u), up);
+                        q[h][i][w] = (uint32_t)to_act_bits<0>(x) | (uint32_t)to_act_bits<0>(y) << 16;
+                    }
+                factor[h] = __builtin_ldexpf(factor[h], -up);
             }
         }
-        for (int off = 32; off >= 1; off >>= 1) s += __shfl_xor(s, off);
-        float vs = 1.0f;
-        if constexpr (KIND == 1) {
-            s *= *reinterpret_cast<const float*>(rec + L::scale(t, a.D, a.P, 0));
-            vs = *reinterpret_cast<const float*>(rec + L::scale(t, a.D, a.P, 1));
+    }
+
+    __device__ __forceinline__ void load_keys(const unsigned char* rec, int sub) {
+        const u32x4* p = reinterpret_cast<const u32x4*>(rec + (int64_t)sub * NL * 1024) + lane;
+#pragma unroll
+        for (int i = 0; i < NL; ++i) kb[i] = p[64 * i];
+    }
+    __device__ __forceinline__ void load_values(const unsigned char* rec, int sub) {
+        const u32x4* p = reinterpret_cast<const u32x4*>(rec + L::keys_bytes(D, a.P) + (int64_t)sub * NL * 1024) + lane;
+#pragma unroll
+        for (int i = 0; i < NL; ++i) vb[i] = p[64 * i];
+        if constexpr (kI8) {
+            const float* sc = reinterpret_cast<const float*>(rec + 2 * L::keys_bytes(D, a.P)) + sub * kTile + 4 * g;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                ks[i] = *reinterpret_cast<const floatx4*>(sc + 16 * i);
+                vs[i] = *reinterpret_cast<const floatx4*>(sc + a.P + 16 * i);
+            }
         }
-        s *= a.scale;
-        const float mn = fmaxf(m, s);
-        const float ref = mn == -INFINITY ? 0.0f : mn;
-        const float alpha = expf(m - ref), p = expf(s - ref);
-        l = l * alpha + p;
-        for (int i = 0; i < kMaxD / 64; ++i) o[i] = o[i] * alpha + p * vs * v[i];
+    }
+
+    // s[h][0..3]: tokens 4g .. 4g+3 of the tile, s[h][4..7]: 16 tokens on.
+    __device__ __forceinline__ void scores(float (&s)[HT][8]) {
+        floatx4 acc[HT][2];
+#pragma unroll
+        for (int h = 0; h < HT; ++h)
+#pragma unroll
+            for (int t = 0; t < 2; ++t) acc[h][t] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int i = 0; i < NQ; ++i)
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                u32x4 k;
+                if constexpr (kI8) {
+                    const u32x4& w = kb[t * (NQ / 2) + i / 2];
+                    k = i % 2 == 0 ? codes8_to_f16(w[0], w[1]) : codes8_to_f16(w[2], w[3]);
+                } else {
+                    k = kb[t * NQ + i];
+                }
+#pragma unroll
+                for (int h = 0; h < HT; ++h) acc[h][t] = mfma16x16x32<PDT>(k, q[h][i], acc[h][t]);
+            }
+#pragma unroll
+        for (int h = 0; h < HT; ++h)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) s[h][j] = acc[h][j / 4][j % 4];
+    }
+
+    // Scores to base 2, then to the probabilities' operand; `partial` tiles
+    // see only tokens from lo to hi - 1 of the tile.
+    __device__ __forceinline__ void probabilities(float (&s)[HT][8], u32x4 (&p)[HT], bool partial, int lo, int hi) {
+        uint32_t seen = 0xFFu;
+        if (partial) {
+            seen = 0u;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int t = j / 4 * 16 + 4 * g + j % 4;
+                seen |= (uint32_t)(t >= lo && t < hi) << j;
+            }
+            if constexpr (kI8) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (!(seen >> j & 1u)) vs[j / 4][j % 4] = 0.0f;
+            } else {
+                // An unseen value may be anything, and 0 * NaN is NaN.
+                uint32_t keep[4];
+#pragma unroll
+                for (int w = 0; w < 4; ++w)
+                    keep[w] = (seen >> (2 * w) & 1u ? 0xFFFFu : 0u) | (seen >> (2 * w + 1) & 1u ? 0xFFFF0000u : 0u);
+#pragma unroll
+                for (int i = 0; i < NL; ++i)
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) vb[i][w] &= keep[w];
+            }
+        }
+        float peak[HT];
+        bool above = false;
+#pragma unroll
+        for (int h = 0; h < HT; ++h) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                if constexpr (kI8) s[h][j] *= ks[j / 4][j % 4] * factor[h];
+                else s[h][j] *= factor[h];
+            }
+            if (partial) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (!(seen >> j & 1u)) s[h][j] = -INFINITY;
+            }
+            peak[h] = s[h][0];
+#pragma unroll
+            for (int j = 1; j < 8; ++j) peak[h] = fmaxf(peak[h], s[h][j]);
+            above |= peak[h] > m[h] + Pr::kHeadroom;
+        }
+        float e[HT][8], w[HT][8];
+        auto weigh = [&]() {
+#pragma unroll
+            for (int h = 0; h < HT; ++h) {
+                const float ref = kI8 ? m[h] : m[h] - Pr::kBias;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    e[h][j] = exp2_fast(s[h][j] - ref);
+                    w[h][j] = kI8 ? e[h][j] * vs[j / 4][j % 4] * f[h] : e[h][j];
+                }
+            }
+        };
+        if constexpr (kI8) {
+            weigh();
+#pragma unroll
+            for (int h = 0; h < HT; ++h) {
+                float top = w[h][0];
+#pragma unroll
+                for (int j = 1; j < 8; ++j) top = fmaxf(top, w[h][j]);
+                above |= top > 0x1p15f;
+            }
+        }
+        if (__builtin_amdgcn_ballot_w64(above) != 0) {  // move the references: rare after the first tiles
+#pragma unroll
+            for (int h = 0; h < HT; ++h) {
+                const float mn = column_max(fmaxf(m[h], peak[h]));
+                const float keep_l = exp2_fast(m[h] - mn);
+                float keep_o = keep_l;
+                if constexpr (kI8) {
+                    float y = 0.0f;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) y = fmaxf(y, exp2_fast(s[h][j] - mn) * vs[j / 4][j % 4]);
+                    // f stays within fp32: c is at least mn - 113
+                    const float cn = fmaxf(fmaxf(c[h], mn + __builtin_amdgcn_logf(column_max(y))), mn - 113.0f);
+                    keep_o = exp2_fast(c[h] - cn);
+                    c[h] = cn;
+                    f[h] = exp2_fast(Pr::kBias - (cn - mn));
+                }
+                m[h] = mn;
+                l[h] *= keep_l;
+#pragma unroll
+                for (int i = 0; i < NO; ++i)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) o[h][i][r] *= keep_o;
+            }
+            if constexpr (kI8) weigh();
+        }
+        if constexpr (!kI8) weigh();
+#pragma unroll
+        for (int h = 0; h < HT; ++h) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) l[h] += e[h][j];
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+                p[h][x] = (uint32_t)to_act_bits<PDT>(w[h][2 * x]) | (uint32_t)to_act_bits<PDT>(w[h][2 * x + 1]) << 16;
+        }
+    }
+
+    __device__ __forceinline__ void accumulate(const u32x4 (&p)[HT]) {
+#pragma unroll
+        for (int i = 0; i < NO; ++i) {
+            u32x4 v;
+            if constexpr (kI8) {
+                const u32x4& w = vb[i / 2];
+                v = i % 2 == 0 ? codes8_to_f16(w[0], w[1]) : codes8_to_f16(w[2], w[3]);
+            } else {
+                v = vb[i];
+            }
+#pragma unroll
+            for (int h = 0; h < HT; ++h) o[h][i] = mfma16x16x32<PDT>(v, p[h], o[h][i]);
+        }
+    }
+
+    // This wave's share of tiles [from, to) of sequence b: every kWaves-th,
+    // those of missing pages left out.
+    __device__ __forceinline__ void run(int64_t b, int kv_head, const Span& sp, int from, int to) {
+        const int tiles_per_page = a.P / kTile;
+        int block = from + wave;  // first tile of the 64 in hand, lane i holding block + kWaves * i
+        uint64_t todo = 0;
+        int64_t place = 0;
+        int sub_l = 0;
+        auto fetch = [&]() {
+            while (todo == 0 && block < to) {
+                const int tile = block + kWaves * lane;
+                int64_t page = -1;
+                if (tile < to) {
+                    page = a.table[b * a.table_ld + tile / tiles_per_page];
+                    sub_l = tile % tiles_per_page;
+                }
+                const bool ok = page >= 0 && page < a.pages;
+                place = ok ? (page * a.H + kv_head) * L::record_bytes(D, a.P) : 0;
+                todo = __builtin_amdgcn_ballot_w64(ok);
+                if (todo == 0) block += 64 * kWaves;
+            }
+        };
+        const unsigned char* rec = nullptr;
+        int sub = 0, tile = 0;
+        auto next = [&]() -> bool {  // the next tile's place, if there is one
+            if (todo == 0) fetch();
+            if (todo == 0) return false;
+            const int i = __builtin_ctzll(todo);
+            todo &= todo - 1;
+            rec = a.cache + read_lane(place, i);
+            sub = __builtin_amdgcn_readlane(sub_l, i);
+            tile = block + kWaves * i;
+            if (todo == 0) block += 64 * kWaves;
+            return true;
+        };
+        if (!next()) return;
+        load_keys(rec, sub);
+        load_values(rec, sub);
+        convert_query();
+        bool more = true;
+        while (more) {
+            const int at = tile * kTile;
+            float s[HT][8];
+            u32x4 p[HT];
+            scores(s);
+            more = next();
+            if (more) load_keys(rec, sub);
+            const int lo = sp.lo - at, hi = sp.n - at;
+            probabilities(s, p, lo > 0 || hi < kTile, lo, hi);
+            accumulate(p);
+            if (more) load_values(rec, sub);
+        }
+    }
+
+    // The four waves' results in LDS, relative to each wave's reference.
+    __device__ __forceinline__ void to_lds(float* lds, int heads) {
+        float* ml = lds + kWaves * heads * kLd;
+#pragma unroll
+        for (int h = 0; h < HT; ++h) {
+            l[h] = column_sum(l[h]);
+            const int head = 16 * h + col;
+            if (head < heads) {
+                const float back = kI8 ? exp2_fast(c[h] - Pr::kBias - m[h]) : 1.0f;
+                float* p = lds + (wave * heads + head) * kLd + 4 * g;
+#pragma unroll
+                for (int i = 0; i < NO; ++i) {
+                    floatx4 v = o[h][i];
+                    if constexpr (kI8) {
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) v[r] *= back;
+                    }
+                    *reinterpret_cast<floatx4*>(p + 16 * i) = v;
+                }
+                if (g == 0) {
+                    ml[2 * (wave * heads + head)] = m[h];
+                    ml[2 * (wave * heads + head) + 1] = l[h];
+                }
+            }
+        }
+    }
+};
+
+// A running join of partial results (m, l, o): sums relative to m.
+struct Join {
+    float m = kLowest, l = 0.0f;
+    floatx4 o{0.0f, 0.0f, 0.0f, 0.0f};
+    __device__ __forceinline__ void rescale(float mn) {
+        const float keep = exp2_fast(m - mn);
+        l *= keep;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) o[r] *= keep;
         m = mn;
     }
-    __shared__ float sm[4], sl[4], so[4][kMaxD];
-    if (lane == 0) {
-        sm[wave] = m;
-        sl[wave] = l;
+    __device__ __forceinline__ void add(float pm, float pl, const floatx4& po) {
+        const float w = exp2_fast(pm - m);
+        l += w * pl;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) o[r] += w * po[r];
     }
-    for (int i = 0; i < kMaxD / 64; ++i) so[wave][64 * i + lane] = o[i];
-    __syncthreads();
-    const float mm = fmaxf(fmaxf(sm[0], sm[1]), fmaxf(sm[2], sm[3]));
-    const float ref = mm == -INFINITY ? 0.0f : mm;
-    float total = 0.0f, acc = 0.0f;
-    const int d = threadIdx.x;
-    for (int w = 0; w < 4; ++w) {
-        const float f = expf(sm[w] - ref);
-        total += f * sl[w];
-        acc += f * so[w][d];
+};
+
+template <int DT>
+__device__ __forceinline__ void store_out(const AttentionArgs& a, int64_t b, int head, int d, const Join& j) {
+    const float inv = 1.0f / (j.l == 0.0f ? 1.0f : j.l);
+    u32x2 v;
+#pragma unroll
+    for (int x = 0; x < 2; ++x)
+        v[x] = (uint32_t)to_act_bits<DT>(j.o[2 * x] * inv) | (uint32_t)to_act_bits<DT>(j.o[2 * x + 1] * inv) << 16;
+    *reinterpret_cast<u32x2_any*>(a.out + b * a.o_ts + (int64_t)head * a.o_hs + d) = v;
+}
+
+// Workspace: counters (two per workgroup and level), then two partial results
+// per workgroup (0: of a head begun by an earlier workgroup, 1: of one that
+// begins here): per head two pairs (m, l), for even and odd levels of the join
+// (other waves may still read the one while the next is written), then D floats.
+template <int D, int HT>
+struct Partial {
+    static constexpr int kStride = D + 4;
+    static constexpr int64_t kFloats = 16 * HT * kStride;
+    static __device__ __forceinline__ float* at(float* ws, int64_t wg, int slot) { return ws + (2 * wg + slot) * kFloats; }
+};
+
+template <int DT, int KIND, int D, int HT>
+__global__ __launch_bounds__(256, (kPerCU<KIND, D, HT>)) void attention_kernel(AttentionArgs a) {
+    using A = Attend<DT, KIND, D, HT>;
+    using Pt = Partial<D, HT>;
+    extern __shared__ __align__(16) float lds[];
+    __shared__ int s_last;
+    A w(a);
+    const int lane = w.lane;
+    const int64_t wg = blockIdx.x, wgs = gridDim.x;
+    const int group = a.Hq / a.H;
+    const int head_tiles = (group + A::kCols - 1) / A::kCols;
+    const int64_t units = (int64_t)a.H * head_tiles;  // of one sequence
+
+    // Every wave finds the workgroup's share by itself: lane i sums the
+    // sequences [i * run, (i + 1) * run).
+    const int64_t run = (a.B + 63) / 64;
+    int64_t tiles = 0, chunks = 0;
+    int length = 0;
+    for (int64_t b = lane * run; b < (lane + 1) * run && b < a.B; ++b) {
+        length = a.lengths[b];
+        const int n = Span(a, length).count;
+        tiles += n;
+        chunks += (n + kMinTiles - 1) / kMinTiles;
     }
-    if (d < a.D) a.out[b * a.o_ts + hq * a.o_hs + d] = to_act_bits<DT>(acc / (total == 0.0f ? 1.0f : total));
+    const int64_t tiles_to = wave_scan(tiles, lane), chunks_to = wave_scan(chunks, lane);
+    const int64_t all_tiles = units * read_lane(tiles_to, 63), all_chunks = units * read_lane(chunks_to, 63);
+    // Sequences that see nothing.
+    for (int64_t b = wg; b < a.B; b += wgs) {
+        const int len = run == 1 ? __builtin_amdgcn_readlane(length, (int)b) : a.lengths[b];
+        if (Span(a, len).count != 0) continue;
+        for (int i = threadIdx.x; i < a.Hq * D; i += 256) a.out[b * a.o_ts + (int64_t)(i / D) * a.o_hs + i % D] = 0;
+    }
+    // Few tiles: a workgroup per kMinTiles of one head, so that most heads
+    // need no join. Else equal runs of the list, across heads.
+    const bool by_chunk = all_chunks <= wgs;
+    const int64_t all = by_chunk ? all_chunks : all_tiles;
+    const int64_t per = by_chunk ? 1 : divide(all_tiles + wgs - 1, wgs);
+    int64_t pos = wg * per;
+    const int64_t end = pos + per < all ? pos + per : all;
+    if (pos >= end) return;
+    const int64_t begin = pos;
+
+    // The block of 64 sequences that holds `pos`, and in it the sequence.
+    const int64_t to = by_chunk ? chunks_to : tiles_to, of = by_chunk ? chunks : tiles;
+    int at = __builtin_ctzll(__builtin_amdgcn_ballot_w64(units * to > pos));
+    int64_t base = at * run, before = read_lane(to - of, at);  // items of the sequences before `base`
+    int64_t seq_items = of, seq_to = to;                       // of sequence base + lane, when base is found
+    if (run == 1) {
+        base = 0;
+        before = 0;
+    } else {
+        for (;;) {
+            length = base + lane < a.B ? a.lengths[base + lane] : 0;
+            const int n = Span(a, length).count;
+            seq_items = by_chunk ? (n + kMinTiles - 1) / kMinTiles : n;
+            seq_to = before + wave_scan(seq_items, lane);
+            if (units * read_lane(seq_to, 63) > pos) break;
+            before = read_lane(seq_to, 63);
+            base += 64;
+        }
+        at = __builtin_ctzll(__builtin_amdgcn_ballot_w64(units * seq_to > pos));
+    }
+
+    while (pos < end) {
+        // Sequence b = base + at; its items start at seq_begin.
+        const int64_t b = base + at;
+        const int64_t items = read_lane(seq_items, at);  // of one unit
+        const int64_t seq_end = units * read_lane(seq_to, at), seq_begin = seq_end - units * items;
+        const Span sp(a, __builtin_amdgcn_readlane(length, at));
+        int64_t unit = divide(pos - seq_begin, items);
+        for (; pos < end && pos < seq_end; ++unit) {
+            const int64_t unit_begin = seq_begin + unit * items, unit_end = unit_begin + items;
+            const int64_t stop = unit_end < end ? unit_end : end;
+            int from = (int)(pos - unit_begin), upto = (int)(stop - unit_begin);
+            if (by_chunk) {
+                from *= kMinTiles;
+                upto = upto * kMinTiles < sp.count ? upto * kMinTiles : sp.count;
+            }
+            const bool whole = pos == unit_begin && stop == unit_end;
+            const int kv_head = (int)(unit / head_tiles), head_tile = (int)(unit % head_tiles);
+            const int head0 = kv_head * group + head_tile * A::kCols;
+            const int heads = group - head_tile * A::kCols < A::kCols ? group - head_tile * A::kCols : A::kCols;
+            pos = stop;
+
+            w.load_query(b, head0, heads);
+            w.run(b, kv_head, sp, sp.first + from, sp.first + upto);
+            __syncthreads();  // the last join's reads of LDS are done
+            w.to_lds(lds, heads);
+            __syncthreads();
+            const float* ml = lds + kWaves * heads * A::kLd;
+            const int slot = unit_begin >= begin ? 1 : 0;
+            for (int e = threadIdx.x; e < heads * (D / 4); e += 256) {
+                const int head = e / (D / 4), d = e % (D / 4) * 4;
+                Join j;
+                float mn = j.m;
+#pragma unroll
+                for (int v = 0; v < kWaves; ++v) mn = fmaxf(mn, ml[2 * (v * heads + head)]);
+                j.m = mn;
+#pragma unroll
+                for (int v = 0; v < kWaves; ++v)
+                    j.add(ml[2 * (v * heads + head)], ml[2 * (v * heads + head) + 1],
+                          *reinterpret_cast<const floatx4*>(lds + (v * heads + head) * A::kLd + d));
+                if (whole) {
+                    store_out<DT>(a, b, head0 + head, d, j);
+                } else {
+                    float* p = Pt::at(a.partials, wg, slot) + head * Pt::kStride;
+                    store_coherent(p + 4 + d, j.o);
+                    if (d == 0) store_coherent2(p, j.m, j.l);
+                }
+            }
+            if (whole) continue;
+
+            // Join: of kFan workgroups, by the last of them; then of those results.
+            const int64_t first = by_chunk ? wg - (from / kMinTiles) : divide(unit_begin, per);
+            const int64_t last = by_chunk ? first + items - 1 : divide(unit_end - 1, per);
+            int64_t rank = wg - first, count = last - first + 1, step = 1;
+            uint32_t* counters = a.counters;
+            for (int level = 0;; ++level) {
+                const int64_t lead = rank / kFan * kFan;
+                const int size = (int)(count - lead < kFan ? count - lead : kFan);
+                const int64_t lead_wg = first + lead * step;
+                const int lead_slot = lead == 0 ? 1 : 0;
+                wait_vector_memory();
+                __syncthreads();
+                if (threadIdx.x == 0) {
+                    uint32_t* counter = counters + 2 * lead_wg + lead_slot;
+                    const uint32_t old = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+                    s_last = old + 1 == (uint32_t)size;
+                    if (old + 1 == (uint32_t)size) __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+                }
+                __syncthreads();
+                const bool mine = s_last != 0;
+                if (!mine) break;
+                const bool done = count <= kFan;
+                for (int e = threadIdx.x; e < heads * (D / 4); e += 256) {
+                    const int head = e / (D / 4), d = e % (D / 4) * 4;
+                    Join j;
+#pragma unroll 1
+                    for (int i0 = 0; i0 < size; i0 += kBatch) {
+                        float2 pml[kBatch];
+                        floatx4 po[kBatch];
+#pragma unroll
+                        for (int i = 0; i < kBatch; ++i) {
+                            const int r = i0 + i < size ? i0 + i : i0;
+                            const float* p = Pt::at(a.partials, lead_wg + r * step, lead == 0 && r == 0 ? 1 : 0) + head * Pt::kStride;
+                            pml[i] = load_coherent2(p + (level & 1 ? 2 : 0));
+                            po[i] = load_coherent(p + 4 + d);
+                        }
+                        float mn = j.m;
+#pragma unroll
+                        for (int i = 0; i < kBatch; ++i) mn = fmaxf(mn, pml[i].x);
+                        j.rescale(mn);
+#pragma unroll
+                        for (int i = 0; i < kBatch; ++i)
+                            if (i0 + i < size) j.add(pml[i].x, pml[i].y, po[i]);
+                    }
+                    if (done) {
+                        store_out<DT>(a, b, head0 + head, d, j);
+                    } else {  // in the leader's place
+                        float* p = Pt::at(a.partials, lead_wg, lead_slot) + head * Pt::kStride;
+                        store_coherent(p + 4 + d, j.o);
+                        if (d == 0) store_coherent2(p + (level & 1 ? 0 : 2), j.m, j.l);
+                    }
+                }
+                if (done) break;
+                rank = lead / kFan;
+                step *= kFan;
+                count = (count + kFan - 1) / kFan;
+                counters += 2 * wgs;
+            }
+        }
+        // The next sequence that sees anything.
+        if (pos >= end) break;
+        uint64_t rest = at < 63 ? __builtin_amdgcn_ballot_w64(seq_items > 0) >> (at + 1) << (at + 1) : 0;
+        while (rest == 0) {
+            before = read_lane(seq_to, 63);
+            base += 64;
+            length = base + lane < a.B ? a.lengths[base + lane] : 0;
+            const int n = Span(a, length).count;
+            seq_items = by_chunk ? (n + kMinTiles - 1) / kMinTiles : n;
+            seq_to = before + wave_scan(seq_items, lane);
+            rest = __builtin_amdgcn_ballot_w64(seq_items > 0);
+        }
+        at = __builtin_ctzll(rest);
+    }
+}
+
+struct Shape {
+    int heads, per_cu;      // query heads of a workgroup's operand, workgroups per CU
+    int64_t wgs;
+    int64_t partial_floats; // of one workgroup
+};
+
+template <int KIND, int D, int HT>
+Shape shape_of() {
+    return {16 * HT, kPerCU<KIND, D, HT>, 0, 2 * Partial<D, HT>::kFloats};
+}
+
+// Calls fn with the head size and the head tiles as constants.
+template <class Fn>
+void by_shape(int D, int group, Fn&& fn) {
+    using std::integral_constant;
+    auto with = [&](auto d) {
+        if (group <= 16) fn(d, integral_constant<int, 1>{});
+        else fn(d, integral_constant<int, 2>{});
+    };
+    if (D == 64) with(integral_constant<int, 64>{});
+    else if (D == 128) with(integral_constant<int, 128>{});
+    else if (D == 192) with(integral_constant<int, 192>{});
+    else with(integral_constant<int, 256>{});
+}
+
+// As many workgroups as run at once, or as there can be parts of kMinTiles.
+Shape plan(const AttentionArgs& a, int kind) {
+    Shape s{};
+    const int group = a.Hq / a.H;
+    by_shape(a.D, group, [&](auto d, auto ht) {
+        s = kind == 0 ? shape_of<0, decltype(d)::value, decltype(ht)::value>() : shape_of<1, decltype(d)::value, decltype(ht)::value>();
+    });
+    int64_t tokens = a.width * a.P;
+    if (a.window > 0 && a.window < tokens) tokens = a.window + kTile;
+    const int64_t parts = (tokens / kTile + kMinTiles) / kMinTiles;
+    const int64_t units = (int64_t)a.H * ((group + s.heads - 1) / s.heads);
+    s.wgs = kCUs * s.per_cu;
+    if (a.B * units < s.wgs && a.B * units * parts < s.wgs) s.wgs = a.B * units * parts;
+    return s;
+}
+
+template <int DT, int KIND>
+hipError_t launch(const AttentionArgs& a, const Shape& s, hipStream_t stream) {
+    hipError_t e = hipSuccess;
+    const int group = a.Hq / a.H;
+    by_shape(a.D, group, [&](auto d, auto ht) {
+        constexpr int D = decltype(d)::value, HT = decltype(ht)::value;
+        const int heads = group < 16 * HT ? group : 16 * HT;
+        const size_t lds = (size_t)kWaves * heads * (Attend<DT, KIND, D, HT>::kLd + 2) * 4;
+        e = allow_lds<attention_kernel<DT, KIND, D, HT>>(lds);
+        if (e != hipSuccess) return;
+        hipLaunchKernelGGL((attention_kernel<DT, KIND, D, HT>), dim3((unsigned)s.wgs), dim3(256), lds, stream, a);
+        e = hipGetLastError();
+    });
+    return e;
 }
 
 }  // namespace
 
-hipError_t launch_attention(const AttentionArgs& a, int kind, int dtype, hipStream_t stream) {
-    const dim3 grid((unsigned)(a.B * a.Hq));
-    if (kind == 0 && dtype == 0) hipLaunchKernelGGL((attention_kernel<0, 0>), grid, dim3(256), 0, stream, a);
-    else if (kind == 0) hipLaunchKernelGGL((attention_kernel<1, 0>), grid, dim3(256), 0, stream, a);
-    else if (dtype == 0) hipLaunchKernelGGL((attention_kernel<0, 1>), grid, dim3(256), 0, stream, a);
-    else hipLaunchKernelGGL((attention_kernel<1, 1>), grid, dim3(256), 0, stream, a);
-    return hipGetLastError();
+size_t attention_workspace(const AttentionArgs& a, int kind) {
+    const Shape s = plan(a, kind);
+    return kCounterRegionBytes + (size_t)s.wgs * s.partial_floats * 4;
+}
+
+hipError_t launch_attention(AttentionArgs a, int kind, int dtype, void* workspace, hipStream_t stream) {
+    const Shape s = plan(a, kind);
+    a.counters = static_cast<uint32_t*>(workspace);
+    a.partials = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + kCounterRegionBytes);
+    if (kind == 0) return dtype == 0 ? launch<0, 0>(a, s, stream) : launch<1, 0>(a, s, stream);
+    return dtype == 0 ? launch<0, 1>(a, s, stream) : launch<1, 1>(a, s, stream);
 }
 
 }  // namespace w4a16

@@ -21,6 +21,10 @@ __device__ __forceinline__ void store_coherent(float* p, const floatx4& v) {
     __hip_atomic_store(q + 1, __builtin_bit_cast(uint64_t, __builtin_shufflevector(v, v, 2, 3)), __ATOMIC_RELAXED,
                        __HIP_MEMORY_SCOPE_AGENT);
 }
+__device__ __forceinline__ void store_coherent2(float* p, float x, float y) {
+    __hip_atomic_store(reinterpret_cast<uint64_t*>(p), __builtin_bit_cast(uint64_t, make_float2(x, y)), __ATOMIC_RELAXED,
+                       __HIP_MEMORY_SCOPE_AGENT);
+}
 // Four coherent 16-byte loads and the wait for them, in one asm statement so
 // that no compiler-inserted instruction can read the destination registers
 // while the loads are in flight (the compiler does not track asm loads).
@@ -44,6 +48,10 @@ __device__ __forceinline__ floatx4 load_coherent(const float* p) {
     const uint64_t hi = __hip_atomic_load(q + 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     const float2 a = __builtin_bit_cast(float2, lo), b = __builtin_bit_cast(float2, hi);
     return floatx4{a.x, a.y, b.x, b.y};
+}
+__device__ __forceinline__ float2 load_coherent2(const float* p) {
+    return __builtin_bit_cast(float2, __hip_atomic_load(reinterpret_cast<const uint64_t*>(p), __ATOMIC_RELAXED,
+                                                        __HIP_MEMORY_SCOPE_AGENT));
 }
 // Waits until every vector memory access this wave issued has completed
 // (write-through stores: reached the coherence point).

@@ -195,7 +195,12 @@ struct AttentionArgs {
     int64_t window = 0;
     int Hq = 0, H = 0, D = 0, P = 0;
     float scale = 0.0f;
+    uint32_t* counters = nullptr;  // set by launch_attention
+    float* partials = nullptr;
 };
-hipError_t launch_attention(const AttentionArgs& a, int kind, int dtype, hipStream_t stream);
+// Bytes of workspace: the counter region, then the partial results of heads
+// that several workgroups share. Only sizes are read from `a`.
+size_t attention_workspace(const AttentionArgs& a, int kind);
+hipError_t launch_attention(AttentionArgs a, int kind, int dtype, void* workspace, hipStream_t stream);
 
 }  // namespace w4a16

@@ -727,7 +727,10 @@ w4a16_status w4a16_attention_workspace_size(int64_t B, int32_t q_heads, int32_t 
     size_t unused = 0;
     w4a16_status st = check_cache(0, kv_heads, head_dim, page_size, kind, &unused);
     if (st != W4A16_OK || (st = check_attention(B, q_heads, kv_heads, page_size, table_width, window)) != W4A16_OK) return st;
-    *out_bytes = 0;
+    AttentionArgs a;
+    a.B = B, a.width = table_width, a.window = window;
+    a.Hq = q_heads, a.H = kv_heads, a.D = head_dim, a.P = page_size;
+    *out_bytes = B > 0 ? attention_workspace(a, kind) : 0;
     return W4A16_OK;
 }
 
@@ -764,8 +767,13 @@ w4a16_status w4a16_attention(const void* q, int64_t q_bs, int64_t q_hs, int64_t 
     a.window = window;
     a.Hq = q_heads, a.H = kv_heads, a.D = head_dim, a.P = page_size;
     a.scale = scale;
-    (void)workspace, (void)workspace_bytes;
-    hipError_t e = launch_attention(a, kind, dtype, stream);
+    const size_t ws_need = attention_workspace(a, kind);
+    if (workspace == nullptr || workspace_bytes < ws_need)
+        return fail(W4A16_ERR_SIZE, "workspace of %zu bytes is smaller than the %zu bytes this call needs",
+                    workspace == nullptr ? (size_t)0 : workspace_bytes, ws_need);
+    if (reinterpret_cast<uintptr_t>(workspace) & 255u)
+        return fail(W4A16_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+    hipError_t e = launch_attention(a, kind, dtype, workspace, stream);
     if (e != hipSuccess) return hip_fail("attention kernel launch", e);
     return W4A16_OK;
 }

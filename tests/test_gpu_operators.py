@@ -402,6 +402,31 @@ def test_attention_long(Hq, H, D, P, lens, kind, dtype):
     assert first.shape == (len(lens), Hq, D)
 
 
+@pytest.mark.parametrize("kind,D,n", [(ref.KV_ACT, 64, 140000), (ref.KV_ACT, 64, 500000), (ref.KV_ACT, 256, 8200),
+                                      (ref.KV_INT8, 64, 140000), (ref.KV_INT8, 128, 8200)])
+def test_attention_one_head_joined_over_levels(kind, D, n):
+    Batch("levels", [n], 1, D, 32, kind, "f16").check(3)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("B,most,zeros", [(64, 1500, 3), (96, 2000, 4), (200, 300, 2), (700, 40, 2), (130, 5000, 60)])
+def test_attention_many_sequences(B, most, zeros, kind):
+    """Lengths from a square law, most of them cut by the division of work; every `zeros`-th is empty, with runs of
+    empty ones longer than a block of 64 in the last case."""
+    r = np.random.default_rng(B)
+    lens = (most * r.random(B) ** 2).astype(int) + 1
+    lens[::zeros] = 0
+    if zeros == 60:
+        lens[5:125] = 0
+    Batch("many", lens.tolist(), 2, 64, 32, kind, "bf16").check(8)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_attention_split_windows_and_wide_groups(kind):
+    """Heads shared by workgroups with a window that starts inside a tile, and more query heads than one operand."""
+    Batch("split window", [9000, 4000, 0, 7777, 12345], 2, 128, 64, kind, "f16").check(40, window=5001)
+
+
 @pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("window", [1, 2, 31, 32, 33, 100, 1000, 100000])
 def test_attention_window(window, kind):

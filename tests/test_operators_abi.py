@@ -254,6 +254,22 @@ def test_attention_workspace_size(lib):
     assert lib.w4a16_attention_workspace_size(1, 32, 8, 120, 64, 4, 0, 0, ctypes.byref(out)) == UNSUPPORTED
     assert lib.w4a16_attention_workspace_size(1, 32, 8, 128, 64, 4, -1, 0, ctypes.byref(out)) == INVALID
     assert w4.attention_workspace_size(0, 32, 8, 128, 64, 4, 0, w4.KV_ACT) == 0
+    # bounded whatever the lengths, and never below the counter region
+    small = w4.attention_workspace_size(1, 32, 8, 128, 64, 4, 0, w4.KV_ACT)
+    assert w4.workspace_counter_bytes() < small < 1 << 20
+    large = w4.attention_workspace_size(4096, 32, 8, 128, 64, 1 << 20, 0, w4.KV_ACT)
+    assert large == w4.attention_workspace_size(256, 32, 8, 128, 64, 1 << 20, 0, w4.KV_ACT) < 64 << 20
+    # a short window needs no more than a short table
+    assert w4.attention_workspace_size(1, 32, 8, 128, 64, 1 << 20, 100, w4.KV_ACT) <= small
+
+
+def test_attention_checks_its_workspace(lib):
+    need = w4.attention_workspace_size(2, 32, 8, 128, 64, 2, 0, w4.KV_ACT)
+    for ws, nbytes in ((None, 0), (None, need), (P, need - 1)):
+        assert _attention(lib, ws=ws, wsb=nbytes) == SIZE
+        assert f"smaller than the {need} bytes" in w4.last_error()
+    assert _attention(lib, ws=ctypes.c_void_p(4096 + 16), wsb=need) == INVALID
+    assert "256-byte aligned" in w4.last_error()
 
 
 def test_binding_refuses_cpu_tensors():
