@@ -94,13 +94,28 @@ __device__ __forceinline__ int64_t read_lane(int64_t v, int lane) {
     return (int64_t)((uint64_t)hi << 32 | lo);
 }
 
-__device__ __forceinline__ int64_t wave_scan(int64_t v, int lane) {
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) {
-        const int64_t o = __shfl_up(v, d);
-        if (lane >= d) v += o;
-    }
+// v of the lane that a DPP control names, 0 where there is none.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int64_t from_lane(int64_t v) {
+    const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)v, CTRL, ROWS, 0xF, false);
+    const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)(v >> 32), CTRL, ROWS, 0xF, false);
+    return (int64_t)((uint64_t)hi << 32 | lo);
+}
+// Sum over lanes 0 .. lane.
+__device__ __forceinline__ int64_t wave_scan(int64_t v) {
+    v += from_lane<0x111, 0xF>(v);  // row_shr:1, 2, 4, 8: within 16 lanes
+    v += from_lane<0x112, 0xF>(v);
+    v += from_lane<0x114, 0xF>(v);
+    v += from_lane<0x118, 0xF>(v);
+    v += from_lane<0x142, 0xA>(v);  // row_bcast:15 into rows 1 and 3
+    v += from_lane<0x143, 0xC>(v);  // row_bcast:31 into rows 2 and 3
     return v;
+}
+
+// The loads before this are issued before anything after it.
+__device__ __forceinline__ void issue_fence() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
 }
 
 // a / b of non-negative numbers, mostly small.
@@ -202,16 +217,14 @@ struct Attend {
         }
     }
 
-    __device__ __forceinline__ void load_keys(const unsigned char* rec, int sub) {
-        const u32x4* p = reinterpret_cast<const u32x4*>(rec + (int64_t)sub * NL * 1024) + lane;
+    __device__ __forceinline__ void load_keys(const unsigned char* rec, int sub, int unit) {
+        const u32x4* p = reinterpret_cast<const u32x4*>(rec + (int64_t)sub * NL * 1024) + unit;
 #pragma unroll
         for (int i = 0; i < NL; ++i) kb[i] = p[64 * i];
     }
-    __device__ __forceinline__ void load_values(const unsigned char* rec, int sub) {
-        const u32x4* p = reinterpret_cast<const u32x4*>(rec + L::keys_bytes(D, a.P) + (int64_t)sub * NL * 1024) + lane;
-#pragma unroll
-        for (int i = 0; i < NL; ++i) vb[i] = p[64 * i];
-        if constexpr (kI8) {
+    __device__ __forceinline__ void load_values(const unsigned char* rec, int sub, int unit) {
+        if constexpr (kI8) {  // first: they are needed first
+
             const float* sc = reinterpret_cast<const float*>(rec + 2 * L::keys_bytes(D, a.P)) + sub * kTile + 4 * g;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
@@ -219,6 +232,9 @@ struct Attend {
                 vs[i] = *reinterpret_cast<const floatx4*>(sc + a.P + 16 * i);
             }
         }
+        const u32x4* p = reinterpret_cast<const u32x4*>(rec + L::keys_bytes(D, a.P) + (int64_t)sub * NL * 1024) + unit;
+#pragma unroll
+        for (int i = 0; i < NL; ++i) vb[i] = p[64 * i];
     }
 
     // s[h][0..3]: tokens 4g .. 4g+3 of the tile, s[h][4..7]: 16 tokens on.
@@ -371,6 +387,7 @@ struct Attend {
     // those of missing pages left out.
     __device__ __forceinline__ void run(int64_t b, int kv_head, const Span& sp, int from, int to) {
         const int tiles_per_page = a.P / kTile;
+        const int whole_shift = (tiles_per_page & (tiles_per_page - 1)) == 0 ? __builtin_ctz(tiles_per_page) : -1;
         int block = from + wave;  // first tile of the 64 in hand, lane i holding block + kWaves * i
         uint64_t todo = 0;
         int64_t place = 0;
@@ -380,8 +397,9 @@ struct Attend {
                 const int tile = block + kWaves * lane;
                 int64_t page = -1;
                 if (tile < to) {
-                    page = a.table[b * a.table_ld + tile / tiles_per_page];
-                    sub_l = tile % tiles_per_page;
+                    const int at = whole_shift >= 0 ? tile >> whole_shift : tile / tiles_per_page;
+                    page = a.table[b * a.table_ld + at];
+                    sub_l = tile - at * tiles_per_page;
                 }
                 const bool ok = page >= 0 && page < a.pages;
                 place = ok ? (page * a.H + kv_head) * L::record_bytes(D, a.P) : 0;
@@ -403,22 +421,32 @@ struct Attend {
             return true;
         };
         if (!next()) return;
-        load_keys(rec, sub);
-        load_values(rec, sub);
+        load_keys(rec, sub, lane);
+        issue_fence();
+        load_values(rec, sub, lane);
+        issue_fence();
         convert_query();
         bool more = true;
-        while (more) {
+        do {
             const int at = tile * kTile;
             float s[HT][8];
             u32x4 p[HT];
-            scores(s);
+            // After the last tile every lane loads that tile's first unit
+            // again (one cache line): loads on a condition would have to be
+            // waited for as if they were the newest.
             more = next();
-            if (more) load_keys(rec, sub);
+            const int unit = more ? lane : 0;
+            scores(s);
+            issue_fence();
+            load_keys(rec, sub, unit);
+            issue_fence();
             const int lo = sp.lo - at, hi = sp.n - at;
             probabilities(s, p, lo > 0 || hi < kTile, lo, hi);
             accumulate(p);
-            if (more) load_values(rec, sub);
-        }
+            issue_fence();
+            load_values(rec, sub, unit);
+            issue_fence();
+        } while (more);
     }
 
     // The four waves' results in LDS, relative to each wave's reference.
@@ -498,9 +526,9 @@ __global__ __launch_bounds__(256, (kPerCU<KIND, D, HT>)) void attention_kernel(A
     A w(a);
     const int lane = w.lane;
     const int64_t wg = blockIdx.x, wgs = gridDim.x;
-    const int group = a.Hq / a.H;
+    const int group = a.group;
     const int head_tiles = (group + A::kCols - 1) / A::kCols;
-    const int64_t units = (int64_t)a.H * head_tiles;  // of one sequence
+    const int units = a.H * head_tiles;  // of one sequence
 
     // Every wave finds the workgroup's share by itself: lane i sums the
     // sequences [i * run, (i + 1) * run).
@@ -513,7 +541,7 @@ __global__ __launch_bounds__(256, (kPerCU<KIND, D, HT>)) void attention_kernel(A
         tiles += n;
         chunks += (n + kMinTiles - 1) / kMinTiles;
     }
-    const int64_t tiles_to = wave_scan(tiles, lane), chunks_to = wave_scan(chunks, lane);
+    const int64_t tiles_to = wave_scan(tiles), chunks_to = wave_scan(chunks);
     const int64_t all_tiles = units * read_lane(tiles_to, 63), all_chunks = units * read_lane(chunks_to, 63);
     // Sequences that see nothing.
     for (int64_t b = wg; b < a.B; b += wgs) {
@@ -544,7 +572,7 @@ __global__ __launch_bounds__(256, (kPerCU<KIND, D, HT>)) void attention_kernel(A
             length = base + lane < a.B ? a.lengths[base + lane] : 0;
             const int n = Span(a, length).count;
             seq_items = by_chunk ? (n + kMinTiles - 1) / kMinTiles : n;
-            seq_to = before + wave_scan(seq_items, lane);
+            seq_to = before + wave_scan(seq_items);
             if (units * read_lane(seq_to, 63) > pos) break;
             before = read_lane(seq_to, 63);
             base += 64;
@@ -558,7 +586,7 @@ __global__ __launch_bounds__(256, (kPerCU<KIND, D, HT>)) void attention_kernel(A
         const int64_t items = read_lane(seq_items, at);  // of one unit
         const int64_t seq_end = units * read_lane(seq_to, at), seq_begin = seq_end - units * items;
         const Span sp(a, __builtin_amdgcn_readlane(length, at));
-        int64_t unit = divide(pos - seq_begin, items);
+        int unit = (int)divide(pos - seq_begin, items);
         for (; pos < end && pos < seq_end; ++unit) {
             const int64_t unit_begin = seq_begin + unit * items, unit_end = unit_begin + items;
             const int64_t stop = unit_end < end ? unit_end : end;
@@ -568,7 +596,7 @@ __global__ __launch_bounds__(256, (kPerCU<KIND, D, HT>)) void attention_kernel(A
                 upto = upto * kMinTiles < sp.count ? upto * kMinTiles : sp.count;
             }
             const bool whole = pos == unit_begin && stop == unit_end;
-            const int kv_head = (int)(unit / head_tiles), head_tile = (int)(unit % head_tiles);
+            const int kv_head = head_tiles == 1 ? unit : unit / head_tiles, head_tile = unit - kv_head * head_tiles;
             const int head0 = kv_head * group + head_tile * A::kCols;
             const int heads = group - head_tile * A::kCols < A::kCols ? group - head_tile * A::kCols : A::kCols;
             pos = stop;
@@ -669,7 +697,7 @@ __global__ __launch_bounds__(256, (kPerCU<KIND, D, HT>)) void attention_kernel(A
             length = base + lane < a.B ? a.lengths[base + lane] : 0;
             const int n = Span(a, length).count;
             seq_items = by_chunk ? (n + kMinTiles - 1) / kMinTiles : n;
-            seq_to = before + wave_scan(seq_items, lane);
+            seq_to = before + wave_scan(seq_items);
             rest = __builtin_amdgcn_ballot_w64(seq_items > 0);
         }
         at = __builtin_ctzll(rest);
@@ -742,6 +770,7 @@ size_t attention_workspace(const AttentionArgs& a, int kind) {
 
 hipError_t launch_attention(AttentionArgs a, int kind, int dtype, void* workspace, hipStream_t stream) {
     const Shape s = plan(a, kind);
+    a.group = a.Hq / a.H;
     a.counters = static_cast<uint32_t*>(workspace);
     a.partials = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + kCounterRegionBytes);
     if (kind == 0) return dtype == 0 ? launch<0, 0>(a, s, stream) : launch<1, 0>(a, s, stream);

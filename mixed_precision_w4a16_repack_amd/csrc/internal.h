@@ -195,7 +195,8 @@ struct AttentionArgs {
     int64_t window = 0;
     int Hq = 0, H = 0, D = 0, P = 0;
     float scale = 0.0f;
-    uint32_t* counters = nullptr;  // set by launch_attention
+    int group = 0;                 // the rest is set by launch_attention: Hq / H, the workspace's parts
+    uint32_t* counters = nullptr;
     float* partials = nullptr;
 };
 // Bytes of workspace: the counter region, then the partial results of heads
