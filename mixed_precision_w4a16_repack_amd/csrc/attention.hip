@@ -41,8 +41,10 @@ namespace {
 constexpr int kWaves = 4;
 constexpr int kTile = 32;              // tokens
 constexpr int kMinTiles = 16;          // least tiles per workgroup when a head is split
-constexpr int kFan = 16;               // partial results joined by one workgroup ...
-constexpr int kBatch = 8;              // ... with the loads of this many in flight
+constexpr int kHeadBytes = 80 << 10;   // a head's start and end cost a workgroup about as much as reading this
+constexpr int kFan = 8;                // partial results joined at once (their loads are in flight together)
+constexpr int kChunkBits = 24;         // a sum over sequences: slots << kChunkBits | chunks, the latter cut to kChunkMost a lane
+constexpr int64_t kChunkMask = ((int64_t)1 << kChunkBits) - 1, kChunkMost = 1 << 16;
 constexpr float kLowest = -3.402823466e38f;
 
 typedef u32x4 u32x4_any __attribute__((aligned(2)));
@@ -51,7 +53,7 @@ typedef u32x2 u32x2_any __attribute__((aligned(2)));
 
 // How many workgroups of each kernel share a CU (registers allow that many).
 template <int KIND, int D, int HT>
-constexpr int kPerCU = HT == 2 ? (D > 128 ? 1 : 2) : (KIND == 1 ? (D > 128 ? 2 : 3) : (D > 128 ? 1 : (D == 64 ? 3 : 2)));
+constexpr int kPerCU = HT == 2 || D > 192 || (KIND == 0 && D > 128) ? 1 : 2;
 
 // What is left of the references in fp16 (2^13 * 2^2 < 65504).
 template <bool F16P>
@@ -118,10 +120,12 @@ __device__ __forceinline__ void issue_fence() {
     __builtin_amdgcn_sched_barrier(0);
 }
 
-// a / b of non-negative numbers, mostly small.
-__device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {
-    if (((uint64_t)a | (uint64_t)b) >> 32 == 0) return (uint32_t)a / (uint32_t)b;
-    return a / b;
+// a / b of non-negative numbers below 2^53 whose quotient is below 2^20: the
+// product is off by less than 1 before it is cut.
+__device__ __forceinline__ int divide(int64_t a, int64_t b) {
+    const int q = (int)((double)a * __builtin_amdgcn_rcp((double)b));
+    const int64_t r = a - q * b;
+    return r < 0 ? q - 1 : (r >= b ? q + 1 : q);
 }
 
 // What a sequence of a length sees: tokens lo .. n - 1, in the tiles
@@ -129,17 +133,20 @@ __device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {
 struct Span {
     int n, lo, first, count;
     __device__ __forceinline__ Span(const AttentionArgs& a, int length) {
-        const int64_t most = a.width * a.P;
-        const int64_t len = length < 0 ? 0 : (length > most ? most : length);
-        n = (int)len;
-        lo = a.window > 0 && len > a.window ? (int)(len - a.window) : 0;
+        n = length < 0 ? 0 : (length > a.most ? a.most : length);
+        lo = n > a.reach ? n - a.reach : 0;
         first = lo / kTile;
         count = n > lo ? (n - 1) / kTile + 1 - first : 0;
     }
 };
 
+// What a head of n tiles counts for in the two ways to divide the work.
+__device__ __forceinline__ int chunks_of(int n) { return (n + kMinTiles - 1) / kMinTiles; }
+
 template <int DT, int KIND, int D, int HT>
 struct Attend {
+    static constexpr int kHeadCost = kHeadBytes / (kTile * D * (KIND == 1 ? 2 : 4));  // in tiles
+    static __device__ __forceinline__ int slots_of(int n) { return n > 0 ? n + kHeadCost : 0; }
     static constexpr bool kI8 = KIND == 1;
     static constexpr bool kF16P = kI8 || DT == 0;
     static constexpr int PDT = kF16P ? 0 : 1;             // operand type of both products
@@ -220,7 +227,7 @@ struct Attend {
     __device__ __forceinline__ void load_keys(const unsigned char* rec, int sub, int unit) {
         const u32x4* p = reinterpret_cast<const u32x4*>(rec + (int64_t)sub * NL * 1024) + unit;
 #pragma unroll
-        for (int i = 0; i < NL; ++i) kb[i] = p[64 * i];
+        for (int i = 0; i < NL; ++i) kb[i] = __builtin_nontemporal_load(p + 64 * i);
     }
     __device__ __forceinline__ void load_values(const unsigned char* rec, int sub, int unit) {
         if constexpr (kI8) {  // first: they are needed first
@@ -234,7 +241,7 @@ struct Attend {
         }
         const u32x4* p = reinterpret_cast<const u32x4*>(rec + L::keys_bytes(D, a.P) + (int64_t)sub * NL * 1024) + unit;
 #pragma unroll
-        for (int i = 0; i < NL; ++i) vb[i] = p[64 * i];
+        for (int i = 0; i < NL; ++i) vb[i] = __builtin_nontemporal_load(p + 64 * i);
     }
 
     // s[h][0..3]: tokens 4g .. 4g+3 of the tile, s[h][4..7]: 16 tokens on.
@@ -481,13 +488,6 @@ struct Attend {
 struct Join {
     float m = kLowest, l = 0.0f;
     floatx4 o{0.0f, 0.0f, 0.0f, 0.0f};
-    __device__ __forceinline__ void rescale(float mn) {
-        const float keep = exp2_fast(m - mn);
-        l *= keep;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) o[r] *= keep;
-        m = mn;
-    }
     __device__ __forceinline__ void add(float pm, float pl, const floatx4& po) {
         const float w = exp2_fast(pm - m);
         l += w * pl;
@@ -514,7 +514,7 @@ template <int D, int HT>
 struct Partial {
     static constexpr int kStride = D + 4;
     static constexpr int64_t kFloats = 16 * HT * kStride;
-    static __device__ __forceinline__ float* at(float* ws, int64_t wg, int slot) { return ws + (2 * wg + slot) * kFloats; }
+    static __device__ __forceinline__ float* at(float* ws, int wg, int slot) { return ws + (2 * wg + slot) * kFloats; }
 };
 
 template <int DT, int KIND, int D, int HT>
@@ -525,81 +525,83 @@ __global__ __launch_bounds__(256, (kPerCU<KIND, D, HT>)) void attention_kernel(A
     __shared__ int s_last;
     A w(a);
     const int lane = w.lane;
-    const int64_t wg = blockIdx.x, wgs = gridDim.x;
+    const int wg = blockIdx.x, wgs = gridDim.x;
     const int group = a.group;
     const int head_tiles = (group + A::kCols - 1) / A::kCols;
     const int units = a.H * head_tiles;  // of one sequence
 
     // Every wave finds the workgroup's share by itself: lane i sums the
-    // sequences [i * run, (i + 1) * run).
+    // sequences [i * run, (i + 1) * run), slots above the chunks (which need
+    // only be told from more than there are workgroups).
     const int64_t run = (a.B + 63) / 64;
-    int64_t tiles = 0, chunks = 0;
+    int64_t sums = 0;
     int length = 0;
-    for (int64_t b = lane * run; b < (lane + 1) * run && b < a.B; ++b) {
+    for (int64_t b = lane * run, e = b + run < a.B ? b + run : a.B; b < e; ++b) {
         length = a.lengths[b];
         const int n = Span(a, length).count;
-        tiles += n;
-        chunks += (n + kMinTiles - 1) / kMinTiles;
+        sums += (int64_t)A::slots_of(n) << kChunkBits;
+        if ((sums & kChunkMask) < kChunkMost) sums += chunks_of(n) < kChunkMost ? chunks_of(n) : kChunkMost;
     }
-    const int64_t tiles_to = wave_scan(tiles), chunks_to = wave_scan(chunks);
-    const int64_t all_tiles = units * read_lane(tiles_to, 63), all_chunks = units * read_lane(chunks_to, 63);
+    const int64_t sums_to = wave_scan(sums), all_sums = read_lane(sums_to, 63);
     // Sequences that see nothing.
     for (int64_t b = wg; b < a.B; b += wgs) {
         const int len = run == 1 ? __builtin_amdgcn_readlane(length, (int)b) : a.lengths[b];
         if (Span(a, len).count != 0) continue;
-        for (int i = threadIdx.x; i < a.Hq * D; i += 256) a.out[b * a.o_ts + (int64_t)(i / D) * a.o_hs + i % D] = 0;
+        uint16_t* out = a.out + b * a.o_ts;
+        for (int i = threadIdx.x; i < a.H * group * D; i += 256) out[(int64_t)(i / D) * a.o_hs + i % D] = 0;
     }
     // Few tiles: a workgroup per kMinTiles of one head, so that most heads
-    // need no join. Else equal runs of the list, across heads.
-    const bool by_chunk = all_chunks <= wgs;
-    const int64_t all = by_chunk ? all_chunks : all_tiles;
-    const int64_t per = by_chunk ? 1 : divide(all_tiles + wgs - 1, wgs);
+    // need no join. Else equal runs of the list, across heads; a head takes
+    // kHeadCost slots before its tiles' ones.
+    const bool by_chunk = units * (all_sums & kChunkMask) <= wgs;
+    const int64_t all = units * (by_chunk ? all_sums & kChunkMask : all_sums >> kChunkBits);
+    const int64_t per = by_chunk ? 1 : (all + wgs - 1) >> __builtin_ctz(wgs);
     int64_t pos = wg * per;
     const int64_t end = pos + per < all ? pos + per : all;
     if (pos >= end) return;
-    const int64_t begin = pos;
 
     // The block of 64 sequences that holds `pos`, and in it the sequence.
-    const int64_t to = by_chunk ? chunks_to : tiles_to, of = by_chunk ? chunks : tiles;
-    int at = __builtin_ctzll(__builtin_amdgcn_ballot_w64(units * to > pos));
-    int64_t base = at * run, before = read_lane(to - of, at);  // items of the sequences before `base`
-    int64_t seq_items = of, seq_to = to;                       // of sequence base + lane, when base is found
-    if (run == 1) {
-        base = 0;
-        before = 0;
-    } else {
-        for (;;) {
-            length = base + lane < a.B ? a.lengths[base + lane] : 0;
-            const int n = Span(a, length).count;
-            seq_items = by_chunk ? (n + kMinTiles - 1) / kMinTiles : n;
-            seq_to = before + wave_scan(seq_items);
-            if (units * read_lane(seq_to, 63) > pos) break;
-            before = read_lane(seq_to, 63);
-            base += 64;
-        }
-        at = __builtin_ctzll(__builtin_amdgcn_ballot_w64(units * seq_to > pos));
+    int64_t seq_items = by_chunk ? sums & kChunkMask : sums >> kChunkBits;  // of sequence base + lane, when base is found
+    int64_t seq_to = by_chunk ? sums_to & kChunkMask : sums_to >> kChunkBits;
+    int64_t base = 0;
+    auto block_at = [&](int64_t first, int64_t before) {  // `before`: items of the sequences before it
+        base = first;
+        length = base + lane < a.B ? a.lengths[base + lane] : 0;
+        const int n = Span(a, length).count;
+        seq_items = by_chunk ? chunks_of(n) : A::slots_of(n);
+        seq_to = before + wave_scan(seq_items);
+    };
+    if (run > 1) {
+        const int at = __builtin_ctzll(__builtin_amdgcn_ballot_w64(units * seq_to > pos));
+        block_at(at * run, read_lane(seq_to - seq_items, at));
+        while (units * read_lane(seq_to, 63) <= pos) block_at(base + 64, read_lane(seq_to, 63));
     }
+    int at = __builtin_ctzll(__builtin_amdgcn_ballot_w64(units * seq_to > pos));
 
     while (pos < end) {
         // Sequence b = base + at; its items start at seq_begin.
         const int64_t b = base + at;
-        const int64_t items = read_lane(seq_items, at);  // of one unit
-        const int64_t seq_end = units * read_lane(seq_to, at), seq_begin = seq_end - units * items;
+        const int items = (int)read_lane(seq_items, at);  // of one unit
+        const int64_t seq_end = units * read_lane(seq_to, at), seq_begin = seq_end - (int64_t)units * items;
         const Span sp(a, __builtin_amdgcn_readlane(length, at));
-        int unit = (int)divide(pos - seq_begin, items);
+        int unit = divide(pos - seq_begin, items);
         for (; pos < end && pos < seq_end; ++unit) {
-            const int64_t unit_begin = seq_begin + unit * items, unit_end = unit_begin + items;
+            const int64_t unit_begin = seq_begin + (int64_t)unit * items, unit_end = unit_begin + items;
             const int64_t stop = unit_end < end ? unit_end : end;
             int from = (int)(pos - unit_begin), upto = (int)(stop - unit_begin);
+            pos = stop;
             if (by_chunk) {
                 from *= kMinTiles;
                 upto = upto * kMinTiles < sp.count ? upto * kMinTiles : sp.count;
+            } else {
+                from = from > A::kHeadCost ? from - A::kHeadCost : 0;
+                upto -= A::kHeadCost;
+                if (upto <= 0) break;  // the head's tiles begin in the next workgroup
             }
-            const bool whole = pos == unit_begin && stop == unit_end;
+            const bool whole = from == 0 && upto == sp.count;
             const int kv_head = head_tiles == 1 ? unit : unit / head_tiles, head_tile = unit - kv_head * head_tiles;
             const int head0 = kv_head * group + head_tile * A::kCols;
             const int heads = group - head_tile * A::kCols < A::kCols ? group - head_tile * A::kCols : A::kCols;
-            pos = stop;
 
             w.load_query(b, head0, heads);
             w.run(b, kv_head, sp, sp.first + from, sp.first + upto);
@@ -607,7 +609,7 @@ __global__ __launch_bounds__(256, (kPerCU<KIND, D, HT>)) void attention_kernel(A
             w.to_lds(lds, heads);
             __syncthreads();
             const float* ml = lds + kWaves * heads * A::kLd;
-            const int slot = unit_begin >= begin ? 1 : 0;
+            const int slot = from == 0 ? 1 : 0;
             for (int e = threadIdx.x; e < heads * (D / 4); e += 256) {
                 const int head = e / (D / 4), d = e % (D / 4) * 4;
                 Join j;
@@ -630,15 +632,14 @@ __global__ __launch_bounds__(256, (kPerCU<KIND, D, HT>)) void attention_kernel(A
             if (whole) continue;
 
             // Join: of kFan workgroups, by the last of them; then of those results.
-            const int64_t first = by_chunk ? wg - (from / kMinTiles) : divide(unit_begin, per);
-            const int64_t last = by_chunk ? first + items - 1 : divide(unit_end - 1, per);
-            int64_t rank = wg - first, count = last - first + 1, step = 1;
+            const int first = by_chunk ? wg - from / kMinTiles : divide(unit_begin + A::kHeadCost, per);
+            const int last = by_chunk ? first + items - 1 : divide(unit_end - 1, per);
+            int rank = wg - first, count = last - first + 1, step = 1;
             uint32_t* counters = a.counters;
             for (int level = 0;; ++level) {
-                const int64_t lead = rank / kFan * kFan;
-                const int size = (int)(count - lead < kFan ? count - lead : kFan);
-                const int64_t lead_wg = first + lead * step;
-                const int lead_slot = lead == 0 ? 1 : 0;
+                const int lead = rank / kFan * kFan;
+                const int size = count - lead < kFan ? count - lead : kFan;
+                const int lead_wg = first + lead * step, lead_slot = lead == 0 ? 1 : 0;
                 wait_vector_memory();
                 __syncthreads();
                 if (threadIdx.x == 0) {
@@ -651,34 +652,31 @@ __global__ __launch_bounds__(256, (kPerCU<KIND, D, HT>)) void attention_kernel(A
                 const bool mine = s_last != 0;
                 if (!mine) break;
                 const bool done = count <= kFan;
+                const int pair = level & 1 ? 2 : 0;
                 for (int e = threadIdx.x; e < heads * (D / 4); e += 256) {
                     const int head = e / (D / 4), d = e % (D / 4) * 4;
+                    float* lead_p = Pt::at(a.partials, lead_wg, lead_slot) + head * Pt::kStride;
+                    const float* p = Pt::at(a.partials, lead_wg, 0) + head * Pt::kStride;
+                    float2 pml[kFan];
+                    floatx4 po[kFan];
                     Join j;
-#pragma unroll 1
-                    for (int i0 = 0; i0 < size; i0 += kBatch) {
-                        float2 pml[kBatch];
-                        floatx4 po[kBatch];
 #pragma unroll
-                        for (int i = 0; i < kBatch; ++i) {
-                            const int r = i0 + i < size ? i0 + i : i0;
-                            const float* p = Pt::at(a.partials, lead_wg + r * step, lead == 0 && r == 0 ? 1 : 0) + head * Pt::kStride;
-                            pml[i] = load_coherent2(p + (level & 1 ? 2 : 0));
-                            po[i] = load_coherent(p + 4 + d);
-                        }
-                        float mn = j.m;
-#pragma unroll
-                        for (int i = 0; i < kBatch; ++i) mn = fmaxf(mn, pml[i].x);
-                        j.rescale(mn);
-#pragma unroll
-                        for (int i = 0; i < kBatch; ++i)
-                            if (i0 + i < size) j.add(pml[i].x, pml[i].y, po[i]);
+                    for (int i = 0; i < kFan; ++i) {
+                        const float* pi = i == 0 ? lead_p : p;
+                        pml[i] = load_coherent2(pi + pair);
+                        po[i] = load_coherent(pi + 4 + d);
+                        if (i + 1 < size) p += 2 * Pt::kFloats * step;
                     }
+#pragma unroll
+                    for (int i = 0; i < kFan; ++i) j.m = fmaxf(j.m, pml[i].x);
+#pragma unroll
+                    for (int i = 0; i < kFan; ++i)
+                        if (i < size) j.add(pml[i].x, pml[i].y, po[i]);
                     if (done) {
                         store_out<DT>(a, b, head0 + head, d, j);
                     } else {  // in the leader's place
-                        float* p = Pt::at(a.partials, lead_wg, lead_slot) + head * Pt::kStride;
-                        store_coherent(p + 4 + d, j.o);
-                        if (d == 0) store_coherent2(p + (level & 1 ? 0 : 2), j.m, j.l);
+                        store_coherent(lead_p + 4 + d, j.o);
+                        if (d == 0) store_coherent2(lead_p + (2 - pair), j.m, j.l);
                     }
                 }
                 if (done) break;
@@ -692,12 +690,7 @@ __global__ __launch_bounds__(256, (kPerCU<KIND, D, HT>)) void attention_kernel(A
         if (pos >= end) break;
         uint64_t rest = at < 63 ? __builtin_amdgcn_ballot_w64(seq_items > 0) >> (at + 1) << (at + 1) : 0;
         while (rest == 0) {
-            before = read_lane(seq_to, 63);
-            base += 64;
-            length = base + lane < a.B ? a.lengths[base + lane] : 0;
-            const int n = Span(a, length).count;
-            seq_items = by_chunk ? (n + kMinTiles - 1) / kMinTiles : n;
-            seq_to = before + wave_scan(seq_items);
+            block_at(base + 64, read_lane(seq_to, 63));
             rest = __builtin_amdgcn_ballot_w64(seq_items > 0);
         }
         at = __builtin_ctzll(rest);
@@ -771,6 +764,9 @@ size_t attention_workspace(const AttentionArgs& a, int kind) {
 hipError_t launch_attention(AttentionArgs a, int kind, int dtype, void* workspace, hipStream_t stream) {
     const Shape s = plan(a, kind);
     a.group = a.Hq / a.H;
+    const int64_t most = a.width * a.P, all = ((int64_t)1 << 31) - 1;
+    a.most = (int)(most < all ? most : all);
+    a.reach = (int)(a.window > 0 && a.window < all ? a.window : all);
     a.counters = static_cast<uint32_t*>(workspace);
     a.partials = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + kCounterRegionBytes);
     if (kind == 0) return dtype == 0 ? launch<0, 0>(a, s, stream) : launch<1, 0>(a, s, stream);

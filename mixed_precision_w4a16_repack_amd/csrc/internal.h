@@ -195,7 +195,9 @@ struct AttentionArgs {
     int64_t window = 0;
     int Hq = 0, H = 0, D = 0, P = 0;
     float scale = 0.0f;
-    int group = 0;                 // the rest is set by launch_attention: Hq / H, the workspace's parts
+    // Set by launch_attention: Hq / H, the longest length the table allows, the
+    // window as a number of tokens, the workspace's parts.
+    int group = 0, most = 0, reach = 0;
     uint32_t* counters = nullptr;
     float* partials = nullptr;
 };

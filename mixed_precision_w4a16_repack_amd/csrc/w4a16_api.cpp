@@ -656,6 +656,10 @@ w4a16_status check_attention(int64_t B, int32_t q_heads, int32_t kv_heads, int32
         return fail(W4A16_ERR_UNSUPPORTED, "B=%lld sequences of q_heads=%d are too large for one launch", (long long)B, q_heads);
     if (table_width > (((int64_t)1 << 31) + page_size - 1) / page_size)
         return fail(W4A16_ERR_UNSUPPORTED, "table_width=%lld pages hold more than 2^31 tokens", (long long)table_width);
+    // Bounds the sums over sequences that the kernel packs.
+    if (B > 0 && table_width > ((int64_t)1 << 43) / page_size / B)
+        return fail(W4A16_ERR_UNSUPPORTED, "a table of B=%lld rows of %lld pages holds more than 2^43 tokens", (long long)B,
+                    (long long)table_width);
     return W4A16_OK;
 }
 

@@ -221,6 +221,7 @@ def _attention(lib, **kw):
     (dict(dtype=2), INVALID, "dtype=2"),
     (dict(width=-1), INVALID, "table_width=-1"),
     (dict(width=1 << 26, ld=1 << 26), UNSUPPORTED, "more than 2^31 tokens"),
+    (dict(B=1 << 20, width=1 << 20, ld=1 << 20), UNSUPPORTED, "more than 2^43 tokens"),
     (dict(ld=1), INVALID, "table_ld=1 must be >= table_width=2"),
     (dict(window=-5), INVALID, "window=-5"),
     (dict(B=1 << 28), UNSUPPORTED, "too large for one launch"),
