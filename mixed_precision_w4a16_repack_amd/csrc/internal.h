@@ -178,7 +178,9 @@ struct KvArgs {
     unsigned char* cache = nullptr;
     int64_t pages = 0;
     int H = 0, D = 0, P = 0;  // kv heads, head size, tokens per page
+    int shift = 0;            // set by the launch: log2(P), or -1
 };
+constexpr int kKvMaxD = 256;  // largest head size
 int64_t kv_workgroups(int64_t T, int64_t H);  // of launch_kv_write and launch_kv_read
 hipError_t launch_kv_write(const KvArgs& a, int kind, int dtype, hipStream_t stream);
 hipError_t launch_kv_read(const KvArgs& a, int kind, int dtype, hipStream_t stream);

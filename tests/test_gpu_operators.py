@@ -296,6 +296,51 @@ def test_cache_write_places_and_read(H, D, P, T, order, kind, dtype):
     assert torch.equal(rk.cpu()[keep], want_k) and torch.equal(rv.cpu()[keep], want_v)
 
 
+@pytest.mark.parametrize("T", [3, 200])
+def test_cache_int8_rows_with_a_nan_keep_it(T):
+    H, D, P, dt = 2, 64, 32, torch.bfloat16
+    g = gen("cache nan", T)
+    k, v = randn(g, T, H, D, dtype=dt), randn(g, T, H, D, dtype=dt)
+    k[1, 0, 7] = float("nan")
+    v[2, 1, 63] = float("nan")
+    pages = -(-T // P)
+    cache = torch.zeros(w4.kv_cache_size(pages, H, D, P, ref.KV_INT8), dtype=torch.uint8, device=DEV)
+    slots = torch.arange(T, device=DEV)
+    w4.kv_write(k.to(DEV), v.to(DEV), slots, cache, pages, P, ref.KV_INT8)
+    rk, rv = w4.kv_read(slots, cache, pages, H, D, P, ref.KV_INT8, dt)
+    for got, x in ((rk.cpu(), k), (rv.cpu(), v)):
+        assert torch.equal(got.isnan().all(-1), x.isnan().any(-1)) and torch.equal(got.isnan().any(-1), x.isnan().any(-1))
+
+
+@pytest.mark.parametrize("kind", [ref.KV_ACT, ref.KV_INT8])
+@pytest.mark.parametrize("start", [0, 1, 2, 3, 4, 30, 64])
+def test_cache_prompts_that_start_inside_a_tile(start, kind):
+    """A ragged batch of prompts in one call: runs that begin anywhere in a tile and end inside a group of 32 tokens."""
+    H, D, P, dt = 3, 128, 64, torch.float16
+    lens = [33, 100, 5, 64, 31, 200]
+    g = gen("ragged prompts", start, kind)
+    T = sum(lens)
+    pages = sum(-(-(n + start) // P) for n in lens) + 1
+    order, slots, at = torch.randperm(pages, generator=g), [], 0
+    for n in lens:
+        t = torch.arange(n) + start
+        slots.append(order[at + t // P] * P + t % P)
+        at += -(-(n + start) // P)
+    slots = torch.cat(slots)
+    k, v = randn(g, T, H, D, dtype=dt), randn(g, T, H, D, dtype=dt)
+    fill = torch.randint(0, 256, (w4.kv_cache_size(pages, H, D, P, kind),), generator=g, dtype=torch.uint8)
+    cache, whole = fill.to(DEV), fill.to(DEV)
+    w4.kv_write(k.to(DEV), v.to(DEV), slots.to(DEV), cache, pages, P, kind)
+    for i in range(0, T, 50):  # the same by few tokens at a time
+        w4.kv_write(k[i : i + 50].to(DEV), v[i : i + 50].to(DEV), slots[i : i + 50].to(DEV), whole, pages, P, kind)
+    assert torch.equal(cache, whole)
+    rk, rv = w4.kv_read(slots.to(DEV), cache, pages, H, D, P, kind, dt)
+    sk, sv = zip(*(w4.kv_read(slots[i : i + 50].to(DEV), cache, pages, H, D, P, kind, dt) for i in range(0, T, 50)))
+    assert torch.equal(rk, torch.cat(sk)) and torch.equal(rv, torch.cat(sv))
+    if kind == ref.KV_ACT:
+        assert torch.equal(rk.cpu(), k) and torch.equal(rv.cpu(), v)
+
+
 def test_cache_offsets_past_32_bits():
     """A cache of more than 4 GiB: slots at its end are written, read and attended."""
     H, D, P, kind, dt = 8, 128, 64, ref.KV_ACT, torch.float16
