@@ -42,6 +42,7 @@ __device__ __forceinline__ uint32_t lanes_top(uint32_t v, int step) {
 // scales whose reciprocal nears fp32's ends take the division itself.
 struct Coder {
     float s, inv;
+    Coder() = default;
     __device__ __forceinline__ explicit Coder(float scale) : s(scale), inv(scale > 1e-36f && scale < 1e36f ? 1.0f / scale : 0.0f) {}
     __device__ __forceinline__ uint32_t operator()(float x) const {
         float q = x * inv;
@@ -144,7 +145,7 @@ __device__ __forceinline__ uint32_t highs(uint32_t x, uint32_t y) { return __bui
 template <int DT, int KIND, int D>
 __global__ __launch_bounds__(256) void kv_write_tile_kernel(KvArgs a) {
     using L = KvPlace<KIND>;
-    __shared__ float s_scale[32];  // int8: of the values
+    __shared__ Coder s_code[32];  // int8: of the values
     const int64_t t0 = (int64_t)(blockIdx.x / a.H) * 32;
     const int h = blockIdx.x % a.H;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -198,7 +199,7 @@ __global__ __launch_bounds__(256) void kv_write_tile_kernel(KvArgs a) {
                     }
                 }
             }
-            if (!keys && g == 0) s_scale[j] = s;
+            if (!keys && g == 0) s_code[j] = code;
         }
         if (keys) return;
         __syncthreads();
@@ -226,24 +227,21 @@ __global__ __launch_bounds__(256) void kv_write_tile_kernel(KvArgs a) {
                 out[1] = hi;
             }
         } else {
-            for (int i = threadIdx.x; i < 4 * (D / 4); i += 256) {
-                const int tg = i / (D / 4), c = i % (D / 4), d = c / 8 * 32 + c % 8 * 2;
-                uint32_t w[16];
+            for (int i = threadIdx.x; i < 4 * (D / 2); i += 256) {
+                const int tg = i / (D / 2), d = i % (D / 2) * 2;
+                uint32_t w[8];
 #pragma unroll
-                for (int j = 0; j < 16; ++j) w[j] = pair_at(j % 8 / 4 * 16 + 4 * tg + j % 4, d + j / 8 * 16);
-                u32x4 lo{0u, 0u, 0u, 0u}, hi{0u, 0u, 0u, 0u};
+                for (int j = 0; j < 8; ++j) w[j] = pair_at(j / 4 * 16 + 4 * tg + j % 4, d);
+                u32x2 lo{0u, 0u}, hi{0u, 0u};
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    const Coder code(s_scale[j / 4 * 16 + 4 * tg + j % 4]);
-#pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        lo[2 * half + j / 4] |= code(low<DT>(w[8 * half + j])) << (8 * (j % 4));
-                        hi[2 * half + j / 4] |= code(high<DT>(w[8 * half + j])) << (8 * (j % 4));
-                    }
+                    const Coder code = s_code[j / 4 * 16 + 4 * tg + j % 4];
+                    lo[j / 4] |= code(low<DT>(w[j])) << (8 * (j % 4));
+                    hi[j / 4] |= code(high<DT>(w[j])) << (8 * (j % 4));
                 }
-                u32x4* out = reinterpret_cast<u32x4*>(rec + L::value(t + 4 * tg, d, D, a.P));
-                out[0] = lo;
-                out[1] = hi;
+                unsigned char* out = rec + L::value(t + 4 * tg, d, D, a.P);
+                *reinterpret_cast<u32x2*>(out) = lo;
+                *reinterpret_cast<u32x2*>(out + 16) = hi;
             }
         }
         return;
@@ -265,7 +263,7 @@ __global__ __launch_bounds__(256) void kv_write_tile_kernel(KvArgs a) {
         if constexpr (KIND == 1) {  // codes in the low bytes of the two halves
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const Coder code(s_scale[(j0 + j) & 31]);
+                const Coder code = s_code[(j0 + j) & 31];
                 w[j] = code(low<DT>(w[j])) | code(high<DT>(w[j])) << 16;
             }
         }
