@@ -18,6 +18,7 @@ decoder layer's GEMMs: ``rmsnorm``, ``silu_mul`` (and their int8 forms
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -96,6 +97,8 @@ _lock = threading.Lock()
 def load_library(path: str = LIB_PATH):
     """Load libw4a16.so (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(path):
@@ -126,11 +129,12 @@ def _check(status: int):
 
 
 def _stream(t: torch.Tensor):
-    return ctypes.c_void_p(torch.cuda.current_stream(t.device).cuda_stream)
+    # the handle of torch.cuda.current_stream(t.device), without building the object
+    return torch._C._cuda_getCurrentRawStream(t.get_device())
 
 
 def _ptr(t: torch.Tensor | None):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _need_cuda(name: str, t: torch.Tensor | None, dtype=None):
@@ -268,7 +272,8 @@ def _default_workspace(device, kind: str = "w4a16") -> Workspace:
     w4a16_gemm and w4a8_gemm get separate ones: w4a16_gemm needs the counter
     region at the start of its workspace to be zero, and w4a8_gemm writes its
     partial results from the start of its own."""
-    key = (kind, torch.device(device).index, torch.cuda.current_stream(device).cuda_stream)
+    index = torch.device(device).index
+    key = (kind, index, torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if index is None else index))
     ws = _workspaces.get(key)
     if ws is None:
         ws = _workspaces[key] = Workspace(device)
@@ -433,22 +438,35 @@ def _same_device(first: torch.Tensor, **others: torch.Tensor | None):
             raise ValueError(f"{name} is on {t.device}, expected {first.device}")
 
 
-def _rows(name: str, t: torch.Tensor | None, M: int, K: int, dtype):
-    if t is None:
+# The operators between the GEMMs are often shorter than their checks, so each
+# argument is first compared as a whole; only one that does not fit is looked
+# at again, for the message.
+
+
+def _fits(t: torch.Tensor, shape, dtype, device) -> bool:
+    return t.dtype is dtype and t.shape == shape and t.device == device and t.stride(-1) == 1
+
+
+def _rows(name: str, t: torch.Tensor | None, x: torch.Tensor, M: int, K: int):
+    """t must be [M, K] rows of x's dtype on its device."""
+    if t is None or _fits(t, (M, K), x.dtype, x.device):
         return
-    _need_cuda(name, t, dtype)
+    _need_cuda(name, t, x.dtype)
     if tuple(t.shape) != (M, K) or t.stride(1) != 1:
         raise ValueError(f"{name} must be [M={M}, K={K}] with unit column stride, got {tuple(t.shape)} {t.stride()}")
+    _same_device(x, **{name: t})
 
 
 def _ld(t: torch.Tensor | None) -> int:
     """Row stride of [M, K] rows (torch gives a single row any stride)."""
     if t is None:
         return 0
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+    ld = t.stride(0)
+    return ld if t.shape[0] > 1 else max(ld, t.shape[1])
 
 
-def _codes_out(out, M: int, K: int, device):
+def _codes_out(out, x: torch.Tensor, M: int, K: int):
+    device = x.device
     if out is None:
         return (torch.empty((M, K), dtype=torch.int8, device=device),
                 torch.empty((M,), dtype=torch.float32, device=device))
@@ -457,20 +475,23 @@ def _codes_out(out, M: int, K: int, device):
     _need_cuda("xs", xs, torch.float32)
     if tuple(qa.shape) != (M, K) or qa.stride(1) != 1 or xs.shape != (M,) or not xs.is_contiguous():
         raise ValueError(f"out must be (qa [M={M}, K={K}] with unit column stride, contiguous xs [M={M}])")
+    _same_device(x, qa=qa, xs=xs)
     return qa, xs
 
 
 def _norm_args(x, weight, residual, residual_out):
-    _need_cuda("x", x, (torch.float16, torch.bfloat16))
+    if not x.is_cuda or x.dtype not in _DTYPE_CODE:
+        _need_cuda("x", x, (torch.float16, torch.bfloat16))
     if x.dim() != 2 or x.stride(1) != 1:
         raise ValueError("x must be 2-D with unit column stride")
     M, K = x.shape
-    _need_cuda("weight", weight, x.dtype)
-    if tuple(weight.shape) != (K,) or not weight.is_contiguous():
-        raise ValueError(f"weight must be a contiguous [K={K}] tensor")
-    _rows("residual", residual, M, K, x.dtype)
-    _rows("residual_out", residual_out, M, K, x.dtype)
-    _same_device(x, weight=weight, residual=residual, residual_out=residual_out)
+    if not _fits(weight, (K,), x.dtype, x.device):
+        _need_cuda("weight", weight, x.dtype)
+        if tuple(weight.shape) != (K,) or not weight.is_contiguous():
+            raise ValueError(f"weight must be a contiguous [K={K}] tensor")
+        _same_device(x, weight=weight)
+    _rows("residual", residual, x, M, K)
+    _rows("residual_out", residual_out, x, M, K)
     return M, K
 
 
@@ -482,11 +503,11 @@ def rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-5, residual: 
     M, K = _norm_args(x, weight, residual, residual_out)
     if out is None:
         out = torch.empty((M, K), dtype=x.dtype, device=x.device)
-    _rows("out", out, M, K, x.dtype)
-    _same_device(x, out=out)
+    else:
+        _rows("out", out, x, M, K)
     _check(load_library().w4a16_rmsnorm(
-        _ptr(x), M, K, _ld(x), _DTYPE_CODE[x.dtype], _ptr(weight), eps, _ptr(residual), _ld(residual),
-        _ptr(residual_out), _ld(residual_out), _ptr(out), _ld(out), _stream(x)))
+        x.data_ptr(), M, K, _ld(x), _DTYPE_CODE[x.dtype], weight.data_ptr(), eps, _ptr(residual), _ld(residual),
+        _ptr(residual_out), _ld(residual_out), out.data_ptr(), _ld(out), _stream(x)))
     return out
 
 
@@ -494,16 +515,16 @@ def rmsnorm_a8(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-5, residua
                residual_out: torch.Tensor | None = None, out: tuple[torch.Tensor, torch.Tensor] | None = None):
     """``rmsnorm`` as the input of ``gemm_w4a8``: (qa [M, K] int8, xs [M] fp32), as ``quantize_a8`` stores them."""
     M, K = _norm_args(x, weight, residual, residual_out)
-    qa, xs = _codes_out(out, M, K, x.device)
-    _same_device(x, qa=qa, xs=xs)
+    qa, xs = _codes_out(out, x, M, K)
     _check(load_library().w4a8_rmsnorm(
-        _ptr(x), M, K, _ld(x), _DTYPE_CODE[x.dtype], _ptr(weight), eps, _ptr(residual), _ld(residual),
-        _ptr(residual_out), _ld(residual_out), _ptr(qa), _ld(qa), _ptr(xs), _stream(x)))
+        x.data_ptr(), M, K, _ld(x), _DTYPE_CODE[x.dtype], weight.data_ptr(), eps, _ptr(residual), _ld(residual),
+        _ptr(residual_out), _ld(residual_out), qa.data_ptr(), _ld(qa), xs.data_ptr(), _stream(x)))
     return qa, xs
 
 
 def _gate_args(x):
-    _need_cuda("x", x, (torch.float16, torch.bfloat16))
+    if not x.is_cuda or x.dtype not in _DTYPE_CODE:
+        _need_cuda("x", x, (torch.float16, torch.bfloat16))
     if x.dim() != 2 or x.stride(1) != 1 or x.shape[1] % 2:
         raise ValueError(f"x must be [M, 2*K] with unit column stride, got {tuple(x.shape)} {x.stride()}")
     return x.shape[0], x.shape[1] // 2
@@ -514,19 +535,19 @@ def silu_mul(x: torch.Tensor, out: torch.Tensor | None = None) -> torch.Tensor:
     M, K = _gate_args(x)
     if out is None:
         out = torch.empty((M, K), dtype=x.dtype, device=x.device)
-    _rows("out", out, M, K, x.dtype)
-    _same_device(x, out=out)
-    _check(load_library().w4a16_silu_mul(_ptr(x), M, K, _ld(x), _DTYPE_CODE[x.dtype], _ptr(out), _ld(out), _stream(x)))
+    else:
+        _rows("out", out, x, M, K)
+    _check(load_library().w4a16_silu_mul(x.data_ptr(), M, K, _ld(x), _DTYPE_CODE[x.dtype], out.data_ptr(), _ld(out),
+                                         _stream(x)))
     return out
 
 
 def silu_mul_a8(x: torch.Tensor, out: tuple[torch.Tensor, torch.Tensor] | None = None):
     """``silu_mul`` as the input of ``gemm_w4a8``: (qa [M, K] int8, xs [M] fp32)."""
     M, K = _gate_args(x)
-    qa, xs = _codes_out(out, M, K, x.device)
-    _same_device(x, qa=qa, xs=xs)
-    _check(load_library().w4a8_silu_mul(_ptr(x), M, K, _ld(x), _DTYPE_CODE[x.dtype], _ptr(qa), _ld(qa), _ptr(xs),
-                                        _stream(x)))
+    qa, xs = _codes_out(out, x, M, K)
+    _check(load_library().w4a8_silu_mul(x.data_ptr(), M, K, _ld(x), _DTYPE_CODE[x.dtype], qa.data_ptr(), _ld(qa),
+                                        xs.data_ptr(), _stream(x)))
     return qa, xs
 
 
@@ -537,15 +558,21 @@ def kv_cache_size(pages: int, kv_heads: int, head_dim: int, page_size: int, kind
     return int(out.value)
 
 
-def _heads(name: str, t: torch.Tensor, shape, dtype):
+def _heads(name: str, t: torch.Tensor, shape, dtype, device):
+    if _fits(t, shape, dtype, device):
+        return
     _need_cuda(name, t, dtype)
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
     if t.dim() != 3 or tuple(t.shape) != tuple(shape) or t.stride(2) != 1:
         raise ValueError(f"{name} must be {list(shape)} with unit stride in its last dimension, "
                          f"got {tuple(t.shape)} {t.stride()}")
 
 
-def _cache_bytes(cache: torch.Tensor) -> int:
-    _need_cuda("cache", cache)
+def _cache_bytes(cache: torch.Tensor, device) -> int:
+    if cache.device != device:
+        _need_cuda("cache", cache)
+        raise ValueError(f"cache is on {cache.device}, expected {device}")
     if not cache.is_contiguous():
         raise ValueError("cache must be contiguous")
     return cache.numel() * cache.element_size()
@@ -567,14 +594,16 @@ def kv_write(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, cache: torch
     T = _slots(slots)
     if k.dim() != 3:
         raise ValueError("k must be [T, kv_heads, head_dim]")
+    device, dtype = k.device, k.dtype
     H, D = k.shape[1:]
-    _heads("k", k, (T, H, D), k.dtype)
-    _heads("v", v, (T, H, D), k.dtype)
-    nbytes = _cache_bytes(cache)
-    _same_device(k, v=v, slots=slots, cache=cache)
+    _heads("k", k, (T, H, D), dtype, device)
+    _heads("v", v, (T, H, D), dtype, device)
+    nbytes = _cache_bytes(cache, device)
+    if slots.device != device:
+        _same_device(k, slots=slots)
     _check(load_library().w4a16_kv_write(
-        _ptr(k), k.stride(0), k.stride(1), _ptr(v), v.stride(0), v.stride(1), T, _ptr(slots), _ptr(cache), nbytes,
-        pages, H, D, page_size, kind, _DTYPE_CODE[k.dtype], _stream(k)))
+        k.data_ptr(), k.stride(0), k.stride(1), v.data_ptr(), v.stride(0), v.stride(1), T, slots.data_ptr(),
+        cache.data_ptr(), nbytes, pages, H, D, page_size, kind, _DTYPE_CODE[dtype], _stream(k)))
 
 
 def kv_read(slots: torch.Tensor, cache: torch.Tensor, pages: int, kv_heads: int, head_dim: int, page_size: int,
@@ -583,20 +612,21 @@ def kv_read(slots: torch.Tensor, cache: torch.Tensor, pages: int, kv_heads: int,
     T = _slots(slots)
     if dtype not in _DTYPE_CODE:
         raise ValueError(f"dtype {dtype} is not fp16 or bf16")
-    shape = (T, kv_heads, head_dim)
+    shape, device = (T, kv_heads, head_dim), slots.device
     if out is None:
-        out = (torch.empty(shape, dtype=dtype, device=slots.device), torch.empty(shape, dtype=dtype, device=slots.device))
-    k, v = out
-    _heads("k", k, shape, dtype)
-    _heads("v", v, shape, dtype)
-    nbytes = _cache_bytes(cache)
-    _same_device(slots, k=k, v=v, cache=cache)
+        k, v = torch.empty(shape, dtype=dtype, device=device), torch.empty(shape, dtype=dtype, device=device)
+    else:
+        k, v = out
+        _heads("k", k, shape, dtype, device)
+        _heads("v", v, shape, dtype, device)
+    nbytes = _cache_bytes(cache, device)
     _check(load_library().w4a16_kv_read(
-        _ptr(slots), T, _ptr(cache), nbytes, pages, kv_heads, head_dim, page_size, kind, _DTYPE_CODE[dtype],
-        _ptr(k), k.stride(0), k.stride(1), _ptr(v), v.stride(0), v.stride(1), _stream(slots)))
+        slots.data_ptr(), T, cache.data_ptr(), nbytes, pages, kv_heads, head_dim, page_size, kind, _DTYPE_CODE[dtype],
+        k.data_ptr(), k.stride(0), k.stride(1), v.data_ptr(), v.stride(0), v.stride(1), _stream(slots)))
     return k, v
 
 
+@functools.lru_cache(maxsize=4096)
 def attention_workspace_size(B: int, q_heads: int, kv_heads: int, head_dim: int, page_size: int, table_width: int,
                              window: int, kind: int) -> int:
     out = _SZ(0)
@@ -612,28 +642,37 @@ def attention(q: torch.Tensor, cache: torch.Tensor, table: torch.Tensor, lengths
 
     ``table`` [B, width] int32 holds each sequence's pages, ``lengths`` [B] int32 its tokens (the new one
     included); ``window`` > 0 sees only the last tokens; ``scale`` defaults to head_dim ** -0.5."""
-    _need_cuda("q", q, (torch.float16, torch.bfloat16))
+    if not q.is_cuda or q.dtype not in _DTYPE_CODE:
+        _need_cuda("q", q, (torch.float16, torch.bfloat16))
     if q.dim() != 3:
         raise ValueError("q must be [B, q_heads, head_dim]")
-    B, Hq, D = q.shape
-    _heads("q", q, (B, Hq, D), q.dtype)
+    B, Hq, D = shape = q.shape
+    device, dtype = q.device, q.dtype
+    _heads("q", q, shape, dtype, device)
     if out is None:
-        out = torch.empty((B, Hq, D), dtype=q.dtype, device=q.device)
-    _heads("out", out, (B, Hq, D), q.dtype)
-    _need_cuda("table", table, torch.int32)
-    _need_cuda("lengths", lengths, torch.int32)
+        out = torch.empty(shape, dtype=dtype, device=device)
+    else:
+        _heads("out", out, shape, dtype, device)
+    if table.dtype is not torch.int32 or table.device != device:
+        _need_cuda("table", table, torch.int32)
+        _same_device(q, table=table)
     if table.dim() != 2 or table.shape[0] != B or (table.shape[1] > 1 and table.stride(1) != 1):
         raise ValueError(f"table must be [B={B}, width] with unit column stride")
+    if lengths.dtype is not torch.int32 or lengths.device != device:
+        _need_cuda("lengths", lengths, torch.int32)
+        _same_device(q, lengths=lengths)
     if tuple(lengths.shape) != (B,) or not lengths.is_contiguous():
         raise ValueError(f"lengths must be a contiguous [B={B}] tensor")
-    nbytes = _cache_bytes(cache)
-    _same_device(q, cache=cache, table=table, lengths=lengths, out=out)
+    nbytes = _cache_bytes(cache, device)
     width = table.shape[1]
-    ws_bytes = attention_workspace_size(B, Hq, kv_heads, D, page_size, width, window, kind) if B > 0 else 0
-    ws = (workspace or _default_workspace(q.device, "attention")).get(ws_bytes)
+    ws_ptr, ws_bytes = None, 0
+    if B > 0:
+        need = attention_workspace_size(B, Hq, kv_heads, D, page_size, width, window, kind)
+        ws = (workspace or _default_workspace(device, "attention")).get(need)
+        ws_ptr, ws_bytes = ws.data_ptr(), ws.numel()
     _check(load_library().w4a16_attention(
-        _ptr(q), q.stride(0), q.stride(1), B, Hq, _ptr(cache), nbytes, pages, kv_heads, D, page_size, kind,
-        _DTYPE_CODE[q.dtype], _ptr(table), width, _ld(table), _ptr(lengths), window,
-        D ** -0.5 if scale is None else scale, _ptr(out), out.stride(0), out.stride(1),
-        _ptr(ws) if ws_bytes else None, ws.numel() if (ws is not None and ws_bytes) else 0, _stream(q)))
+        q.data_ptr(), q.stride(0), q.stride(1), B, Hq, cache.data_ptr(), nbytes, pages, kv_heads, D, page_size, kind,
+        _DTYPE_CODE[dtype], table.data_ptr(), width, _ld(table), lengths.data_ptr(), window,
+        D ** -0.5 if scale is None else scale, out.data_ptr(), out.stride(0), out.stride(1), ws_ptr, ws_bytes,
+        _stream(q)))
     return out

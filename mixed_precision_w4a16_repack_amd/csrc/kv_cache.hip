@@ -37,15 +37,18 @@ __device__ __forceinline__ uint32_t lanes_top(uint32_t v, int step) {
 }
 
 // The codes of a row of scale s: the quotient is rounded to fp32, then to a
-// code, and may pass 127 by that first rounding only. One reciprocal a row and
-// a corrected product give the rounded quotient (but for rare last bits);
-// scales whose reciprocal nears fp32's ends take the division itself.
+// code, and may pass 127 by that first rounding only. With the row's rounded
+// reciprocal, x * inv is off by less than two last places; the first
+// correction by the exact remainder leaves less than one, the second the
+// rounded quotient. Scales near fp32's ends, whose remainders would be
+// subnormal, take the division itself.
 struct Coder {
     float s, inv;
     Coder() = default;
-    __device__ __forceinline__ explicit Coder(float scale) : s(scale), inv(scale > 1e-36f && scale < 1e36f ? 1.0f / scale : 0.0f) {}
+    __device__ __forceinline__ explicit Coder(float scale) : s(scale), inv(scale > 1e-25f && scale < 1e30f ? 1.0f / scale : 0.0f) {}
     __device__ __forceinline__ uint32_t operator()(float x) const {
         float q = x * inv;
+        q = __builtin_fmaf(__builtin_fmaf(-q, s, x), inv, q);
         q = __builtin_fmaf(__builtin_fmaf(-q, s, x), inv, q);
         if (inv == 0.0f) q = s > 0.0f ? x / s : 0.0f;
         const float c = __builtin_rintf(q);

@@ -622,7 +622,7 @@ w4a16_status kv_impl(bool write, const void* k, int64_t k_ts, int64_t k_hs, cons
     if ((st = check_head_strides("k", k_ts, k_hs)) != W4A16_OK || (st = check_head_strides("v", v_ts, v_hs)) != W4A16_OK)
         return st;
     if (T == 0) return W4A16_OK;
-    if (T > kMaxDim || kv_workgroups(T, kv_heads) > kMaxWorkgroups)
+    if (T > kMaxWorkgroups || kv_workgroups(T, kv_heads) > kMaxWorkgroups)  // tokens are counted in 32 bits too
         return fail(W4A16_ERR_UNSUPPORTED, "T=%lld is too large for one launch", (long long)T);
     if (k == nullptr || v == nullptr || slots == nullptr)
         return fail(W4A16_ERR_INVALID_ARG, "k, v and slots must not be NULL");
