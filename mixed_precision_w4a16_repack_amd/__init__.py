@@ -128,9 +128,12 @@ def _check(status: int):
         raise RuntimeError(f"w4a16 status {status}: {last_error()}")
 
 
+# The handle of torch.cuda.current_stream(index), without building the object.
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
 def _stream(t: torch.Tensor):
-    # the handle of torch.cuda.current_stream(t.device), without building the object
-    return torch._C._cuda_getCurrentRawStream(t.get_device())
+    return _raw_stream(t.get_device())
 
 
 def _ptr(t: torch.Tensor | None):
@@ -273,7 +276,7 @@ def _default_workspace(device, kind: str = "w4a16") -> Workspace:
     region at the start of its workspace to be zero, and w4a8_gemm writes its
     partial results from the start of its own."""
     index = torch.device(device).index
-    key = (kind, index, torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if index is None else index))
+    key = (kind, index, _raw_stream(torch.cuda.current_device() if index is None else index))
     ws = _workspaces.get(key)
     if ws is None:
         ws = _workspaces[key] = Workspace(device)
@@ -447,9 +450,9 @@ def _fits(t: torch.Tensor, shape, dtype, device) -> bool:
     return t.dtype is dtype and t.shape == shape and t.device == device and t.stride(-1) == 1
 
 
-def _rows(name: str, t: torch.Tensor | None, x: torch.Tensor, M: int, K: int):
+def _rows(name: str, t: torch.Tensor, x: torch.Tensor, M: int, K: int):
     """t must be [M, K] rows of x's dtype on its device."""
-    if t is None or _fits(t, (M, K), x.dtype, x.device):
+    if _fits(t, (M, K), x.dtype, x.device):
         return
     _need_cuda(name, t, x.dtype)
     if tuple(t.shape) != (M, K) or t.stride(1) != 1:
@@ -457,12 +460,9 @@ def _rows(name: str, t: torch.Tensor | None, x: torch.Tensor, M: int, K: int):
     _same_device(x, **{name: t})
 
 
-def _ld(t: torch.Tensor | None) -> int:
+def _ld(t: torch.Tensor | None, M: int, K: int) -> int:
     """Row stride of [M, K] rows (torch gives a single row any stride)."""
-    if t is None:
-        return 0
-    ld = t.stride(0)
-    return ld if t.shape[0] > 1 else max(ld, t.shape[1])
+    return 0 if t is None else t.stride(0) if M > 1 else K
 
 
 def _codes_out(out, x: torch.Tensor, M: int, K: int):
@@ -479,6 +479,10 @@ def _codes_out(out, x: torch.Tensor, M: int, K: int):
     return qa, xs
 
 
+def _ld_codes(qa: torch.Tensor, M: int, K: int) -> int:
+    return qa.stride(0) if M > 1 else (K + 7) // 8 * 8
+
+
 def _norm_args(x, weight, residual, residual_out):
     if not x.is_cuda or x.dtype not in _DTYPE_CODE:
         _need_cuda("x", x, (torch.float16, torch.bfloat16))
@@ -490,8 +494,10 @@ def _norm_args(x, weight, residual, residual_out):
         if tuple(weight.shape) != (K,) or not weight.is_contiguous():
             raise ValueError(f"weight must be a contiguous [K={K}] tensor")
         _same_device(x, weight=weight)
-    _rows("residual", residual, x, M, K)
-    _rows("residual_out", residual_out, x, M, K)
+    if residual is not None:
+        _rows("residual", residual, x, M, K)
+    if residual_out is not None and residual_out is not residual:
+        _rows("residual_out", residual_out, x, M, K)
     return M, K
 
 
@@ -505,9 +511,12 @@ def rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-5, residual: 
         out = torch.empty((M, K), dtype=x.dtype, device=x.device)
     else:
         _rows("out", out, x, M, K)
-    _check(load_library().w4a16_rmsnorm(
-        x.data_ptr(), M, K, _ld(x), _DTYPE_CODE[x.dtype], weight.data_ptr(), eps, _ptr(residual), _ld(residual),
-        _ptr(residual_out), _ld(residual_out), out.data_ptr(), _ld(out), _stream(x)))
+    status = (_lib or load_library()).w4a16_rmsnorm(
+        x.data_ptr(), M, K, x.stride(0) if M > 1 else K, _DTYPE_CODE[x.dtype], weight.data_ptr(), eps,
+        _ptr(residual), _ld(residual, M, K), _ptr(residual_out), _ld(residual_out, M, K),
+        out.data_ptr(), out.stride(0) if M > 1 else K, _raw_stream(x.get_device()))
+    if status:
+        _check(status)
     return out
 
 
@@ -516,9 +525,12 @@ def rmsnorm_a8(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-5, residua
     """``rmsnorm`` as the input of ``gemm_w4a8``: (qa [M, K] int8, xs [M] fp32), as ``quantize_a8`` stores them."""
     M, K = _norm_args(x, weight, residual, residual_out)
     qa, xs = _codes_out(out, x, M, K)
-    _check(load_library().w4a8_rmsnorm(
-        x.data_ptr(), M, K, _ld(x), _DTYPE_CODE[x.dtype], weight.data_ptr(), eps, _ptr(residual), _ld(residual),
-        _ptr(residual_out), _ld(residual_out), qa.data_ptr(), _ld(qa), xs.data_ptr(), _stream(x)))
+    status = (_lib or load_library()).w4a8_rmsnorm(
+        x.data_ptr(), M, K, x.stride(0) if M > 1 else K, _DTYPE_CODE[x.dtype], weight.data_ptr(), eps,
+        _ptr(residual), _ld(residual, M, K), _ptr(residual_out), _ld(residual_out, M, K),
+        qa.data_ptr(), _ld_codes(qa, M, K), xs.data_ptr(), _raw_stream(x.get_device()))
+    if status:
+        _check(status)
     return qa, xs
 
 
@@ -537,8 +549,11 @@ def silu_mul(x: torch.Tensor, out: torch.Tensor | None = None) -> torch.Tensor:
         out = torch.empty((M, K), dtype=x.dtype, device=x.device)
     else:
         _rows("out", out, x, M, K)
-    _check(load_library().w4a16_silu_mul(x.data_ptr(), M, K, _ld(x), _DTYPE_CODE[x.dtype], out.data_ptr(), _ld(out),
-                                         _stream(x)))
+    status = (_lib or load_library()).w4a16_silu_mul(
+        x.data_ptr(), M, K, x.stride(0) if M > 1 else 2 * K, _DTYPE_CODE[x.dtype], out.data_ptr(),
+        out.stride(0) if M > 1 else K, _raw_stream(x.get_device()))
+    if status:
+        _check(status)
     return out
 
 
@@ -546,8 +561,11 @@ def silu_mul_a8(x: torch.Tensor, out: tuple[torch.Tensor, torch.Tensor] | None =
     """``silu_mul`` as the input of ``gemm_w4a8``: (qa [M, K] int8, xs [M] fp32)."""
     M, K = _gate_args(x)
     qa, xs = _codes_out(out, x, M, K)
-    _check(load_library().w4a8_silu_mul(x.data_ptr(), M, K, _ld(x), _DTYPE_CODE[x.dtype], qa.data_ptr(), _ld(qa),
-                                        xs.data_ptr(), _stream(x)))
+    status = (_lib or load_library()).w4a8_silu_mul(
+        x.data_ptr(), M, K, x.stride(0) if M > 1 else 2 * K, _DTYPE_CODE[x.dtype], qa.data_ptr(), _ld_codes(qa, M, K),
+        xs.data_ptr(), _raw_stream(x.get_device()))
+    if status:
+        _check(status)
     return qa, xs
 
 
@@ -579,7 +597,8 @@ def _cache_bytes(cache: torch.Tensor, device) -> int:
 
 
 def _slots(slots: torch.Tensor) -> int:
-    _need_cuda("slots", slots, torch.int64)
+    if not slots.is_cuda or slots.dtype is not torch.int64:
+        _need_cuda("slots", slots, torch.int64)
     if slots.dim() != 1 or not slots.is_contiguous():
         raise ValueError("slots must be a contiguous [T] tensor")
     return slots.shape[0]
@@ -590,7 +609,8 @@ def kv_write(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, cache: torch
     """Writes keys and values [T, kv_heads, head_dim] to their slots (page * page_size + offset; -1: not written).
 
     Any token and head strides; ``kind`` is ``KV_ACT`` (values in k's dtype) or ``KV_INT8``."""
-    _need_cuda("k", k, (torch.float16, torch.bfloat16))
+    if not k.is_cuda or k.dtype not in _DTYPE_CODE:
+        _need_cuda("k", k, (torch.float16, torch.bfloat16))
     T = _slots(slots)
     if k.dim() != 3:
         raise ValueError("k must be [T, kv_heads, head_dim]")
@@ -601,9 +621,11 @@ def kv_write(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, cache: torch
     nbytes = _cache_bytes(cache, device)
     if slots.device != device:
         _same_device(k, slots=slots)
-    _check(load_library().w4a16_kv_write(
+    status = (_lib or load_library()).w4a16_kv_write(
         k.data_ptr(), k.stride(0), k.stride(1), v.data_ptr(), v.stride(0), v.stride(1), T, slots.data_ptr(),
-        cache.data_ptr(), nbytes, pages, H, D, page_size, kind, _DTYPE_CODE[dtype], _stream(k)))
+        cache.data_ptr(), nbytes, pages, H, D, page_size, kind, _DTYPE_CODE[dtype], _raw_stream(k.get_device()))
+    if status:
+        _check(status)
 
 
 def kv_read(slots: torch.Tensor, cache: torch.Tensor, pages: int, kv_heads: int, head_dim: int, page_size: int,
@@ -620,9 +642,11 @@ def kv_read(slots: torch.Tensor, cache: torch.Tensor, pages: int, kv_heads: int,
         _heads("k", k, shape, dtype, device)
         _heads("v", v, shape, dtype, device)
     nbytes = _cache_bytes(cache, device)
-    _check(load_library().w4a16_kv_read(
+    status = (_lib or load_library()).w4a16_kv_read(
         slots.data_ptr(), T, cache.data_ptr(), nbytes, pages, kv_heads, head_dim, page_size, kind, _DTYPE_CODE[dtype],
-        k.data_ptr(), k.stride(0), k.stride(1), v.data_ptr(), v.stride(0), v.stride(1), _stream(slots)))
+        k.data_ptr(), k.stride(0), k.stride(1), v.data_ptr(), v.stride(0), v.stride(1), _raw_stream(slots.get_device()))
+    if status:
+        _check(status)
     return k, v
 
 
@@ -661,7 +685,7 @@ def attention(q: torch.Tensor, cache: torch.Tensor, table: torch.Tensor, lengths
     if lengths.dtype is not torch.int32 or lengths.device != device:
         _need_cuda("lengths", lengths, torch.int32)
         _same_device(q, lengths=lengths)
-    if tuple(lengths.shape) != (B,) or not lengths.is_contiguous():
+    if lengths.shape != (B,) or not lengths.is_contiguous():
         raise ValueError(f"lengths must be a contiguous [B={B}] tensor")
     nbytes = _cache_bytes(cache, device)
     width = table.shape[1]
@@ -670,9 +694,11 @@ def attention(q: torch.Tensor, cache: torch.Tensor, table: torch.Tensor, lengths
         need = attention_workspace_size(B, Hq, kv_heads, D, page_size, width, window, kind)
         ws = (workspace or _default_workspace(device, "attention")).get(need)
         ws_ptr, ws_bytes = ws.data_ptr(), ws.numel()
-    _check(load_library().w4a16_attention(
+    status = (_lib or load_library()).w4a16_attention(
         q.data_ptr(), q.stride(0), q.stride(1), B, Hq, cache.data_ptr(), nbytes, pages, kv_heads, D, page_size, kind,
-        _DTYPE_CODE[dtype], table.data_ptr(), width, _ld(table), lengths.data_ptr(), window,
+        _DTYPE_CODE[dtype], table.data_ptr(), width, table.stride(0) if B > 1 else width, lengths.data_ptr(), window,
         D ** -0.5 if scale is None else scale, out.data_ptr(), out.stride(0), out.stride(1), ws_ptr, ws_bytes,
-        _stream(q)))
+        _raw_stream(q.get_device()))
+    if status:
+        _check(status)
     return out

@@ -24,12 +24,25 @@
 // fp16's range (its 8 bits are exact there; elements below 2^-29 of the
 // largest lose bits).
 //
-// What bounds it: the cache's bytes. Work is divided by tiles over a fixed
-// number of workgroups, computed on the device from the lengths (the host
-// does not know them): each takes an equal run of the list of all (sequence,
-// kv head, tile), whatever the lengths are. A (sequence, head) that several
-// workgroups share is joined by the last of them to arrive, in order of
-// position, so the result does not depend on the order of arrival.
+// What bounds it: the cache's bytes. 64 sequences of 2048 tokens, 8 kv heads
+// of 128: 82 us in 16 bits (6.5 TB/s; a plain read of as much reaches 6.9),
+// 46 us in int8 (6.0 TB/s). The loads are non-temporal (each byte is read
+// once; through the caches as usual the 82 us were 92).
+//
+// Work is divided by tiles over a fixed number of workgroups, computed on the
+// device from the lengths (the host does not know them): each takes an equal
+// run of the list of all (sequence, kv head, tile), whatever the lengths are.
+// A head's start (query, page table, first tile: three waits) and end (four
+// waves joined) count as kHeadBytes more: without that, 64 sequences from 0 to
+// 6000 tokens took 112 us, the workgroups of the short ones being last, and
+// now take 91 (80 us at 6.5 TB/s). A (sequence, head) that several workgroups
+// share is joined by the last of them to arrive, in order of position, so the
+// result does not depend on the order of arrival: kFan at a time, over levels,
+// each level about 3 us (one sequence of 131000 tokens, int8: 52 us, of them 6
+// in two levels; with 16 at a time 55, with 64 in one level 63).
+// A short call is bound by its chain of waits: 333 tokens of one sequence
+// 7.1 us, of them 2 before the first instruction and after the last, 1.3 to
+// find its share, 2.6 for three tiles a wave and 1 to join the waves.
 #include "device_common.h"
 #include "exchange.h"
 #include "internal.h"
@@ -40,7 +53,9 @@ namespace {
 
 constexpr int kWaves = 4;
 constexpr int kTile = 32;              // tokens
-constexpr int kMinTiles = 16;          // least tiles per workgroup when a head is split
+// Least tiles per workgroup when a head is split: a split costs a join. With 8,
+// 333 tokens take 8.0 us instead of 7.1; with 32, 1000 tokens 11.5 and not 9.6.
+constexpr int kMinTiles = 16;
 constexpr int kHeadBytes = 80 << 10;   // a head's start and end cost a workgroup about as much as reading this
 constexpr int kFan = 8;                // partial results joined at once (their loads are in flight together)
 constexpr int kChunkBits = 24;         // a sum over sequences: slots << kChunkBits | chunks, the latter cut to kChunkMost a lane
@@ -51,11 +66,17 @@ typedef u32x4 u32x4_any __attribute__((aligned(2)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef u32x2 u32x2_any __attribute__((aligned(2)));
 
-// How many workgroups of each kernel share a CU (registers allow that many).
+// How many workgroups of each kernel share a CU. More waves than the bytes in
+// flight need make the reads slower, not faster: int8 D = 128 takes 63 us with
+// three and 46 with two at 64 x 2048 tokens (49 with one), int8 D = 64 60 us
+// with four, 52 with three, 47 with two. The larger operands' registers allow
+// one; 16 bits with two head tiles lose by a second one too (64 x 4096 tokens
+// of one kv head, 32 query heads: 37 and 39 us), int8 gains (34 and 28 us).
 template <int KIND, int D, int HT>
-constexpr int kPerCU = HT == 2 || D > 192 || (KIND == 0 && D > 128) ? 1 : 2;
+constexpr int kPerCU = D > 192 || (D > 128 && (HT == 2 || KIND == 0)) || (HT == 2 && KIND == 0) ? 1 : 2;
 
-// What is left of the references in fp16 (2^13 * 2^2 < 65504).
+// The factor on probabilities, and how far (in powers of 2) a score may pass
+// the reference: in fp16 2^13 * 2^2 < 65504.
 template <bool F16P>
 struct Prob {
     static constexpr float kBias = F16P ? 13.0f : 0.0f;
@@ -88,6 +109,13 @@ __device__ __forceinline__ u32x4 codes8_to_f16(uint32_t w0, uint32_t w1) {
     codes_to_f16(w0, a, b);
     codes_to_f16(w1, c, d);
     return u32x4{a, b, c, d};
+}
+
+// A pointer that is the same on all lanes, in scalar registers.
+__device__ __forceinline__ const float* uniform(const float* p) {
+    const uint64_t v = reinterpret_cast<uint64_t>(p);
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((int)(uint32_t)v), hi = __builtin_amdgcn_readfirstlane((int)(uint32_t)(v >> 32));
+    return reinterpret_cast<const float*>((uint64_t)hi << 32 | lo);
 }
 
 __device__ __forceinline__ int64_t read_lane(int64_t v, int lane) {
@@ -613,10 +641,8 @@ __global__ __launch_bounds__(256, (kPerCU<KIND, D, HT>)) void attention_kernel(A
             for (int e = threadIdx.x; e < heads * (D / 4); e += 256) {
                 const int head = e / (D / 4), d = e % (D / 4) * 4;
                 Join j;
-                float mn = j.m;
 #pragma unroll
-                for (int v = 0; v < kWaves; ++v) mn = fmaxf(mn, ml[2 * (v * heads + head)]);
-                j.m = mn;
+                for (int v = 0; v < kWaves; ++v) j.m = fmaxf(j.m, ml[2 * (v * heads + head)]);
 #pragma unroll
                 for (int v = 0; v < kWaves; ++v)
                     j.add(ml[2 * (v * heads + head)], ml[2 * (v * heads + head) + 1],
@@ -653,20 +679,17 @@ __global__ __launch_bounds__(256, (kPerCU<KIND, D, HT>)) void attention_kernel(A
                 if (!mine) break;
                 const bool done = count <= kFan;
                 const int pair = level & 1 ? 2 : 0;
+                float* lead_p = Pt::at(a.partials, lead_wg, lead_slot);
+                const float* from[kFan];
+#pragma unroll
+                for (int i = 0; i < kFan; ++i)
+                    from[i] = uniform(i == 0 || size == 1 ? lead_p : Pt::at(a.partials, lead_wg + (i < size ? i : size - 1) * step, 0));
                 for (int e = threadIdx.x; e < heads * (D / 4); e += 256) {
                     const int head = e / (D / 4), d = e % (D / 4) * 4;
-                    float* lead_p = Pt::at(a.partials, lead_wg, lead_slot) + head * Pt::kStride;
-                    const float* p = Pt::at(a.partials, lead_wg, 0) + head * Pt::kStride;
                     float2 pml[kFan];
                     floatx4 po[kFan];
                     Join j;
-#pragma unroll
-                    for (int i = 0; i < kFan; ++i) {
-                        const float* pi = i == 0 ? lead_p : p;
-                        pml[i] = load_coherent2(pi + pair);
-                        po[i] = load_coherent(pi + 4 + d);
-                        if (i + 1 < size) p += 2 * Pt::kFloats * step;
-                    }
+                    load_coherent8(from, (head * Pt::kStride + 4 + d) * 4, (head * Pt::kStride + pair) * 4, po, pml);
 #pragma unroll
                     for (int i = 0; i < kFan; ++i) j.m = fmaxf(j.m, pml[i].x);
 #pragma unroll
@@ -675,8 +698,9 @@ __global__ __launch_bounds__(256, (kPerCU<KIND, D, HT>)) void attention_kernel(A
                     if (done) {
                         store_out<DT>(a, b, head0 + head, d, j);
                     } else {  // in the leader's place
-                        store_coherent(lead_p + 4 + d, j.o);
-                        if (d == 0) store_coherent2(lead_p + (2 - pair), j.m, j.l);
+                        float* p = lead_p + head * Pt::kStride;
+                        store_coherent(p + 4 + d, j.o);
+                        if (d == 0) store_coherent2(p + (2 - pair), j.m, j.l);
                     }
                 }
                 if (done) break;

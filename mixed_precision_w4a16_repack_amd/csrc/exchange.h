@@ -49,9 +49,32 @@ __device__ __forceinline__ floatx4 load_coherent(const float* p) {
     const float2 a = __builtin_bit_cast(float2, lo), b = __builtin_bit_cast(float2, hi);
     return floatx4{a.x, a.y, b.x, b.y};
 }
-__device__ __forceinline__ float2 load_coherent2(const float* p) {
-    return __builtin_bit_cast(float2, __hip_atomic_load(reinterpret_cast<const uint64_t*>(p), __ATOMIC_RELAXED,
-                                                        __HIP_MEMORY_SCOPE_AGENT));
+// Eight coherent 16-byte loads and eight of 8 bytes at two byte offsets from
+// eight uniform bases, with the wait in the same asm statement (as above).
+__device__ __forceinline__ void load_coherent8(const float* const (&p)[8], uint32_t off4, uint32_t off2, floatx4 (&v)[8],
+                                               float2 (&w)[8]) {
+    asm volatile(
+        "global_load_dwordx4 %0, %16, %18 sc1\n\t"
+        "global_load_dwordx4 %1, %16, %19 sc1\n\t"
+        "global_load_dwordx4 %2, %16, %20 sc1\n\t"
+        "global_load_dwordx4 %3, %16, %21 sc1\n\t"
+        "global_load_dwordx4 %4, %16, %22 sc1\n\t"
+        "global_load_dwordx4 %5, %16, %23 sc1\n\t"
+        "global_load_dwordx4 %6, %16, %24 sc1\n\t"
+        "global_load_dwordx4 %7, %16, %25 sc1\n\t"
+        "global_load_dwordx2 %8, %17, %18 sc1\n\t"
+        "global_load_dwordx2 %9, %17, %19 sc1\n\t"
+        "global_load_dwordx2 %10, %17, %20 sc1\n\t"
+        "global_load_dwordx2 %11, %17, %21 sc1\n\t"
+        "global_load_dwordx2 %12, %17, %22 sc1\n\t"
+        "global_load_dwordx2 %13, %17, %23 sc1\n\t"
+        "global_load_dwordx2 %14, %17, %24 sc1\n\t"
+        "global_load_dwordx2 %15, %17, %25 sc1\n\t"
+        "s_waitcnt vmcnt(0)"
+        : "=&v"(v[0]), "=&v"(v[1]), "=&v"(v[2]), "=&v"(v[3]), "=&v"(v[4]), "=&v"(v[5]), "=&v"(v[6]), "=&v"(v[7]),
+          "=&v"(w[0]), "=&v"(w[1]), "=&v"(w[2]), "=&v"(w[3]), "=&v"(w[4]), "=&v"(w[5]), "=&v"(w[6]), "=&v"(w[7])
+        : "v"(off4), "v"(off2), "s"(p[0]), "s"(p[1]), "s"(p[2]), "s"(p[3]), "s"(p[4]), "s"(p[5]), "s"(p[6]), "s"(p[7])
+        : "memory");
 }
 // Waits until every vector memory access this wave issued has completed
 // (write-through stores: reached the coherence point).
