@@ -364,7 +364,7 @@ w4a16_status w4a8_silu_mul(const void *x, int64_t M, int64_t K, int64_t ldx, int
  * multiple of 32. `kind` is a w4a16_kv_kind: 16-bit values in the act dtype,
  * or int8 codes with one fp32 scale per token and head for the key and one
  * for the value (scale = max_d |x| / 127, code = rint(x / scale), a row of
- * zeros has scale 0).
+ * zeros has scale 0, a row that holds a NaN scale NaN).
  *
  * Layout: page p, head h is a record of R bytes at (p * kv_heads + h) * R,
  * where D = head_dim, P = page_size, R = 4 P D (16 bit) or 2 P D + 8 P (int8):
@@ -407,7 +407,8 @@ w4a16_status w4a16_kv_read(const int64_t *slots, int64_t T, const void *cache, s
                            int64_t k_ts, int64_t k_hs, void *v, int64_t v_ts, int64_t v_hs, hipStream_t stream);
 
 /* Bytes of device workspace w4a16_attention needs for these arguments (0 if
- * none). It starts with the counter region of w4a16_workspace_size(), with
+ * B == 0; it does not grow with B or the table beyond what a full card of
+ * workgroups needs). It starts with the counter region of w4a16_workspace_size(), with
  * the same rule: w4a16_workspace_counter_bytes() zero bytes before the first
  * use, left zero by every completed call. Calls that share a workspace must
  * be ordered. out_bytes is a host pointer. */
@@ -427,10 +428,14 @@ w4a16_status w4a16_attention_workspace_size(int64_t B, int32_t q_heads, int32_t 
  *   q, out  element (b, head, d) at b * bs + head * hs + d, act dtype
  *   table   [B, table_ld] int32, table_ld >= table_width (device)
  *   lengths [B] int32 (device)
- * q_heads must be a multiple of kv_heads; scale finite; B == 0 is a no-op. The
+ * q_heads must be a multiple of kv_heads; scale finite; table_width *
+ * page_size at most 2^31, B times it at most 2^43; B == 0 is a no-op. The
  * result does not depend on the workspace's contents or on earlier calls
- * (no float atomics: the order of every sum is fixed). W4A16_ERR_SIZE if the
- * cache or the workspace is too small. */
+ * (no float atomics: the order of every sum follows from the sizes and lengths).
+ * Probabilities are rounded to the 16 bits of the matrix operand (the act
+ * dtype's, fp16's over an int8 cache); scores, their maximum and every sum are
+ * fp32. W4A16_ERR_SIZE if the cache or the workspace is too small. The
+ * workspace must be 256-byte aligned. */
 w4a16_status w4a16_attention(const void *q, int64_t q_bs, int64_t q_hs, int64_t B, int32_t q_heads, const void *cache,
                              size_t cache_bytes, int64_t pages, int32_t kv_heads, int32_t head_dim, int32_t page_size,
                              int32_t kind, int32_t dtype, const int32_t *table, int64_t table_width, int64_t table_ld,

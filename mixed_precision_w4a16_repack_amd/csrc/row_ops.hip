@@ -7,6 +7,12 @@
 // to read back. Statistics, products and the scale are fp32; y is rounded
 // once (to 16 bits, or to a code).
 //
+// What bounds them: bytes for many rows (8192 x 4096 with residual 42 us for 268
+// MB, 6.4 TB/s; 2048 x 14336 of the gate 28 us, 6.3 TB/s; torch's copy of as
+// many bytes reaches 5.3), the chain load - reduce - store for few (1 x 4096
+// 2.3 us, 64 x 4096 to codes 3.7 us). A row is read once: it stays in registers
+// up to 32768 columns.
+//
 // Rows need no alignment beyond their element's: 16-byte accesses are made
 // on any 2-byte address (global memory takes them), and the up to 7 elements
 // of a row's end are moved one by one.

@@ -312,6 +312,33 @@ def test_cache_int8_rows_with_a_nan_keep_it(T):
         assert torch.equal(got.isnan().all(-1), x.isnan().any(-1)) and torch.equal(got.isnan().any(-1), x.isnan().any(-1))
 
 
+@pytest.mark.parametrize("dtype", BOTH)
+@pytest.mark.parametrize("T", [40, 520])
+def test_cache_int8_codes_are_exact_at_ties_and_at_the_range_ends(T, dtype):
+    """code = 127 x / max rounded half to even, in integers: rows of small integers (many quotients are ties)
+    times a power of two from far below to far above 1."""
+    H, D, P, dt = 8, 64, 32, DTYPES[dtype]
+    g = gen("cache ties", T, dtype)
+    top = torch.randint(1, 128, (T, H, 1), generator=g)
+    n = torch.minimum(torch.maximum(torch.randint(-127, 128, (T, H, D), generator=g), -top), top)
+    n[:, :, :1] = top
+    n[:, 0] = torch.where(torch.arange(D) % 2 == 0, 2 * top[:, 0], top[:, 0])  # max / 2: 63.5
+    span = 110 if dtype == "bf16" else 7
+    x = (n.double() * 2.0 ** torch.randint(-span, span, (T, H, 1), generator=g).double()).to(dt)
+    amax = n.abs().amax(-1, keepdim=True)
+    twice, whole = 254 * n, 2 * amax  # 127 n / amax + 1/2 = (254 n + amax) / (2 amax)
+    up = torch.div(twice + amax, whole, rounding_mode="floor")
+    tie = (twice + amax) % whole == 0
+    want = torch.where(tie & (up % 2 != 0), up - 1, up)
+    pages = -(-T // P)
+    cache = torch.zeros(w4.kv_cache_size(pages, H, D, P, ref.KV_INT8), dtype=torch.uint8, device=DEV)
+    slots = torch.arange(T)
+    w4.kv_write(x.to(DEV), x.flip(0).to(DEV), slots.to(DEV), cache, pages, P, ref.KV_INT8)
+    kc, vc, _, _ = stored(cache, slots.numpy(), H, D, P, ref.KV_INT8)
+    assert bool(tie.any())
+    assert np.array_equal(kc, want.numpy()) and np.array_equal(vc, want.flip(0).numpy())
+
+
 @pytest.mark.parametrize("kind", [ref.KV_ACT, ref.KV_INT8])
 @pytest.mark.parametrize("start", [0, 1, 2, 3, 4, 30, 64])
 def test_cache_prompts_that_start_inside_a_tile(start, kind):
