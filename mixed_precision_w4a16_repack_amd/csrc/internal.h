@@ -156,6 +156,7 @@ struct NormArgs {
     int64_t M = 0, K = 0, ldx = 0, ldr = 0, ldro = 0, ldy = 0, ldq = 0;
     float eps = 0.0f;
 };
+int64_t row_threads(int64_t M, int64_t K);  // threads per row of launch_norm, and of launch_gate with codes
 hipError_t launch_norm(const NormArgs& a, int dtype, hipStream_t stream);
 
 struct GateArgs {
@@ -165,7 +166,7 @@ struct GateArgs {
     float* xs = nullptr;
     int64_t M = 0, K = 0, ldx = 0, ldy = 0, ldq = 0;
 };
-int64_t gate_workgroups(int64_t M, int64_t K, bool out8);  // of launch_gate
+int64_t gate_workgroups(int64_t M, int64_t K);  // of launch_gate with 16-bit output, 256 threads each
 hipError_t launch_gate(const GateArgs& a, int dtype, hipStream_t stream);
 
 struct KvArgs {
@@ -181,7 +182,7 @@ struct KvArgs {
     int shift = 0;            // set by the launch: log2(P), or -1
 };
 constexpr int kKvMaxD = 256;  // largest head size
-int64_t kv_workgroups(int64_t T, int64_t H);  // of launch_kv_write and launch_kv_read
+int64_t kv_workgroups(int64_t T, int64_t H);  // of launch_kv_write and launch_kv_read, 256 threads each
 hipError_t launch_kv_write(const KvArgs& a, int kind, int dtype, hipStream_t stream);
 hipError_t launch_kv_read(const KvArgs& a, int kind, int dtype, hipStream_t stream);
 

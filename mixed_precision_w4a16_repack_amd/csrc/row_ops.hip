@@ -350,7 +350,13 @@ void gate_dispatch(const GateArgs& a, hipStream_t stream) {
 
 }  // namespace
 
-int64_t gate_workgroups(int64_t M, int64_t K, bool out8) { return out8 ? M : M * ((K + 2047) / 2048); }
+int64_t row_threads(int64_t M, int64_t K) {
+    int64_t n = 0;
+    by_width(M, K, [&](auto tpr, auto) { n = decltype(tpr)::value; });
+    return n;
+}
+
+int64_t gate_workgroups(int64_t M, int64_t K) { return M * ((K + 2047) / 2048); }
 
 hipError_t launch_norm(const NormArgs& a, int dtype, hipStream_t stream) {
     if (dtype == 0) norm_dispatch<0>(a, stream);

@@ -481,8 +481,8 @@ w4a16_status w4a16_gemm_dense(const void* A, int64_t M, int64_t lda, const void*
 namespace w4a16 {
 namespace {
 
-// Workgroups of one launch are counted in 32 bits.
-constexpr int64_t kMaxWorkgroups = ((int64_t)1 << 31) - 1;
+// The threads of one launch are counted in 32 bits.
+constexpr int64_t kMaxThreads = ((int64_t)1 << 32) - 1;
 
 bool aligned_to(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
@@ -497,8 +497,7 @@ w4a16_status check_row_stride(const char* name, int64_t ld, const char* width, i
     return check_stride(name, ld);
 }
 
-// M rows of K elements for a kernel of at most one workgroup per row (norm)
-// or per 2048 columns (gate).
+// M rows of K elements.
 w4a16_status check_rows(int64_t M, int64_t K, int32_t dtype, bool out8) {
     if (M < 0) return fail(W4A16_ERR_INVALID_ARG, "M=%lld must be >= 0", (long long)M);
     if (K <= 0) return fail(W4A16_ERR_INVALID_ARG, "K=%lld must be positive", (long long)K);
@@ -506,7 +505,8 @@ w4a16_status check_rows(int64_t M, int64_t K, int32_t dtype, bool out8) {
     if (st != W4A16_OK) return st;
     if (K > kMaxDim) return fail(W4A16_ERR_UNSUPPORTED, "K=%lld must be at most 2^32", (long long)K);
     if (out8 && K % 8 != 0) return fail(W4A16_ERR_UNSUPPORTED, "K=%lld must be divisible by 8", (long long)K);
-    if (M > kMaxWorkgroups) return fail(W4A16_ERR_UNSUPPORTED, "M=%lld is too large for one launch", (long long)M);
+    if (M > kMaxThreads / row_threads(M, K))
+        return fail(W4A16_ERR_UNSUPPORTED, "M=%lld rows of K=%lld are too large for one launch", (long long)M, (long long)K);
     return W4A16_OK;
 }
 
@@ -557,7 +557,7 @@ w4a16_status gate_impl(const void* x, int64_t M, int64_t K, int64_t ldx, int32_t
     if (out8 ? (st = check_row_stride("ldq", ldq, "K", K)) != W4A16_OK : (st = check_row_stride("ldy", ldy, "K", K)) != W4A16_OK)
         return st;
     if (M == 0) return W4A16_OK;
-    if (gate_workgroups(M, K, out8) > kMaxWorkgroups)
+    if (!out8 && gate_workgroups(M, K) > kMaxThreads / 256)
         return fail(W4A16_ERR_UNSUPPORTED, "M=%lld rows of K=%lld are too large for one launch", (long long)M, (long long)K);
     if (x == nullptr) return fail(W4A16_ERR_INVALID_ARG, "x must not be NULL");
     if (out8 ? (qa == nullptr || xs == nullptr) : y == nullptr)
@@ -622,7 +622,7 @@ w4a16_status kv_impl(bool write, const void* k, int64_t k_ts, int64_t k_hs, cons
     if ((st = check_head_strides("k", k_ts, k_hs)) != W4A16_OK || (st = check_head_strides("v", v_ts, v_hs)) != W4A16_OK)
         return st;
     if (T == 0) return W4A16_OK;
-    if (T > kMaxWorkgroups || kv_workgroups(T, kv_heads) > kMaxWorkgroups)  // tokens are counted in 32 bits too
+    if (T > kMaxThreads / 2 || kv_workgroups(T, kv_heads) > kMaxThreads / 256)  // tokens are counted in 31 bits
         return fail(W4A16_ERR_UNSUPPORTED, "T=%lld is too large for one launch", (long long)T);
     if (k == nullptr || v == nullptr || slots == nullptr)
         return fail(W4A16_ERR_INVALID_ARG, "k, v and slots must not be NULL");
@@ -652,7 +652,7 @@ w4a16_status check_attention(int64_t B, int32_t q_heads, int32_t kv_heads, int32
         return fail(W4A16_ERR_INVALID_ARG, "q_heads=%d must be a positive multiple of kv_heads=%d", q_heads, kv_heads);
     if (table_width < 0) return fail(W4A16_ERR_INVALID_ARG, "table_width=%lld must be >= 0", (long long)table_width);
     if (window < 0) return fail(W4A16_ERR_INVALID_ARG, "window=%lld must be >= 0", (long long)window);
-    if (q_heads > (1 << 20) || B > (int64_t)1 << 31 || B * q_heads > kMaxWorkgroups)
+    if (q_heads > (1 << 20) || B > (int64_t)1 << 31 || B * q_heads >= (int64_t)1 << 31)
         return fail(W4A16_ERR_UNSUPPORTED, "B=%lld sequences of q_heads=%d are too large for one launch", (long long)B, q_heads);
     if (table_width > (((int64_t)1 << 31) + page_size - 1) / page_size)
         return fail(W4A16_ERR_UNSUPPORTED, "table_width=%lld pages hold more than 2^31 tokens", (long long)table_width);

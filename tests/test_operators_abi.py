@@ -107,6 +107,10 @@ def test_silu_mul_rejects_by_output(lib):
     assert _gate(lib, True, ldy=5) == INVALID and "ldq=5 must be >= K=4096" in w4.last_error()
     assert _gate(lib, True, K=4092) == UNSUPPORTED and "divisible by 8" in w4.last_error()
     assert _gate(lib, True, y=ctypes.c_void_p(4100)) == UNSUPPORTED and "8-byte aligned" in w4.last_error()
+    # rows of 14336 columns take 1024 threads each for codes, 7 workgroups of 256 else
+    assert _gate(lib, True, M=1 << 22, K=14336, ldx=28672, ldy=14336) == UNSUPPORTED
+    assert "too large for one launch" in w4.last_error()
+    assert _gate(lib, M=3 << 20, K=14336, ldx=28672, ldy=14336) == UNSUPPORTED
     # rows of 2^20 columns take 512 workgroups each
     assert _gate(lib, M=1 << 23, K=1 << 20, ldx=1 << 21, ldy=1 << 20) == UNSUPPORTED
     assert "too large for one launch" in w4.last_error()
