@@ -446,13 +446,18 @@ def _same_device(first: torch.Tensor, **others: torch.Tensor | None):
 # at again, for the message.
 
 
-def _fits(t: torch.Tensor, shape, dtype, device) -> bool:
-    return t.dtype is dtype and t.shape == shape and t.device == device and t.stride(-1) == 1
+def _fits(t: torch.Tensor, shape, dtype, device: int) -> bool:
+    return t.dtype is dtype and t.shape == shape and t.get_device() == device and t.stride(-1) == 1
+
+
+def _empty(like: torch.Tensor, shape) -> torch.Tensor:
+    """A contiguous tensor of the shape, which is `like`'s."""
+    return torch.empty_like(like) if like.is_contiguous() else torch.empty(shape, dtype=like.dtype, device=like.device)
 
 
 def _rows(name: str, t: torch.Tensor, x: torch.Tensor, M: int, K: int):
     """t must be [M, K] rows of x's dtype on its device."""
-    if _fits(t, (M, K), x.dtype, x.device):
+    if _fits(t, (M, K), x.dtype, x.get_device()):
         return
     _need_cuda(name, t, x.dtype)
     if tuple(t.shape) != (M, K) or t.stride(1) != 1:
@@ -489,7 +494,7 @@ def _norm_args(x, weight, residual, residual_out):
     if x.dim() != 2 or x.stride(1) != 1:
         raise ValueError("x must be 2-D with unit column stride")
     M, K = x.shape
-    if not _fits(weight, (K,), x.dtype, x.device):
+    if not _fits(weight, (K,), x.dtype, x.get_device()):
         _need_cuda("weight", weight, x.dtype)
         if tuple(weight.shape) != (K,) or not weight.is_contiguous():
             raise ValueError(f"weight must be a contiguous [K={K}] tensor")
@@ -508,7 +513,7 @@ def rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-5, residual: 
     ``residual_out`` (which may be ``residual`` itself) receives h."""
     M, K = _norm_args(x, weight, residual, residual_out)
     if out is None:
-        out = torch.empty((M, K), dtype=x.dtype, device=x.device)
+        out = _empty(x, (M, K))
     else:
         _rows("out", out, x, M, K)
     status = (_lib or load_library()).w4a16_rmsnorm(
@@ -576,21 +581,21 @@ def kv_cache_size(pages: int, kv_heads: int, head_dim: int, page_size: int, kind
     return int(out.value)
 
 
-def _heads(name: str, t: torch.Tensor, shape, dtype, device):
+def _heads(name: str, t: torch.Tensor, shape, dtype, device: int):
     if _fits(t, shape, dtype, device):
         return
     _need_cuda(name, t, dtype)
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{device}")
     if t.dim() != 3 or tuple(t.shape) != tuple(shape) or t.stride(2) != 1:
         raise ValueError(f"{name} must be {list(shape)} with unit stride in its last dimension, "
                          f"got {tuple(t.shape)} {t.stride()}")
 
 
-def _cache_bytes(cache: torch.Tensor, device) -> int:
-    if cache.device != device:
+def _cache_bytes(cache: torch.Tensor, device: int) -> int:
+    if cache.get_device() != device:
         _need_cuda("cache", cache)
-        raise ValueError(f"cache is on {cache.device}, expected {device}")
+        raise ValueError(f"cache is on {cache.device}, expected cuda:{device}")
     if not cache.is_contiguous():
         raise ValueError("cache must be contiguous")
     return cache.numel() * cache.element_size()
@@ -614,16 +619,16 @@ def kv_write(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, cache: torch
     T = _slots(slots)
     if k.dim() != 3:
         raise ValueError("k must be [T, kv_heads, head_dim]")
-    device, dtype = k.device, k.dtype
+    device, dtype = k.get_device(), k.dtype
     H, D = k.shape[1:]
     _heads("k", k, (T, H, D), dtype, device)
     _heads("v", v, (T, H, D), dtype, device)
     nbytes = _cache_bytes(cache, device)
-    if slots.device != device:
+    if slots.get_device() != device:
         _same_device(k, slots=slots)
     status = (_lib or load_library()).w4a16_kv_write(
         k.data_ptr(), k.stride(0), k.stride(1), v.data_ptr(), v.stride(0), v.stride(1), T, slots.data_ptr(),
-        cache.data_ptr(), nbytes, pages, H, D, page_size, kind, _DTYPE_CODE[dtype], _raw_stream(k.get_device()))
+        cache.data_ptr(), nbytes, pages, H, D, page_size, kind, _DTYPE_CODE[dtype], _raw_stream(device))
     if status:
         _check(status)
 
@@ -634,9 +639,10 @@ def kv_read(slots: torch.Tensor, cache: torch.Tensor, pages: int, kv_heads: int,
     T = _slots(slots)
     if dtype not in _DTYPE_CODE:
         raise ValueError(f"dtype {dtype} is not fp16 or bf16")
-    shape, device = (T, kv_heads, head_dim), slots.device
+    shape, device = (T, kv_heads, head_dim), slots.get_device()
     if out is None:
-        k, v = torch.empty(shape, dtype=dtype, device=device), torch.empty(shape, dtype=dtype, device=device)
+        k = torch.empty(shape, dtype=dtype, device=slots.device)
+        v = torch.empty_like(k)
     else:
         k, v = out
         _heads("k", k, shape, dtype, device)
@@ -644,7 +650,7 @@ def kv_read(slots: torch.Tensor, cache: torch.Tensor, pages: int, kv_heads: int,
     nbytes = _cache_bytes(cache, device)
     status = (_lib or load_library()).w4a16_kv_read(
         slots.data_ptr(), T, cache.data_ptr(), nbytes, pages, kv_heads, head_dim, page_size, kind, _DTYPE_CODE[dtype],
-        k.data_ptr(), k.stride(0), k.stride(1), v.data_ptr(), v.stride(0), v.stride(1), _raw_stream(slots.get_device()))
+        k.data_ptr(), k.stride(0), k.stride(1), v.data_ptr(), v.stride(0), v.stride(1), _raw_stream(device))
     if status:
         _check(status)
     return k, v
@@ -671,18 +677,18 @@ def attention(q: torch.Tensor, cache: torch.Tensor, table: torch.Tensor, lengths
     if q.dim() != 3:
         raise ValueError("q must be [B, q_heads, head_dim]")
     B, Hq, D = shape = q.shape
-    device, dtype = q.device, q.dtype
+    device, dtype = q.get_device(), q.dtype
     _heads("q", q, shape, dtype, device)
     if out is None:
-        out = torch.empty(shape, dtype=dtype, device=device)
+        out = _empty(q, shape)
     else:
         _heads("out", out, shape, dtype, device)
-    if table.dtype is not torch.int32 or table.device != device:
+    if table.dtype is not torch.int32 or table.get_device() != device:
         _need_cuda("table", table, torch.int32)
         _same_device(q, table=table)
     if table.dim() != 2 or table.shape[0] != B or (table.shape[1] > 1 and table.stride(1) != 1):
         raise ValueError(f"table must be [B={B}, width] with unit column stride")
-    if lengths.dtype is not torch.int32 or lengths.device != device:
+    if lengths.dtype is not torch.int32 or lengths.get_device() != device:
         _need_cuda("lengths", lengths, torch.int32)
         _same_device(q, lengths=lengths)
     if lengths.shape != (B,) or not lengths.is_contiguous():
@@ -692,13 +698,13 @@ def attention(q: torch.Tensor, cache: torch.Tensor, table: torch.Tensor, lengths
     ws_ptr, ws_bytes = None, 0
     if B > 0:
         need = attention_workspace_size(B, Hq, kv_heads, D, page_size, width, window, kind)
-        ws = (workspace or _default_workspace(device, "attention")).get(need)
+        ws = (workspace or _default_workspace(q.device, "attention")).get(need)
         ws_ptr, ws_bytes = ws.data_ptr(), ws.numel()
     status = (_lib or load_library()).w4a16_attention(
         q.data_ptr(), q.stride(0), q.stride(1), B, Hq, cache.data_ptr(), nbytes, pages, kv_heads, D, page_size, kind,
         _DTYPE_CODE[dtype], table.data_ptr(), width, table.stride(0) if B > 1 else width, lengths.data_ptr(), window,
         D ** -0.5 if scale is None else scale, out.data_ptr(), out.stride(0), out.stride(1), ws_ptr, ws_bytes,
-        _raw_stream(q.get_device()))
+        _raw_stream(device))
     if status:
         _check(status)
     return out
