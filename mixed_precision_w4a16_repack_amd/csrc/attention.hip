@@ -689,12 +689,21 @@ __global__ __launch_bounds__(256, (kPerCU<KIND, D, HT>)) void attention_kernel(A
                     float2 pml[kFan];
                     floatx4 po[kFan];
                     Join j;
-                    load_coherent8(from, (head * Pt::kStride + 4 + d) * 4, (head * Pt::kStride + pair) * 4, po, pml);
+                    const uint32_t at4 = (head * Pt::kStride + 4 + d) * 4, at2 = (head * Pt::kStride + pair) * 4;
+                    auto add = [&](int most) {
 #pragma unroll
-                    for (int i = 0; i < kFan; ++i) j.m = fmaxf(j.m, pml[i].x);
+                        for (int i = 0; i < most; ++i) j.m = fmaxf(j.m, pml[i].x);
 #pragma unroll
-                    for (int i = 0; i < kFan; ++i)
-                        if (i < size) j.add(pml[i].x, pml[i].y, po[i]);
+                        for (int i = 0; i < most; ++i)
+                            if (i < size) j.add(pml[i].x, pml[i].y, po[i]);
+                    };
+                    if (size <= kFan / 2) {
+                        load_coherent8_half(from, at4, at2, po, pml);
+                        add(kFan / 2);
+                    } else {
+                        load_coherent8(from, at4, at2, po, pml);
+                        add(kFan);
+                    }
                     if (done) {
                         store_out<DT>(a, b, head0 + head, d, j);
                     } else {  // in the leader's place

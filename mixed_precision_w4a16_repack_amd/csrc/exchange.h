@@ -76,6 +76,23 @@ __device__ __forceinline__ void load_coherent8(const float* const (&p)[8], uint3
         : "v"(off4), "v"(off2), "s"(p[0]), "s"(p[1]), "s"(p[2]), "s"(p[3]), "s"(p[4]), "s"(p[5]), "s"(p[6]), "s"(p[7])
         : "memory");
 }
+// The first four of them only.
+__device__ __forceinline__ void load_coherent8_half(const float* const (&p)[8], uint32_t off4, uint32_t off2,
+                                                    floatx4 (&v)[8], float2 (&w)[8]) {
+    asm volatile(
+        "global_load_dwordx4 %0, %8, %10 sc1\n\t"
+        "global_load_dwordx4 %1, %8, %11 sc1\n\t"
+        "global_load_dwordx4 %2, %8, %12 sc1\n\t"
+        "global_load_dwordx4 %3, %8, %13 sc1\n\t"
+        "global_load_dwordx2 %4, %9, %10 sc1\n\t"
+        "global_load_dwordx2 %5, %9, %11 sc1\n\t"
+        "global_load_dwordx2 %6, %9, %12 sc1\n\t"
+        "global_load_dwordx2 %7, %9, %13 sc1\n\t"
+        "s_waitcnt vmcnt(0)"
+        : "=&v"(v[0]), "=&v"(v[1]), "=&v"(v[2]), "=&v"(v[3]), "=&v"(w[0]), "=&v"(w[1]), "=&v"(w[2]), "=&v"(w[3])
+        : "v"(off4), "v"(off2), "s"(p[0]), "s"(p[1]), "s"(p[2]), "s"(p[3])
+        : "memory");
+}
 // Waits until every vector memory access this wave issued has completed
 // (write-through stores: reached the coherence point).
 __device__ __forceinline__ void wait_vector_memory() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
