@@ -581,16 +581,37 @@ __global__ __launch_bounds__(256, (kPerCU<KIND, D, HT>)) void attention_kernel(A
     // Few tiles: a workgroup per kMinTiles of one head, so that most heads
     // need no join. Else equal runs of the list, across heads; a head takes
     // kHeadCost slots before its tiles' ones.
-    const bool by_chunk = units * (all_sums & kChunkMask) <= wgs;
-    const int64_t all = units * (by_chunk ? all_sums & kChunkMask : all_sums >> kChunkBits);
-    const int64_t per = by_chunk ? 1 : (all + wgs - 1) >> __builtin_ctz(wgs);
+    int chunk = kMinTiles;
+    bool by_chunk = units * (all_sums & kChunkMask) <= wgs;
+    int64_t all = units * (by_chunk ? all_sums & kChunkMask : all_sums >> kChunkBits);
+    int64_t per = by_chunk ? 1 : (all + wgs - 1) >> __builtin_ctz(wgs);
+    int64_t seq_items = by_chunk ? sums & kChunkMask : sums >> kChunkBits;  // of sequence base + lane, when base is found
+    int64_t seq_to = by_chunk ? sums_to & kChunkMask : sums_to >> kChunkBits;
+    if (!by_chunk && run == 1 && units * a.B < wgs && 16 * units * a.B >= wgs) {
+        // Heads that are cut anyway, but in few parts, are cut evenly if that
+        // fits: a run across two heads starts and ends twice (64 x 4096 tokens
+        // of one kv head, 32 query heads: 36 and 32 us; 4 x 9000 of 8 heads of
+        // 256 in int8 39 and 33).
+        const int n = Span(a, length).count;
+        const int most = (int)per + A::kHeadCost / 2, least = (int)per - A::kHeadCost;
+        for (int c = most; c >= kMinTiles && c >= least; c -= A::kHeadCost / 2) {
+            const int64_t items = (n + c - 1) / c, to = wave_scan(items);
+            if (units * read_lane(to, 63) > wgs) break;
+            chunk = c;
+            by_chunk = true;
+            seq_items = items;
+            seq_to = to;
+        }
+        if (by_chunk) {
+            all = units * read_lane(seq_to, 63);
+            per = 1;
+        }
+    }
     int64_t pos = wg * per;
     const int64_t end = pos + per < all ? pos + per : all;
     if (pos >= end) return;
 
     // The block of 64 sequences that holds `pos`, and in it the sequence.
-    int64_t seq_items = by_chunk ? sums & kChunkMask : sums >> kChunkBits;  // of sequence base + lane, when base is found
-    int64_t seq_to = by_chunk ? sums_to & kChunkMask : sums_to >> kChunkBits;
     int64_t base = 0;
     auto block_at = [&](int64_t first, int64_t before) {  // `before`: items of the sequences before it
         base = first;
@@ -619,8 +640,8 @@ __global__ __launch_bounds__(256, (kPerCU<KIND, D, HT>)) void attention_kernel(A
             int from = (int)(pos - unit_begin), upto = (int)(stop - unit_begin);
             pos = stop;
             if (by_chunk) {
-                from *= kMinTiles;
-                upto = upto * kMinTiles < sp.count ? upto * kMinTiles : sp.count;
+                from *= chunk;
+                upto = upto * chunk < sp.count ? upto * chunk : sp.count;
             } else {
                 from = from > A::kHeadCost ? from - A::kHeadCost : 0;
                 upto -= A::kHeadCost;
@@ -658,7 +679,7 @@ __global__ __launch_bounds__(256, (kPerCU<KIND, D, HT>)) void attention_kernel(A
             if (whole) continue;
 
             // Join: of kFan workgroups, by the last of them; then of those results.
-            const int first = by_chunk ? wg - from / kMinTiles : divide(unit_begin + A::kHeadCost, per);
+            const int first = by_chunk ? wg - from / chunk : divide(unit_begin + A::kHeadCost, per);
             const int last = by_chunk ? first + items - 1 : divide(unit_end - 1, per);
             int rank = wg - first, count = last - first + 1, step = 1;
             uint32_t* counters = a.counters;

@@ -493,6 +493,15 @@ def test_attention_many_sequences(B, most, zeros, kind):
     Batch("many", lens.tolist(), 2, 64, 32, kind, "bf16").check(8)
 
 
+@pytest.mark.parametrize("kind,most,window", [(ref.KV_ACT, 16000, 0), (ref.KV_ACT, 20000, 9001), (ref.KV_INT8, 34000, 0)])
+def test_attention_few_heads_cut_evenly(kind, most, window):
+    """Fewer heads than workgroups and more tiles than the smallest parts would cover: cut into equal larger parts."""
+    r = np.random.default_rng(7)
+    lens = r.integers(most // 3, most, 20)
+    lens[3], lens[11] = 0, 40
+    Batch("even", lens.tolist(), 1, 64, 32, kind, "f16").check(20, window=window)
+
+
 @pytest.mark.parametrize("kind", KINDS)
 def test_attention_split_windows_and_wide_groups(kind):
     """Heads shared by workgroups with a window that starts inside a tile, and more query heads than one operand."""
