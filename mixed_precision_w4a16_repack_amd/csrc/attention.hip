@@ -31,7 +31,8 @@
 //
 // Work is divided by tiles over a fixed number of workgroups, computed on the
 // device from the lengths (the host does not know them): each takes an equal
-// run of the list of all (sequence, kv head, tile), whatever the lengths are.
+// run of the list of all (sequence, kv head, tile), whatever the lengths are,
+// or, where there are few heads or few tiles, an equal part of one head.
 // A head's start (query, page table, first tile: three waits) and end (four
 // waves joined) count as kHeadBytes more: without that, 64 sequences from 0 to
 // 6000 tokens took 112 us, the workgroups of the short ones being last, and
