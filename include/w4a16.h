@@ -434,7 +434,8 @@ w4a16_status w4a16_attention_workspace_size(int64_t B, int32_t q_heads, int32_t 
  * (no float atomics: the order of every sum follows from the sizes and lengths).
  * Probabilities are rounded to the 16 bits of the matrix operand (the act
  * dtype's, fp16's over an int8 cache); scores, their maximum and every sum are
- * fp32. W4A16_ERR_SIZE if the cache or the workspace is too small. The
+ * fp32, and a sum of values that passes the fp32 range before it is divided
+ * gives infinity. W4A16_ERR_SIZE if the cache or the workspace is too small. The
  * workspace must be 256-byte aligned. */
 w4a16_status w4a16_attention(const void *q, int64_t q_bs, int64_t q_hs, int64_t B, int32_t q_heads, const void *cache,
                              size_t cache_bytes, int64_t pages, int32_t kv_heads, int32_t head_dim, int32_t page_size,

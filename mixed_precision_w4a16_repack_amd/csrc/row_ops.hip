@@ -7,10 +7,11 @@
 // to read back. Statistics, products and the scale are fp32; y is rounded
 // once (to 16 bits, or to a code).
 //
-// What bounds them: bytes for many rows (8192 x 4096 with residual 42 us for 268
-// MB, 6.4 TB/s; 2048 x 14336 of the gate 28 us, 6.3 TB/s; torch's copy of as
-// many bytes reaches 5.3), the chain load - reduce - store for few (1 x 4096
-// 2.3 us, 64 x 4096 to codes 3.7 us). A row is read once: it stays in registers
+// What bounds them: bytes for many rows (8192 x 4096 with residual 41 us for 268
+// MB, 6.5 TB/s; 2048 x 14336 of the gate 28 us, 6.2 TB/s; torch's copy of as
+// many bytes reaches 5.3; rows of an odd width 4.9, their 16-byte pieces
+// crossing lines), the chain load - reduce - store for few (1 x 4096
+// 2.3 us, 64 x 4096 to codes 3.8 us). A row is read once: it stays in registers
 // up to 32768 columns.
 //
 // Rows need no alignment beyond their element's: 16-byte accesses are made
@@ -20,34 +21,38 @@
 #include "internal.h"
 
 namespace w4a16 {
+
+int64_t gate_workgroups(int64_t M, int64_t K) { return (M * ((K + 7) / 8) + 255) / 256; }
+
 namespace {
 
 typedef u32x4 u32x4_any __attribute__((aligned(2)));
 
-// Eight elements of a row of K from p (n of them inside the row, 1 .. 8; the
-// rest 0). The end of a row of 8 or more is taken from its last 8 elements.
+// Eight elements of a row of K from p, n of them inside the row (1 .. 8). The
+// end of a row of 8 or more is taken from its last 8 elements, so that every
+// lane makes one load and none waits for another's; align8 then moves them
+// to the front (the rest 0). Shorter rows are read element by element.
 __device__ __forceinline__ u32x4 load8(const uint16_t* p, int64_t n, int64_t K) {
-    if (n >= 8) return *reinterpret_cast<const u32x4_any*>(p);
+    if (K >= 8) return *reinterpret_cast<const u32x4_any*>(p + (n < 8 ? n - 8 : 0));
     u32x4 v{0u, 0u, 0u, 0u};
-    if (K >= 8) {
-        const u32x4 w = *reinterpret_cast<const u32x4_any*>(p + n - 8);
-        const int drop = 8 - (int)n;  // leading elements that belong to the chunk before
-        uint64_t lo = (uint64_t)w[1] << 32 | w[0], hi = (uint64_t)w[3] << 32 | w[2];
-        if (drop >= 4) {
-            lo = hi;
-            hi = 0;
-        }
-        const int bits = drop % 4 * 16;
-        if (bits != 0) {
-            lo = lo >> bits | hi << (64 - bits);
-            hi >>= bits;
-        }
-        return u32x4{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
-    }
 #pragma unroll
     for (int e = 0; e < 7; ++e)
         if (e < n) v[e >> 1] |= (uint32_t)p[e] << (16 * (e & 1));
     return v;
+}
+__device__ __forceinline__ void align8(u32x4& v, int64_t n) {  // n < 8
+    const int drop = 8 - (int)n;  // leading elements that belong to the chunk before
+    uint64_t lo = (uint64_t)v[1] << 32 | v[0], hi = (uint64_t)v[3] << 32 | v[2];
+    if (drop >= 4) {
+        lo = hi;
+        hi = 0;
+    }
+    const int bits = drop % 4 * 16;
+    if (bits != 0) {
+        lo = lo >> bits | hi << (64 - bits);
+        hi >>= bits;
+    }
+    v = u32x4{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
 }
 
 __device__ __forceinline__ void store8(uint16_t* p, int64_t n, const u32x4& v) {
@@ -148,21 +153,29 @@ __global__ __launch_bounds__(kThreads<TPR>) void norm_kernel(NormArgs a) {
     const int64_t chunks = (a.K + 7) / 8;
     constexpr int R = CPT > 0 ? CPT : 1;
     float h[R][8];
-    u32x4 w[R];
+    u32x4 w[R], vx[R], vr[R];
+    if constexpr (CPT == 0) vr[0] = u32x4{0u, 0u, 0u, 0u};
     float sum = 0.0f;
     uint32_t amax = 0u;
 
-    auto load = [&](int64_t c, float* hc, u32x4& wc) {
+    auto load = [&](int64_t c, int i) {
         const int64_t n = a.K - 8 * c;
-        const u32x4 vx = load8(x + 8 * c, n, a.K);
-        wc = load8(a.weight + 8 * c, n, a.K);
+        vx[i] = load8(x + 8 * c, n, a.K);
+        if (a.residual != nullptr) vr[i] = load8(r + 8 * c, n, a.K);
+        w[i] = load8(a.weight + 8 * c, n, a.K);
+    };
+    auto sum_up = [&](int64_t c, int i) {  // h = x (+ residual)
+        const int64_t n = a.K - 8 * c;
+        if (n < 8 && a.K >= 8) {
+            align8(vx[i], n);
+            align8(w[i], n);
+            align8(vr[i], n);
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) h[i][e] = elem<DT>(vx[i], e);
         if (a.residual != nullptr) {
-            const u32x4 vr = load8(r + 8 * c, n, a.K);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) hc[e] = elem<DT>(vx, e) + elem<DT>(vr, e);
-        } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) hc[e] = elem<DT>(vx, e);
+            for (int e = 0; e < 8; ++e) h[i][e] += elem<DT>(vr[i], e);
         }
     };
     auto reduce = [&](float* hc, const u32x4& wc) {
@@ -192,19 +205,20 @@ __global__ __launch_bounds__(kThreads<TPR>) void norm_kernel(NormArgs a) {
 #pragma unroll
         for (int i = 0; i < R; ++i) {
             const int64_t c = t + (int64_t)TPR * i;
-            if (c < chunks) {
-                load(c, h[i], w[i]);
-            } else {
-                w[i] = u32x4{0u, 0u, 0u, 0u};
+            vx[i] = vr[i] = w[i] = u32x4{0u, 0u, 0u, 0u};
+            if (c < chunks) load(c, i);
+        }
 #pragma unroll
-                for (int e = 0; e < 8; ++e) h[i][e] = 0.0f;
-            }
+        for (int i = 0; i < R; ++i) {
+            const int64_t c = t + (int64_t)TPR * i;
+            sum_up(c < chunks ? c : 0, i);
         }
 #pragma unroll
         for (int i = 0; i < R; ++i) reduce(h[i], w[i]);
     } else {
         for (int64_t c = t; c < chunks; c += TPR) {
-            load(c, h[0], w[0]);
+            load(c, 0);
+            sum_up(c, 0);
             reduce(h[0], w[0]);
         }
     }
@@ -222,7 +236,8 @@ __global__ __launch_bounds__(kThreads<TPR>) void norm_kernel(NormArgs a) {
         }
     } else {
         for (int64_t c = t; c < chunks; c += TPR) {
-            load(c, h[0], w[0]);
+            load(c, 0);
+            sum_up(c, 0);
             finish(c, h[0], w[0], rs, cs);
         }
     }
@@ -237,18 +252,26 @@ __device__ __forceinline__ void gate8(const u32x4& g, const u32x4& u, float* y) 
     }
 }
 
-// 16-bit output: chunks of 8 columns, 256 per workgroup.
+// 16-bit output: the chunks of 8 columns of all rows in one list, so that
+// narrow rows and rows' ends leave no threads idle.
 template <int DT>
-__global__ __launch_bounds__(256) void gate_kernel(GateArgs a, int64_t blocks_per_row) {
-    const int64_t m = blockIdx.x / blocks_per_row;
-    const int64_t c = (blockIdx.x % blocks_per_row) * 256 + threadIdx.x;
-    const int64_t n = a.K - 8 * c;
-    if (n <= 0) return;
-    const uint16_t* x = a.x + m * a.ldx + 8 * c;
-    const u32x4 g = load8(x, n, a.K), u = load8(x + a.K, n, a.K);
+__global__ __launch_bounds__(256) void gate_kernel(GateArgs a, uint32_t chunks) {  // of a row
+    const int64_t first = (int64_t)blockIdx.x * 256;
+    const int64_t m0 = first >> 32 == 0 ? (int64_t)((uint32_t)first / chunks) : first / chunks;
+    const uint32_t at = (uint32_t)(first - m0 * chunks) + threadIdx.x;
+    const uint32_t rows = at / chunks, c = at - rows * chunks;
+    const int64_t m = m0 + rows;
+    if (m >= a.M) return;
+    const int64_t n = a.K - 8 * (int64_t)c;
+    const uint16_t* x = a.x + m * a.ldx + 8 * (int64_t)c;
+    u32x4 g = load8(x, n, a.K), u = load8(x + a.K, n, a.K);
+    if (n < 8 && a.K >= 8) {
+        align8(g, n);
+        align8(u, n);
+    }
     float y[8];
     gate8<DT>(g, u, y);
-    store8(a.y + m * a.ldy + 8 * c, n, pack8<DT>(y));
+    store8(a.y + m * a.ldy + 8 * (int64_t)c, n, pack8<DT>(y));
 }
 
 // Codes: one row on TPR threads, held in registers (CPT > 0) or computed
@@ -338,8 +361,8 @@ void norm_dispatch(const NormArgs& a, hipStream_t stream) {
 template <int DT>
 void gate_dispatch(const GateArgs& a, hipStream_t stream) {
     if (a.q == nullptr) {
-        const int64_t bpr = (a.K + 2047) / 2048;
-        hipLaunchKernelGGL((gate_kernel<DT>), dim3((unsigned)(a.M * bpr)), dim3(256), 0, stream, a, bpr);
+        hipLaunchKernelGGL((gate_kernel<DT>), dim3((unsigned)gate_workgroups(a.M, a.K)), dim3(256), 0, stream, a,
+                           (uint32_t)((a.K + 7) / 8));
         return;
     }
     by_width(a.M, a.K, [&](auto tpr, auto cpt) {
@@ -356,7 +379,6 @@ int64_t row_threads(int64_t M, int64_t K) {
     return n;
 }
 
-int64_t gate_workgroups(int64_t M, int64_t K) { return M * ((K + 2047) / 2048); }
 
 hipError_t launch_norm(const NormArgs& a, int dtype, hipStream_t stream) {
     if (dtype == 0) norm_dispatch<0>(a, stream);
