@@ -135,6 +135,19 @@ def test_a8_codes_of_tiny_and_huge_rows():
     check_codes(qa.cpu(), xs.cpu(), ref.silu_mul(torch.cat([gate, up], 1)), 2.0**-16)
 
 
+@pytest.mark.parametrize("dtype", BOTH)
+def test_silu_mul_a8_of_large_gates(dtype):
+    """Gates from -80 to 80: the scale and the codes stay within 2^-20 of the definition at any of them (the codes'
+    quotient: 7 roundings of 2^-24 each in the value and in the maximum, and two)."""
+    g = gen("gate a8 large", dtype)
+    K = 4096
+    gate = (torch.linspace(-80, 80, K) + randn(g, 40, K, dtype=torch.float32, std=0.1)).to(DTYPES[dtype])
+    gate[::2] = -gate[::2].abs()  # rows of small results only
+    x = torch.cat([gate, randn(g, 40, K, dtype=DTYPES[dtype])], 1)
+    qa, xs = w4.silu_mul_a8(x.to(DEV))
+    check_codes(qa.cpu(), xs.cpu(), ref.silu_mul(x), 2.0**-20)
+
+
 def test_a8_rows_with_a_nan_keep_it():
     x = torch.ones(3, 512, dtype=torch.float16)
     x[1, 77] = float("nan")
