@@ -277,14 +277,18 @@ __global__ __launch_bounds__(256) void gate_kernel(GateArgs a, uint32_t chunks) 
 // The same for codes, whose rounding steps are far apart: an error of the
 // quotient moves a code to its neighbour with that probability, and the fast
 // form is off by |g| last places (exp's argument), which is visible next to
-// fp16's rounding. Here the argument is in two parts: a few last places at any
-// g (4096 x 3000 to codes 13.4 us, 12.6 with the fast form).
+// fp16's rounding. Here the argument is in two parts: a few last places
+// (4096 x 3000 to codes 13.4 us, 12.6 with the fast form). The second part
+// counts only where the first one's exp is neither 0 nor infinity: outside,
+// 1 + e is 1 or infinity whatever it is, and inf * (rest <= 0) + inf, or the
+// rest of an infinite argument, would be NaN.
 __device__ __forceinline__ float gate_exact(float g, float u) {
     constexpr float kLog2e = 1.44269504f, kRest = 1.92596299e-8f, kLn2 = 0.693147181f;
     const float p = -g * kLog2e;
     const float rest = __builtin_fmaf(-g, kRest, __builtin_fmaf(-g, kLog2e, -p));
-    const float e = __builtin_amdgcn_exp2f(p);
-    return g * __builtin_amdgcn_rcpf(1.0f + __builtin_fmaf(e, rest * kLn2, e)) * u;
+    float e = __builtin_amdgcn_exp2f(p);
+    if (__builtin_fabsf(p) < 128.0f) e = __builtin_fmaf(e, rest * kLn2, e);
+    return g * __builtin_amdgcn_rcpf(1.0f + e) * u;
 }
 
 // Codes: one row on TPR threads, held in registers (CPT > 0) or computed
