@@ -252,17 +252,41 @@ class Workspace:
     """A zero-initialised device workspace that grows on demand.
 
     The library returns the counter region to zero after every call, so one
-    workspace serves every shape; calls that share it must be stream-ordered.
+    workspace serves every shape; calls that share it must be stream-ordered,
+    replays of graphs that were captured with it among them.
+
+    For calls that are captured into a graph, size the workspace first, by one
+    call of the same sizes before the capture, and keep it as long as the graph.
+    Former buffers stay allocated when it grows, since a graph may hold their
+    address (it at least doubles, so they are never more than the present one).
+    A captured call that needs more than the buffer holds, or that is given no
+    workspace, takes memory of the graph's own, whose counter region is cleared
+    at each replay (one fill kernel more).
     """
 
-    def __init__(self, device):
+    def __init__(self, device, default: bool = False):
         self.device = torch.device(device)
         self.buf: torch.Tensor | None = None
+        # A default workspace belongs to one stream's eager calls: a graph may
+        # be replayed beside them, on any stream.
+        self._eager_only = default
+        self._former: list[torch.Tensor] = []
 
     def get(self, nbytes: int) -> torch.Tensor | None:
         if nbytes == 0:
             return self.buf
-        if self.buf is None or self.buf.numel() < nbytes:
+        fits = self.buf is not None and self.buf.numel() >= nbytes
+        if fits and not self._eager_only:
+            return self.buf
+        if torch.cuda.is_current_stream_capturing():
+            # Not kept as buf: what is captured clears it at replays only.
+            buf = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
+            buf[: min(nbytes, workspace_counter_bytes())].zero_()
+            return buf
+        if not fits:
+            if self.buf is not None and not self._eager_only:
+                self._former.append(self.buf)
+                nbytes = max(nbytes, 2 * self.buf.numel())
             self.buf = torch.zeros(nbytes, dtype=torch.uint8, device=self.device)
         return self.buf
 
@@ -275,11 +299,11 @@ def _default_workspace(device, kind: str = "w4a16") -> Workspace:
     w4a16_gemm and w4a8_gemm get separate ones: w4a16_gemm needs the counter
     region at the start of its workspace to be zero, and w4a8_gemm writes its
     partial results from the start of its own."""
-    index = torch.device(device).index
+    index = (device if isinstance(device, torch.device) else torch.device(device)).index
     key = (kind, index, _raw_stream(torch.cuda.current_device() if index is None else index))
     ws = _workspaces.get(key)
     if ws is None:
-        ws = _workspaces[key] = Workspace(device)
+        ws = _workspaces[key] = Workspace(device, default=True)
     return ws
 
 
@@ -671,7 +695,8 @@ def attention(q: torch.Tensor, cache: torch.Tensor, table: torch.Tensor, lengths
     """Attention of one new token per sequence over the cache: q [B, q_heads, head_dim] -> the same shape.
 
     ``table`` [B, width] int32 holds each sequence's pages, ``lengths`` [B] int32 its tokens (the new one
-    included); ``window`` > 0 sees only the last tokens; ``scale`` defaults to head_dim ** -0.5."""
+    included); ``window`` > 0 sees only the last tokens; ``scale`` defaults to head_dim ** -0.5. For calls that
+    are captured into a graph see ``Workspace``."""
     if not q.is_cuda or q.dtype not in _DTYPE_CODE:
         _need_cuda("q", q, (torch.float16, torch.bfloat16))
     if q.dim() != 3:
@@ -695,16 +720,17 @@ def attention(q: torch.Tensor, cache: torch.Tensor, table: torch.Tensor, lengths
         raise ValueError(f"lengths must be a contiguous [B={B}] tensor")
     nbytes = _cache_bytes(cache, device)
     width = table.shape[1]
+    stream = _raw_stream(device)
     ws_ptr, ws_bytes = None, 0
     if B > 0:
         need = attention_workspace_size(B, Hq, kv_heads, D, page_size, width, window, kind)
-        ws = (workspace or _default_workspace(q.device, "attention")).get(need)
+        # the first look is _default_workspace's own, without building the device object
+        ws = (workspace or _workspaces.get(("attention", device, stream)) or _default_workspace(q.device, "attention")).get(need)
         ws_ptr, ws_bytes = ws.data_ptr(), ws.numel()
     status = (_lib or load_library()).w4a16_attention(
         q.data_ptr(), q.stride(0), q.stride(1), B, Hq, cache.data_ptr(), nbytes, pages, kv_heads, D, page_size, kind,
         _DTYPE_CODE[dtype], table.data_ptr(), width, table.stride(0) if B > 1 else width, lengths.data_ptr(), window,
-        D ** -0.5 if scale is None else scale, out.data_ptr(), out.stride(0), out.stride(1), ws_ptr, ws_bytes,
-        _raw_stream(device))
+        D ** -0.5 if scale is None else scale, out.data_ptr(), out.stride(0), out.stride(1), ws_ptr, ws_bytes, stream)
     if status:
         _check(status)
     return out

@@ -78,3 +78,106 @@ def test_silu_mul_a8_of_an_infinite_gate(dtype):
     x[1, 7] = float("inf")
     _, xs = w4.silu_mul_a8(x.to(DEV))
     assert xs[1].item() == float("inf") and bool(xs[[0, 2]].isfinite().all())
+
+
+# ---------------------------------------------------------------- workspaces and graphs
+
+
+def split_attention(n, kind, seed):
+    """An attention call on one long sequence, whose heads many workgroups share: (call, eager result)."""
+    H, D, P, Hq = 1, 64, 32, 8
+    g = gen("split attention", n, kind, seed)
+    pages = -(-n // P)
+    cache = torch.zeros(w4.kv_cache_size(pages, H, D, P, kind), dtype=torch.uint8, device=DEV)
+    k, v = (randn(g, n, H, D, dtype=torch.float16).to(DEV) for _ in range(2))
+    w4.kv_write(k, v, torch.arange(n, device=DEV), cache, pages, P, kind)
+    table = torch.arange(pages, dtype=torch.int32, device=DEV)[None]
+    lengths = torch.tensor([n], dtype=torch.int32, device=DEV)
+    q = randn(g, 1, Hq, D, dtype=torch.float16).to(DEV)
+
+    def call(**kw):
+        return w4.attention(q, cache, table, lengths, pages, H, P, kind, **kw)
+
+    return call, call()
+
+
+@pytest.mark.parametrize("kind", [w4.KV_ACT, w4.KV_INT8])
+def test_graphs_captured_without_a_workspace_replay_in_any_order(kind):
+    calls = [split_attention(n, kind, i) for i, n in enumerate((20000, 15000))]
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for call, _ in calls:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            outs.append(call())
+        graphs.append(graph)
+    for i in (1, 0, 1, 1, 0):
+        outs[i].fill_(7.0)
+        graphs[i].replay()
+        torch.cuda.synchronize()
+        assert torch.equal(outs[i], calls[i][1]), f"graph {i}"
+        for call, want in calls:
+            assert torch.equal(call(), want)
+
+
+def test_products_captured_without_a_workspace_replay_in_any_order():
+    """Split-K products: their arrival counters live in the workspace too."""
+    import w4a16_inputs as wi
+    from tests.gpu_cases import repack
+
+    graphs, outs, wants = [], [], []
+    for seed, (M, N, K, G) in enumerate([(16, 4096, 14336, 128), (5, 1024, 4096, 64)]):
+        assert w4.workspace_size(M, N, K, G) > 0
+        case = wi.make_case(70 + seed, M, N, K, G, wi.UINT4B8, "f16")
+        packed, A = repack(case), case.A.to(DEV)
+        wants.append(w4.gemm(A, packed, N, K, G, wi.UINT4B8))
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            outs.append(w4.gemm(A, packed, N, K, G, wi.UINT4B8))
+        graphs.append((graph, packed, A))
+    for i in (1, 0, 1, 0):
+        outs[i].fill_(7.0)
+        graphs[i][0].replay()
+        torch.cuda.synchronize()
+        assert torch.equal(outs[i], wants[i]), f"graph {i}"
+
+
+def test_a_larger_eager_call_between_replays_leaves_the_graph_its_workspace():
+    small, want = split_attention(600, w4.KV_ACT, 0)
+    large, want_large = split_attention(30000, w4.KV_ACT, 1)
+    ws = w4.Workspace(DEV)
+    assert torch.equal(small(workspace=ws), want)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = small(workspace=ws)
+    before = ws.buf.numel()
+    for rep in range(4):
+        out.fill_(7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want), f"replay {rep}"
+        assert torch.equal(large(workspace=ws), want_large)
+        assert ws.buf.numel() > before
+        # memory that the allocator hands out now is not the graph's
+        other = [torch.full((before,), 0x5A, dtype=torch.uint8, device=DEV) for _ in range(4)]
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(bool((t == 0x5A).all()) for t in other)
+        assert torch.equal(out, want)
+
+
+def test_a_workspace_first_used_in_a_capture_serves_eager_calls_before_the_replay():
+    call, want = split_attention(9000, w4.KV_INT8, 0)
+    ws = w4.Workspace(DEV)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = call(workspace=ws)
+    for rep in range(3):
+        assert torch.equal(call(workspace=ws), want)
+        out.fill_(7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want), f"replay {rep}"
