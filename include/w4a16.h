@@ -333,7 +333,9 @@ w4a16_status w4a8_gemm(const int8_t *qa, const float *xs, int64_t M, int64_t ldq
  *   y            [M, ldy] act dtype, ldy >= K; may be x itself if
  *                residual_out is not
  * eps >= 0 and finite. M == 0 is a no-op. A row whose sum of squares passes
- * the fp32 range, or that holds a NaN, has no defined values. */
+ * the fp32 range, whose mean square plus eps is below 2^-100 (about 1e-30; the
+ * squares are then below that range), or that holds a NaN, has no defined
+ * values. */
 w4a16_status w4a16_rmsnorm(const void *x, int64_t M, int64_t K, int64_t ldx, int32_t dtype, const void *weight,
                            float eps, const void *residual, int64_t ldr, void *residual_out, int64_t ldro, void *y,
                            int64_t ldy, hipStream_t stream);
@@ -341,8 +343,8 @@ w4a16_status w4a16_rmsnorm(const void *x, int64_t M, int64_t K, int64_t ldx, int
 /* The same norm with y as the input of w4a8_gemm: codes and a scale per row,
  * quantised from the fp32 values,
  *   xs[m] = max_k |y[m, k]| / 127,  qa[m, k] = rint(y[m, k] / xs[m])
- * with w4a8_quantize's order of codes, row of zeros and rules for K, qa, ldq
- * and xs. A quotient within fp32's rounding of a tie may go to either code. */
+ * with w4a8_quantize's order of codes, row of zeros (at any eps) and rules for
+ * K, qa, ldq and xs. A quotient within fp32's rounding of a tie may go to either code. */
 w4a16_status w4a8_rmsnorm(const void *x, int64_t M, int64_t K, int64_t ldx, int32_t dtype, const void *weight,
                           float eps, const void *residual, int64_t ldr, void *residual_out, int64_t ldro, int8_t *qa,
                           int64_t ldq, float *xs, hipStream_t stream);

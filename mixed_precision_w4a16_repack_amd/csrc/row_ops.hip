@@ -227,7 +227,8 @@ __global__ __launch_bounds__(kThreads<TPR>) void norm_kernel(NormArgs a) {
     // The codes do not depend on rs: it scales the row and its maximum alike.
     const float top = __builtin_bit_cast(float, amax);
     const CodeScale cs(top);
-    if (OUT8 && t == 0) a.xs[m] = top * rs / 127.0f;
+    // A row of zeros has scale 0 also where eps is 0 and rs infinite.
+    if (OUT8 && t == 0) a.xs[m] = top == 0.0f ? 0.0f : top * rs / 127.0f;
     if constexpr (CPT > 0) {
 #pragma unroll
         for (int i = 0; i < R; ++i) {

@@ -10,8 +10,8 @@ import torch
 
 import mixed_precision_w4a16_repack_amd as w4
 from tests import operator_reference as ref
-from tests.operator_reference import DTYPES
-from tests.test_gpu_operators import BOTH, DEV, check_codes, gen, randn
+from tests.operator_reference import DTYPES, HALF, TINY
+from tests.test_gpu_operators import BOTH, DEV, REL, check_codes, gen, randn, within
 
 pytestmark = pytest.mark.gpu
 
@@ -28,6 +28,35 @@ def finite_values(dtype):
     """Every finite value of a 16-bit type."""
     v = torch.arange(-(2**15), 2**15, dtype=torch.int32).to(torch.int16).view(DTYPES[dtype])
     return v[v.isfinite()]
+
+
+# ---------------------------------------------------------------- norm
+
+
+@pytest.mark.parametrize("dtype", BOTH)
+@pytest.mark.parametrize("K", [64, 1000, 4096, 40000])
+def test_rmsnorm_a8_row_of_zeros_without_eps(K, dtype):
+    """eps = 0: a row of zeros (given so, or where the residual cancels x) has scale 0 and codes 0."""
+    g = gen("norm a8 zeros", K, dtype)
+    dt = DTYPES[dtype]
+    x, w, r = randn(g, 4, K, dtype=dt, std=3.0), randn(g, K, dtype=dt), randn(g, 4, K, dtype=dt)
+    x[1], r[1] = 0, 0
+    r[2] = -x[2]
+    qa, xs = w4.rmsnorm_a8(x.to(DEV), w.to(DEV), eps=0.0, residual=r.to(DEV))
+    assert xs[1:3].tolist() == [0.0, 0.0] and not bool(qa[1:3].any())
+    keep = [0, 3]
+    check_codes(qa.cpu()[keep], xs.cpu()[keep], ref.norm(x[keep], w, 0.0, r[keep])[0], REL)
+
+
+@pytest.mark.parametrize("K", [64, 4099])
+def test_rmsnorm_of_small_rows_without_eps(K):
+    """Down to a mean square of 2^-100: squares of elements that leave fp32's range do not count there."""
+    g = gen("norm small", K)
+    x, w = randn(g, 3, K, dtype=torch.bfloat16, std=2e-15), randn(g, K, dtype=torch.bfloat16)
+    want, _ = ref.norm(x, w, 0.0)
+    assert (x.double() ** 2).mean(1).min().item() > 2.0**-100
+    y = w4.rmsnorm(x.to(DEV), w.to(DEV), eps=0.0)
+    within(y.cpu(), want, want.abs() * (HALF["bf16"] + REL) + TINY["bf16"], "y")
 
 
 # ---------------------------------------------------------------- gate
