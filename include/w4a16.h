@@ -344,7 +344,10 @@ w4a16_status w4a16_rmsnorm(const void *x, int64_t M, int64_t K, int64_t ldx, int
  * quantised from the fp32 values,
  *   xs[m] = max_k |y[m, k]| / 127,  qa[m, k] = rint(y[m, k] / xs[m])
  * with w4a8_quantize's order of codes, row of zeros (at any eps) and rules for
- * K, qa, ldq and xs. A quotient within fp32's rounding of a tie may go to either code. */
+ * K, qa, ldq and xs. A quotient within fp32's rounding of a tie may go to either
+ * code. In bf16 a row whose largest |h * weight| is outside fp32's normal range
+ * (2^-126 .. 2^128; 0 is inside) has no defined codes and scale, whatever y
+ * would be (fp16 products cannot leave it). */
 w4a16_status w4a8_rmsnorm(const void *x, int64_t M, int64_t K, int64_t ldx, int32_t dtype, const void *weight,
                           float eps, const void *residual, int64_t ldr, void *residual_out, int64_t ldro, int8_t *qa,
                           int64_t ldq, float *xs, hipStream_t stream);
@@ -352,7 +355,9 @@ w4a16_status w4a8_rmsnorm(const void *x, int64_t M, int64_t K, int64_t ldx, int3
 /* The gate of a fused gate/up product: x [M, ldx] act dtype, ldx >= 2 K, holds
  * the gate in columns 0 .. K - 1 and the up projection in K .. 2 K - 1;
  *   y[m, k] = silu(x[m, k]) * x[m, K + k],  silu(g) = g / (1 + exp(-g))
- * y [M, ldy] act dtype, ldy >= K; must not overlap x. M == 0 is a no-op. */
+ * in fp32: a gate below about -87.3, where 1 / (1 + exp(-g)) is below fp32's
+ * normal range, gives 0. y [M, ldy] act dtype, ldy >= K; must not overlap x.
+ * M == 0 is a no-op. */
 w4a16_status w4a16_silu_mul(const void *x, int64_t M, int64_t K, int64_t ldx, int32_t dtype, void *y, int64_t ldy,
                             hipStream_t stream);
 
@@ -365,8 +370,11 @@ w4a16_status w4a8_silu_mul(const void *x, int64_t M, int64_t K, int64_t ldx, int
  * page * page_size + offset. head_dim is 64, 128, 192 or 256, page_size a
  * multiple of 32. `kind` is a w4a16_kv_kind: 16-bit values in the act dtype,
  * or int8 codes with one fp32 scale per token and head for the key and one
- * for the value (scale = max_d |x| / 127, code = rint(x / scale), a row of
- * zeros has scale 0, a row that holds a NaN scale NaN).
+ * for the value: scale = fp32(max_d |x| / 127) and code = 127 x / max_d |x|, the
+ * exact quotient rounded half to even (not x / scale, whose rounding would
+ * decide ties). A row of zeros has scale 0 and codes 0, a row that holds a NaN
+ * scale NaN, one that holds an infinity scale infinity; the codes of the last
+ * two are not defined.
  *
  * Layout: page p, head h is a record of R bytes at (p * kv_heads + h) * R,
  * where D = head_dim, P = page_size, R = 4 P D (16 bit) or 2 P D + 8 P (int8):

@@ -1,8 +1,8 @@
 // kv_cache.hip -- writing keys and values to the paged cache and reading them
 // back (layout in include/w4a16.h, kv_layout.h).
 //
-// int8: scale = fp32(max_d |x|) / 127 per token and head, code = x / scale
-// rounded half to even (see Coder).
+// int8: scale = max_d |x| / 127 in fp32 per token and head, code = 127 x / max
+// rounded half to even, without the scale's own rounding (see Coder).
 //
 // Both are copies, bound by bytes and, below a few MB, by their chain of waits
 // (slot, row, store: about 3 us); what differs between rows and tiles is the
