@@ -128,8 +128,12 @@ def _check(status: int):
         raise RuntimeError(f"w4a16 status {status}: {last_error()}")
 
 
-# The handle of torch.cuda.current_stream(index), without building the object.
-_raw_stream = torch._C._cuda_getCurrentRawStream
+def _current_stream(index: int) -> int:
+    return torch.cuda.current_stream(index).cuda_stream
+
+
+# The same without building the object, where torch has it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _current_stream)
 
 
 def _stream(t: torch.Tensor):
