@@ -15,8 +15,8 @@
 // up to 32768 columns.
 //
 // Rows need no alignment beyond their element's: 16-byte accesses are made
-// on any 2-byte address (global memory takes them), and the up to 7 elements
-// of a row's end are moved one by one.
+// on any 2-byte address (global memory takes them). The up to 7 elements of a
+// row's end are stored one by one and read as part of the row's last 8.
 #include "device_common.h"
 #include "internal.h"
 
@@ -32,6 +32,9 @@ typedef u32x4 u32x4_any __attribute__((aligned(2)));
 // end of a row of 8 or more is taken from its last 8 elements, so that every
 // lane makes one load and none waits for another's; align8 then moves them
 // to the front (the rest 0). Shorter rows are read element by element.
+// The elements that align8 drops may be overwritten meanwhile: where a row is
+// read a second time while its output goes over it (norm_kernel, CPT 0), they
+// belong to another lane's chunk. No other element is read after its store.
 __device__ __forceinline__ u32x4 load8(const uint16_t* p, int64_t n, int64_t K) {
     if (K >= 8) return *reinterpret_cast<const u32x4_any*>(p + (n < 8 ? n - 8 : 0));
     u32x4 v{0u, 0u, 0u, 0u};

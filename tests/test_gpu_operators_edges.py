@@ -59,6 +59,31 @@ def test_rmsnorm_of_small_rows_without_eps(K):
     within(y.cpu(), want, want.abs() * (HALF["bf16"] + REL) + TINY["bf16"], "y")
 
 
+@pytest.mark.parametrize("dtype", BOTH)
+@pytest.mark.parametrize("K", [32769, 33000, 40001, 70000])
+def test_rmsnorm_of_wide_rows_in_place(K, dtype):
+    """Rows that are read twice (above 32768 columns), with an output over an input: bit for bit as beside it."""
+    g = gen("norm wide in place", K, dtype)
+    dt = DTYPES[dtype]
+    x, w, r = (randn(g, *s, dtype=dt).to(DEV) for s in ((3, K), (K,), (3, K)))
+    h = torch.empty_like(x)
+    y = w4.rmsnorm(x, w, residual=r, residual_out=h)
+    want, want_h = ref.norm(x.cpu(), w.cpu(), 1e-5, r.cpu())
+    within(y.cpu(), want, want.abs() * (HALF[dtype] + REL) + TINY[dtype], "y")
+    within(h.cpu(), want_h, want_h.abs() * (HALF[dtype] + 2.0**-23) + TINY[dtype], "residual_out")
+    r2 = r.clone()
+    assert torch.equal(w4.rmsnorm(x, w, residual=r2, residual_out=r2), y) and torch.equal(r2, h)
+    x2 = x.clone()
+    assert torch.equal(w4.rmsnorm(x2, w, residual=r, residual_out=x2), y) and torch.equal(x2, h)
+    x2 = x.clone()
+    assert torch.equal(w4.rmsnorm(x2, w, residual=r, out=x2), y) and torch.equal(x2, y)
+    if K % 8 == 0:
+        qa, xs = w4.rmsnorm_a8(x, w, residual=r)
+        r2 = r.clone()
+        qb, ys = w4.rmsnorm_a8(x, w, residual=r2, residual_out=r2)
+        assert torch.equal(qa, qb) and torch.equal(xs, ys) and torch.equal(r2, h)
+
+
 # ---------------------------------------------------------------- gate
 
 
