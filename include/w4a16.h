@@ -442,9 +442,10 @@ w4a16_status w4a16_attention_workspace_size(int64_t B, int32_t q_heads, int32_t 
  * page_size at most 2^31, B times it at most 2^43; B == 0 is a no-op. The
  * result does not depend on the workspace's contents or on earlier calls
  * (no float atomics: the order of every sum follows from the sizes and lengths).
- * Probabilities are rounded to the 16 bits of the matrix operand (the act
- * dtype's, fp16's over an int8 cache); scores, their maximum and every sum are
- * fp32, and a sum of values that passes the fp32 range before it is divided
+ * Probabilities (over an int8 cache times the value's scale) enter the product
+ * with the values as two numbers of the matrix operand's type, together 16 bits
+ * (bf16) or 20 (fp16; over int8 too), and as one fp16 number (11 bits) where the
+ * cache is int8 and the result bf16; scores, their maximum and every sum are fp32, and a sum of values that passes the fp32 range before it is divided
  * gives infinity. W4A16_ERR_SIZE if the cache or the workspace is too small. The
  * workspace must be 256-byte aligned. */
 w4a16_status w4a16_attention(const void *q, int64_t q_bs, int64_t q_hs, int64_t B, int32_t q_heads, const void *cache,

@@ -16,6 +16,14 @@
 // keeps them out of the subnormals down to 2^-27 of the largest (and not lost
 // above 2^-38); the sums take the unrounded fp32 ones.
 //
+// A probability is two operands, a 16-bit number and the rest's, and the
+// product with the values is made with both: one alone moves the result by as
+// much as the result's own rounding does. The matrix cores have the time (64 x
+// 2048 tokens, 16 bits: 80.9 us with one, 81.2 with two; int8, D = 64: 25.5 and
+// 26.2; 333 tokens of one sequence 7.1 and 7.35). Over int8 with bf16 results
+// it is one fp16 operand: its 2^-11 is an eighth of the result's half step, and
+// the second one would cost 1.5 % (with two head tiles 4.5 %).
+//
 // int8: codes become exact fp16 values (0x6400 | (code ^ 0x80) is 1152 + code),
 // the key's scale multiplies the score, and the value's scale its probability,
 // w = p * vs. Scales of any size must not leave fp16's range, so w has a
@@ -169,6 +177,27 @@ struct Span {
     }
 };
 
+// Two probabilities as NP packed operands, each what the ones before leave.
+// fp16 is cut, not rounded (one instruction a pair): the next operand takes
+// what is cut off.
+template <int PDT, int NP>
+__device__ __forceinline__ void split_pair(float x, float y, uint32_t (&out)[NP]) {
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+        if constexpr (PDT == 0 && NP > 1) {
+            const auto h = __builtin_amdgcn_cvt_pkrtz(x, y);
+            out[i] = __builtin_bit_cast(uint32_t, h);
+            x = __builtin_fmaf((float)h[0], -1.0f, x);
+            y = __builtin_fmaf((float)h[1], -1.0f, y);
+        } else {
+            const uint16_t a = to_act_bits<PDT>(x), b = to_act_bits<PDT>(y);
+            out[i] = (uint32_t)a | (uint32_t)b << 16;
+            x -= act_to_float<PDT>(a);
+            y -= act_to_float<PDT>(b);
+        }
+    }
+}
+
 // What a head of n tiles counts for in the two ways to divide the work.
 __device__ __forceinline__ int chunks_of(int n) { return (n + kMinTiles - 1) / kMinTiles; }
 
@@ -179,6 +208,7 @@ struct Attend {
     static constexpr bool kI8 = KIND == 1;
     static constexpr bool kF16P = kI8 || DT == 0;
     static constexpr int PDT = kF16P ? 0 : 1;             // operand type of both products
+    static constexpr int NP = kI8 && DT == 1 ? 1 : 2;     // operands of a probability
     static constexpr int NL = D * (kI8 ? 1 : 2) / 32;     // 16-byte loads a lane for a tile's keys (and its values)
     static constexpr int NQ = D / 32;                     // MFMAs along d
     static constexpr int NO = D / 16;
@@ -300,9 +330,9 @@ struct Attend {
             for (int j = 0; j < 8; ++j) s[h][j] = acc[h][j / 4][j % 4];
     }
 
-    // Scores to base 2, then to the probabilities' operand; `partial` tiles
+    // Scores to base 2, then to the probabilities' operands; `partial` tiles
     // see only tokens from lo to hi - 1 of the tile.
-    __device__ __forceinline__ void probabilities(float (&s)[HT][8], u32x4 (&p)[HT], bool partial, int lo, int hi) {
+    __device__ __forceinline__ void probabilities(float (&s)[HT][8], u32x4 (&p)[HT][NP], bool partial, int lo, int hi) {
         uint32_t seen = 0xFFu;
         if (partial) {
             seen = 0u;
@@ -399,24 +429,37 @@ struct Attend {
 #pragma unroll
             for (int j = 0; j < 8; ++j) l[h] += e[h][j];
 #pragma unroll
-            for (int x = 0; x < 4; ++x)
-                p[h][x] = (uint32_t)to_act_bits<PDT>(w[h][2 * x]) | (uint32_t)to_act_bits<PDT>(w[h][2 * x + 1]) << 16;
+            for (int x = 0; x < 4; ++x) {
+                uint32_t parts[NP];
+                split_pair<PDT, NP>(w[h][2 * x], w[h][2 * x + 1], parts);
+#pragma unroll
+                for (int i = 0; i < NP; ++i) p[h][i][x] = parts[i];
+            }
         }
     }
 
-    __device__ __forceinline__ void accumulate(const u32x4 (&p)[HT]) {
+    __device__ __forceinline__ void accumulate(const u32x4 (&p)[HT][NP]) {
+        // A product should not wait for the one before it: with one head tile
+        // the second operands' products come after all of the first ones'
+        // (64 ragged sequences: 90 us side by side, 87.6 so); with two they
+        // take turns, and the other order spills at D = 256 (30 and 40 us).
+        constexpr int kPasses = HT == 1 ? NP : 1, kEach = NP / kPasses;
 #pragma unroll
-        for (int i = 0; i < NO; ++i) {
-            u32x4 v;
-            if constexpr (kI8) {
-                const u32x4& w = vb[i / 2];
-                v = i % 2 == 0 ? codes8_to_f16(w[0], w[1]) : codes8_to_f16(w[2], w[3]);
-            } else {
-                v = vb[i];
+        for (int pass = 0; pass < kPasses; ++pass)
+#pragma unroll
+            for (int i = 0; i < NO; ++i) {
+                u32x4 v;
+                if constexpr (kI8) {
+                    const u32x4& w = vb[i / 2];
+                    v = i % 2 == 0 ? codes8_to_f16(w[0], w[1]) : codes8_to_f16(w[2], w[3]);
+                } else {
+                    v = vb[i];
+                }
+#pragma unroll
+                for (int j = 0; j < kEach; ++j)
+#pragma unroll
+                    for (int h = 0; h < HT; ++h) o[h][i] = mfma16x16x32<PDT>(v, p[h][pass * kEach + j], o[h][i]);
             }
-#pragma unroll
-            for (int h = 0; h < HT; ++h) o[h][i] = mfma16x16x32<PDT>(v, p[h], o[h][i]);
-        }
     }
 
     // This wave's share of tiles [from, to) of sequence b: every kWaves-th,
@@ -466,7 +509,7 @@ struct Attend {
         do {
             const int at = tile * kTile;
             float s[HT][8];
-            u32x4 p[HT];
+            u32x4 p[HT][NP];
             // After the last tile every lane loads that tile's first unit
             // again (one cache line): loads on a condition would have to be
             // waited for as if they were the newest.

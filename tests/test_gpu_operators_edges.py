@@ -5,13 +5,15 @@ in place, workspaces under capture. References in 64 bits
 
 from __future__ import annotations
 
+import math
+
 import pytest
 import torch
 
 import mixed_precision_w4a16_repack_amd as w4
 from tests import operator_reference as ref
 from tests.operator_reference import DTYPES, HALF, TINY
-from tests.test_gpu_operators import BOTH, DEV, REL, check_codes, gen, randn, within
+from tests.test_gpu_operators import BOTH, DEV, REL, Batch, check_codes, gen, randn, within
 
 pytestmark = pytest.mark.gpu
 
@@ -132,6 +134,52 @@ def test_silu_mul_a8_of_an_infinite_gate(dtype):
     x[1, 7] = float("inf")
     _, xs = w4.silu_mul_a8(x.to(DEV))
     assert xs[1].item() == float("inf") and bool(xs[[0, 2]].isfinite().all())
+
+
+# ---------------------------------------------------------------- attention: the probabilities' bits
+
+
+def two_part_tolerance(out, A, S, dtype, n):
+    """ref.attention_tolerance with the probability in two parts: they leave a half step of a half step (fp16,
+    cut instead of rounded: a step of a step)."""
+    delta = 2 * 64 * 2.0**-24 * S[:, None]
+    part = (HALF[dtype] if dtype == "bf16" else 2 * HALF[dtype]) ** 2
+    return A * (part + delta + 2.0**-17) + HALF[dtype] * out.abs() + n * 2.0**-36 * A.amax() + TINY[dtype]
+
+
+@pytest.mark.parametrize("dtype", BOTH)
+def test_attention_equal_probabilities_between_two_steps(dtype):
+    """All but the first tokens have one probability, almost half a step above a 16-bit number relative to the
+    first ones': rounded alone it would move every result the same way, by as much as the result's own rounding."""
+    H, D, P, n = 1, 64, 32, 512
+    batch = Batch("between", [n], H, D, P, ref.KV_ACT, dtype)
+    k = torch.zeros(n, H, D, dtype=batch.dt)
+    k[128:, 0, 0] = 1.0
+    v = (torch.rand(n, H, D, generator=batch.g) + 1.0).to(batch.dt)
+    t = torch.arange(n)
+    slots = batch.table[0].long()[t // P] * P + t % P
+    w4.kv_write(k.to(DEV), v.to(DEV), slots.to(DEV), batch.cache, batch.pages, P, ref.KV_ACT)
+    q = torch.zeros(1, 3, D, dtype=batch.dt)
+    q[:, :, 0] = 1.0
+    scale = math.log(2 * (1 + 0.95 * HALF[dtype]))
+    o = w4.attention(q.to(DEV), batch.cache, batch.dev_table, batch.lengths, batch.pages, H, P, ref.KV_ACT, scale=scale)
+    want, A, S = ref.attention(q[0], k, v, torch.ones(n, dtype=torch.bool), scale)
+    within(o[0].cpu(), want, two_part_tolerance(want, A, S, dtype, n))
+
+
+@pytest.mark.parametrize("dtype,kind", [("f16", ref.KV_ACT), ("bf16", ref.KV_ACT), ("f16", ref.KV_INT8)])
+@pytest.mark.parametrize("Hq,H,D,P,lens,window", [
+    (32, 8, 128, 64, [0, 1, 33, 333, 2000], 0), (16, 16, 64, 32, [700, 5000], 300), (34, 2, 256, 32, [1000, 77], 0),
+    (40, 8, 192, 64, [129, 2500], 0), (32, 1, 128, 32, [9000], 0),
+])
+def test_attention_probabilities_in_two_parts(Hq, H, D, P, lens, window, dtype, kind):
+    batch = Batch("two parts", lens, H, D, P, kind, dtype)
+    q = randn(batch.g, len(lens), Hq, D, dtype=batch.dt)
+    o = w4.attention(q.to(DEV), batch.cache, batch.dev_table, batch.lengths, batch.pages, H, P, kind,
+                     window=window).cpu()
+    for b, n in enumerate(lens):
+        want, A, S = ref.attention(q[b], batch.k[b], batch.v[b], batch.seen(b, window), D**-0.5)
+        within(o[b], want, two_part_tolerance(want, A, S, dtype, n), f"sequence {b} ({n} tokens)")
 
 
 # ---------------------------------------------------------------- workspaces and graphs
