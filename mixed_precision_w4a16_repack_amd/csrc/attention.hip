@@ -33,9 +33,9 @@
 // largest lose bits).
 //
 // What bounds it: the cache's bytes. 64 sequences of 2048 tokens, 8 kv heads
-// of 128: 82 us in 16 bits (6.5 TB/s; a plain read of as much reaches 6.9),
-// 46 us in int8 (6.0 TB/s). The loads are non-temporal (each byte is read
-// once; through the caches as usual the 82 us were 92).
+// of 128: 81 us in 16 bits (6.6 TB/s; a plain read of as much reaches 6.9),
+// 44 us in int8 (6.3 TB/s). The loads are non-temporal (each byte is read
+// once; through the caches as usual they take 10 us more).
 //
 // Work is divided by tiles over a fixed number of workgroups, computed on the
 // device from the lengths (the host does not know them): each takes an equal
@@ -50,8 +50,8 @@
 // each level about 3 us (one sequence of 131000 tokens, int8: 52 us, of them 6
 // in two levels; with 16 at a time 55, with 64 in one level 63).
 // A short call is bound by its chain of waits: 333 tokens of one sequence
-// 7.1 us, of them 2 before the first instruction and after the last, 1.3 to
-// find its share, 2.6 for three tiles a wave and 1 to join the waves.
+// 7.35 us, of them 2 before the first instruction and after the last, 1.3 to
+// find its share, 2.9 for three tiles a wave and 1 to join the waves.
 #include "device_common.h"
 #include "exchange.h"
 #include "internal.h"
@@ -63,7 +63,7 @@ namespace {
 constexpr int kWaves = 4;
 constexpr int kTile = 32;              // tokens
 // Least tiles per workgroup when a head is split: a split costs a join. With 8,
-// 333 tokens take 8.0 us instead of 7.1; with 32, 1000 tokens 11.5 and not 9.6.
+// 333 tokens took 0.9 us more (of 7.1); with 32, 1000 tokens 11.5 and not 9.6.
 constexpr int kMinTiles = 16;
 constexpr int kHeadBytes = 80 << 10;   // a head's start and end cost a workgroup about as much as reading this
 constexpr int kFan = 8;                // partial results joined at once (their loads are in flight together)

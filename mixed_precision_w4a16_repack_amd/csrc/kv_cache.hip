@@ -16,11 +16,13 @@
 // units; where it starts or ends inside a tile, as aligned groups of 4 tokens;
 // any other slots, element by element.
 //
-// 8 heads of 128, 16 bits, write and read: 8000 tokens in a row 14.1 and 12.0
-// us (4.6 and 5.5 TB/s; by rows 37 and 35); 8000 scattered ones 62 and 41 us
-// (67 and 49): a scattered token's row touches 48 pieces of 64 bytes for its
-// 512, and the memory moves those whole (142 MB written and 173 MB read, by
-// the counters, for 33), a write of a part of one being a read and a write.
+// 8 heads of 128, write and read, past the last-level cache: 8000 tokens in a
+// row 16.8 and 17.7 us (3.8 TB/s: exactly the bytes needed, but 3 us of start
+// and end), int8 15.8 and 14.4 (two of the four waves wait while the rows are
+// quantised). Scattered 78 and 41 us, int8 41 and 28: a scattered token's row
+// touches 48 pieces of 64 bytes for its 512, and the memory moves those whole
+// (145 MB written and 175 MB read, by the counters, for 33), a write of a part
+// of one being a read and a write.
 #include "device_common.h"
 #include "internal.h"
 #include "kv_layout.h"
