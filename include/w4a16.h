@@ -416,6 +416,30 @@ w4a16_status w4a16_kv_read(const int64_t *slots, int64_t T, const void *cache, s
                            int32_t kv_heads, int32_t head_dim, int32_t page_size, int32_t kind, int32_t dtype, void *k,
                            int64_t k_ts, int64_t k_hs, void *v, int64_t v_ts, int64_t v_hs, hipStream_t stream);
 
+/* Writes T tokens' keys and values to their slots like w4a16_kv_write, the keys
+ * and, on the way, the queries turned by the tokens' positions:
+ *   pair i of a head's row, i < pairs, elements (x, y) = (i, i + pairs), or
+ *   (2 i, 2 i + 1) if neighbours is 1, becomes
+ *   (x cos w - y sin w, y cos w + x sin w),  w = positions[token] * rates[i],
+ * the elements behind the 2 * pairs first ones stay as they are. The angle is
+ * formed and reduced in fp64, the pair turned in fp32 and rounded once: to the
+ * act dtype, or, in an int8 cache, to codes from the fp32 values (a code whose
+ * quotient 127 x / max is within fp32's rounding of a tie may go to either
+ * neighbour). Values are written as by w4a16_kv_write.
+ *   q, q_out   q_heads query heads of the same tokens, element (token, head, d)
+ *              at token * ts + head * hs + d; q_out may be q itself (same
+ *              pointer and strides), and must not overlap k or v. q_heads 0: no queries
+ *              (q and q_out may be NULL)
+ *   positions  [T] int32 (device);  rates [pairs] fp32 (device)
+ * The queries of a token whose slot is outside the cache are turned like
+ * others. pairs is a multiple of 8, at most head_dim / 2. T == 0 is a no-op. */
+w4a16_status w4a16_kv_append(const void *q, int64_t q_ts, int64_t q_hs, int32_t q_heads, void *q_out, int64_t o_ts,
+                             int64_t o_hs, const void *k, int64_t k_ts, int64_t k_hs, const void *v, int64_t v_ts,
+                             int64_t v_hs, int64_t T, const int32_t *positions, const float *rates, int32_t pairs,
+                             int32_t neighbours, const int64_t *slots, void *cache, size_t cache_bytes, int64_t pages,
+                             int32_t kv_heads, int32_t head_dim, int32_t page_size, int32_t kind, int32_t dtype,
+                             hipStream_t stream);
+
 /* Bytes of device workspace w4a16_attention needs for these arguments (0 if
  * B == 0; it does not grow with B or the table beyond what a full card of
  * workgroups needs). It starts with the counter region of w4a16_workspace_size(), with
@@ -453,6 +477,87 @@ w4a16_status w4a16_attention(const void *q, int64_t q_bs, int64_t q_hs, int64_t 
                              int32_t kind, int32_t dtype, const int32_t *table, int64_t table_width, int64_t table_ld,
                              const int32_t *lengths, int64_t window, float scale, void *out, int64_t o_bs, int64_t o_hs,
                              void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* w4a16_attention with first tokens that stay visible: a window > 0 also sees
+ * the sequence's tokens 0 .. sinks - 1 (each token counts once). window 0 sees
+ * all, whatever sinks is; sinks 0 is w4a16_attention. Its workspace is
+ * w4a16_attention's kind, of the size given by the call below. */
+w4a16_status w4a16_attention_sinks_workspace_size(int64_t B, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
+                                                  int32_t page_size, int64_t table_width, int64_t window, int64_t sinks,
+                                                  int32_t kind, size_t *out_bytes);
+w4a16_status w4a16_attention_sinks(const void *q, int64_t q_bs, int64_t q_hs, int64_t B, int32_t q_heads,
+                                   const void *cache, size_t cache_bytes, int64_t pages, int32_t kv_heads,
+                                   int32_t head_dim, int32_t page_size, int32_t kind, int32_t dtype,
+                                   const int32_t *table, int64_t table_width, int64_t table_ld, const int32_t *lengths,
+                                   int64_t window, int64_t sinks, float scale, void *out, int64_t o_bs, int64_t o_hs,
+                                   void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* Bytes of device workspace w4a16_attention_tokens needs (0 if T or B is 0).
+ * The workspace need not be cleared; calls that share one must be ordered. A
+ * buffer that it shares with a call that needs a zero counter region must have
+ * that region zeroed again. out_bytes is a host pointer. */
+w4a16_status w4a16_attention_tokens_workspace_size(int64_t T, int64_t B, int32_t q_heads, int32_t kv_heads,
+                                                   int32_t head_dim, int32_t page_size, int64_t table_width,
+                                                   int32_t kind, size_t *out_bytes);
+
+/* Attention of several new tokens per sequence over the cache, their own keys
+ * and values included: prompts, parts of prompts, and trees of drafted tokens.
+ *   out[r, i] = sum_t p_t v_t,  p = softmax_t(scale * q[r, i] . k_t)
+ * Sequence b's new tokens are the rows starts[b] .. starts[b + 1] - 1 of q (m of
+ * them), and the last m of its n = lengths[b] tokens in the cache: row
+ * starts[b] + i is token n - m + i. Without a tree that token sees the tokens
+ * 0 .. n - m + i, with window > 0 the last `window` of them and the first
+ * `sinks`. With a tree, tree[row * tree_ld + j / 64] bit j % 64 says whether the
+ * row sees its sequence's new token j (itself as well, if the bit is set; bits
+ * from m on do not count); of the tokens before the new ones it sees all, or
+ * with window > 0 those less than `window` before its position and the first
+ * `sinks`, its position being n - m + (set bits) - 1, that is its depth behind
+ * the past. A row without a set bit (padding) sees nothing.
+ *   q, out   element (row, head, d) at row * ts + head * hs + d, act dtype;
+ *            rows of no sequence are neither read nor written
+ *   starts   [B + 1] int32 (device), not decreasing, cut to 0 .. T
+ *   tree     [T, tree_ld] int64 (device), tree_ld >= tree_words >= 1, or NULL
+ *   table, lengths, heads, the cache and its missing pages as for
+ *            w4a16_attention; a new token that has no place (m > n) sees
+ *            nothing. Rows that see nothing, or only scores of -infinity, are
+ *            zeros
+ * Memory of tokens that a row does not see may hold anything, NaN included; a
+ * NaN or an infinity among the values that it sees gives it one (either).
+ * Probabilities enter the products as in w4a16_attention; scores, maxima and
+ * sums are fp32. The result does not depend on the workspace's contents or on
+ * earlier calls. T * q_heads must be below 2^31. */
+w4a16_status w4a16_attention_tokens(const void *q, int64_t q_ts, int64_t q_hs, int64_t T, int32_t q_heads,
+                                    const int32_t *starts, int64_t B, const int64_t *tree, int64_t tree_words,
+                                    int64_t tree_ld, const void *cache, size_t cache_bytes, int64_t pages,
+                                    int32_t kv_heads, int32_t head_dim, int32_t page_size, int32_t kind, int32_t dtype,
+                                    const int32_t *table, int64_t table_width, int64_t table_ld, const int32_t *lengths,
+                                    int64_t window, int64_t sinks, float scale, void *out, int64_t o_ts, int64_t o_hs,
+                                    void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* A token from each row of logits, by given random numbers:
+ *   weight w = exp((x - max x) / temperature), the row's tokens ordered by
+ *   falling logit, equal ones by index. Of that order are kept
+ *    - the first top_k tokens (top_k <= 0: all),
+ *    - of those the fewest first ones whose weights reach top_p of their sum
+ *      (top_p >= 1 or NaN: all; top_p <= 0: the first),
+ *    - of those the ones with w >= min_p (min_p <= 0 or NaN: all; above 1: as 1).
+ *   tokens[m] is the first kept token at which the sum of the kept weights up
+ *   to it is above uniforms[m] times the sum of all kept ones; probs[m] its
+ *   weight over that sum.
+ * A temperature that is 0, negative or NaN takes the row's first token (its
+ * largest logit's lowest index) with probability 1. Logits of -infinity and NaN
+ * are never drawn and count nowhere; a row of nothing else gives token -1 and
+ * probability 0. Where the largest logit is +infinity only such ones have
+ * weight. uniforms outside [0, 1) count as the nearest number in it, NaN as 0.
+ *   logits       [M, ldl] act dtype, ldl >= V, 2-byte aligned, any stride
+ *   uniforms     [M] fp32
+ *   temperature, top_p, min_p  [M] fp32, top_k [M] int32, or NULL (1, and off)
+ *   tokens       [M] int64;  probs [M] fp32, or NULL
+ * Weights and their sums are fp64; equal calls give equal tokens. V <= 2^22.
+ * M == 0 is a no-op. */
+w4a16_status w4a16_sample(const void *logits, int64_t M, int64_t V, int64_t ldl, int32_t dtype, const float *uniforms,
+                          const float *temperature, const int32_t *top_k, const float *top_p, const float *min_p,
+                          int64_t *tokens, float *probs, hipStream_t stream);
 
 #ifdef __cplusplus
 }

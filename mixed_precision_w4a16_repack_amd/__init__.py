@@ -12,7 +12,8 @@ Names follow the C ABI (include/w4a16.h): ``packed_size``, ``repack``,
 prefill variant ``dequant`` and ``gemm_dense``, and the operators between a
 decoder layer's GEMMs: ``rmsnorm``, ``silu_mul`` (and their int8 forms
 ``rmsnorm_a8``, ``silu_mul_a8``), ``kv_cache_size``, ``kv_write``,
-``kv_read`` and ``attention``.
+``kv_append``, ``kv_read``, ``attention`` and ``attention_tokens``; and
+``sample``, which turns logits into tokens.
 """
 
 from __future__ import annotations
@@ -81,6 +82,11 @@ SIGNATURES = {
         ctypes.c_int,
         [_P, _I64, _P, _SZ, _I64, _I32, _I32, _I32, _I32, _I32, _P, _I64, _I64, _P, _I64, _I64, _P],
     ),
+    "w4a16_kv_append": (
+        ctypes.c_int,
+        [_P, _I64, _I64, _I32, _P, _I64, _I64, _P, _I64, _I64, _P, _I64, _I64, _I64, _P, _P, _I32, _I32, _P, _P, _SZ,
+         _I64, _I32, _I32, _I32, _I32, _I32, _P],
+    ),
     "w4a16_attention_workspace_size": (
         ctypes.c_int, [_I64, _I32, _I32, _I32, _I32, _I64, _I64, _I32, ctypes.POINTER(_SZ)]),
     "w4a16_attention": (
@@ -88,6 +94,21 @@ SIGNATURES = {
         [_P, _I64, _I64, _I64, _I32, _P, _SZ, _I64, _I32, _I32, _I32, _I32, _I32, _P, _I64, _I64, _P, _I64, _F32,
          _P, _I64, _I64, _P, _SZ, _P],
     ),
+    "w4a16_attention_sinks_workspace_size": (
+        ctypes.c_int, [_I64, _I32, _I32, _I32, _I32, _I64, _I64, _I64, _I32, ctypes.POINTER(_SZ)]),
+    "w4a16_attention_sinks": (
+        ctypes.c_int,
+        [_P, _I64, _I64, _I64, _I32, _P, _SZ, _I64, _I32, _I32, _I32, _I32, _I32, _P, _I64, _I64, _P, _I64, _I64, _F32,
+         _P, _I64, _I64, _P, _SZ, _P],
+    ),
+    "w4a16_attention_tokens_workspace_size": (
+        ctypes.c_int, [_I64, _I64, _I32, _I32, _I32, _I32, _I64, _I32, ctypes.POINTER(_SZ)]),
+    "w4a16_attention_tokens": (
+        ctypes.c_int,
+        [_P, _I64, _I64, _I64, _I32, _P, _I64, _P, _I64, _I64, _P, _SZ, _I64, _I32, _I32, _I32, _I32, _I32, _P, _I64,
+         _I64, _P, _I64, _I64, _F32, _P, _I64, _I64, _P, _SZ, _P],
+    ),
+    "w4a16_sample": (ctypes.c_int, [_P, _I64, _I64, _I64, _I32, _P, _P, _P, _P, _P, _P, _P, _P]),
 }
 
 _lib = None
@@ -684,22 +705,91 @@ def kv_read(slots: torch.Tensor, cache: torch.Tensor, pages: int, kv_heads: int,
     return k, v
 
 
+def _vector(name: str, t: torch.Tensor, n: int, dtype, device: int):
+    """t must be a contiguous [n] tensor."""
+    if t.dtype is dtype and t.get_device() == device and t.shape == (n,) and t.is_contiguous():
+        return
+    _need_cuda(name, t, dtype)
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{device}")
+    raise ValueError(f"{name} must be a contiguous [{n}] tensor, got {tuple(t.shape)} {t.stride()}")
+
+
+def kv_append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor, rates: torch.Tensor,
+              slots: torch.Tensor, cache: torch.Tensor, pages: int, page_size: int, kind: int,
+              interleaved: bool = False, out: torch.Tensor | None = None) -> torch.Tensor | None:
+    """``kv_write`` with the keys and the queries [T, q_heads, head_dim] turned by their positions; returns the
+    turned queries (None without queries).
+
+    ``rates`` [pairs] fp32 holds the angle per position of each pair: elements (i, i + pairs) of a head's row, or
+    (2i, 2i + 1) if ``interleaved``; the rest of the row stays. ``positions`` [T] int32. ``out`` may be ``q`` itself."""
+    if not k.is_cuda or k.dtype not in _DTYPE_CODE:
+        _need_cuda("k", k, (torch.float16, torch.bfloat16))
+    T = _slots(slots)
+    if k.dim() != 3:
+        raise ValueError("k must be [T, kv_heads, head_dim]")
+    device, dtype = k.get_device(), k.dtype
+    H, D = k.shape[1:]
+    _heads("k", k, (T, H, D), dtype, device)
+    _heads("v", v, (T, H, D), dtype, device)
+    _vector("positions", positions, T, torch.int32, device)
+    pairs = rates.numel()
+    _vector("rates", rates, pairs, torch.float32, device)
+    queries = (None, 0, 0, 0, None, 0, 0)
+    if q is not None:
+        if q.dim() != 3:
+            raise ValueError("q must be [T, q_heads, head_dim]")
+        shape = (T, q.shape[1], D)
+        _heads("q", q, shape, dtype, device)
+        if out is None:
+            out = torch.empty(shape, dtype=dtype, device=q.device)
+        elif out is not q:
+            _heads("out", out, shape, dtype, device)
+        queries = (q.data_ptr(), q.stride(0), q.stride(1), q.shape[1], out.data_ptr(), out.stride(0), out.stride(1))
+    elif out is not None:
+        raise ValueError("out needs q")
+    nbytes = _cache_bytes(cache, device)
+    if slots.get_device() != device:
+        _same_device(k, slots=slots)
+    status = (_lib or load_library()).w4a16_kv_append(
+        *queries, k.data_ptr(), k.stride(0), k.stride(1), v.data_ptr(), v.stride(0), v.stride(1), T,
+        positions.data_ptr(), rates.data_ptr(), pairs, 1 if interleaved else 0, slots.data_ptr(), cache.data_ptr(),
+        nbytes, pages, H, D, page_size, kind, _DTYPE_CODE[dtype], _raw_stream(device))
+    if status:
+        _check(status)
+    return out
+
+
 @functools.lru_cache(maxsize=4096)
 def attention_workspace_size(B: int, q_heads: int, kv_heads: int, head_dim: int, page_size: int, table_width: int,
-                             window: int, kind: int) -> int:
+                             window: int, kind: int, sinks: int = 0) -> int:
     out = _SZ(0)
-    _check(load_library().w4a16_attention_workspace_size(B, q_heads, kv_heads, head_dim, page_size, table_width,
-                                                         window, kind, ctypes.byref(out)))
+    _check(load_library().w4a16_attention_sinks_workspace_size(B, q_heads, kv_heads, head_dim, page_size, table_width,
+                                                               window, sinks, kind, ctypes.byref(out)))
     return int(out.value)
+
+
+def _table(q: torch.Tensor, table: torch.Tensor, lengths: torch.Tensor, B: int, device: int):
+    """Checks of a page table [B, width] and its lengths [B]."""
+    if table.dtype is not torch.int32 or table.get_device() != device:
+        _need_cuda("table", table, torch.int32)
+        _same_device(q, table=table)
+    if table.dim() != 2 or table.shape[0] != B or (table.shape[1] > 1 and table.stride(1) != 1):
+        raise ValueError(f"table must be [B={B}, width] with unit column stride")
+    if lengths.dtype is not torch.int32 or lengths.get_device() != device:
+        _need_cuda("lengths", lengths, torch.int32)
+        _same_device(q, lengths=lengths)
+    if lengths.shape != (B,) or not lengths.is_contiguous():
+        raise ValueError(f"lengths must be a contiguous [B={B}] tensor")
 
 
 def attention(q: torch.Tensor, cache: torch.Tensor, table: torch.Tensor, lengths: torch.Tensor, pages: int,
               kv_heads: int, page_size: int, kind: int, window: int = 0, scale: float | None = None,
-              out: torch.Tensor | None = None, workspace: Workspace | None = None) -> torch.Tensor:
+              out: torch.Tensor | None = None, workspace: Workspace | None = None, sinks: int = 0) -> torch.Tensor:
     """Attention of one new token per sequence over the cache: q [B, q_heads, head_dim] -> the same shape.
 
     ``table`` [B, width] int32 holds each sequence's pages, ``lengths`` [B] int32 its tokens (the new one
-    included); ``window`` > 0 sees only the last tokens; ``scale`` defaults to head_dim ** -0.5. For calls that
+    included); ``window`` > 0 sees only the last tokens, and the first ``sinks``; ``scale`` defaults to head_dim ** -0.5. For calls that
     are captured into a graph see ``Workspace``."""
     if not q.is_cuda or q.dtype not in _DTYPE_CODE:
         _need_cuda("q", q, (torch.float16, torch.bfloat16))
@@ -712,29 +802,114 @@ def attention(q: torch.Tensor, cache: torch.Tensor, table: torch.Tensor, lengths
         out = _empty(q, shape)
     else:
         _heads("out", out, shape, dtype, device)
-    if table.dtype is not torch.int32 or table.get_device() != device:
-        _need_cuda("table", table, torch.int32)
-        _same_device(q, table=table)
-    if table.dim() != 2 or table.shape[0] != B or (table.shape[1] > 1 and table.stride(1) != 1):
-        raise ValueError(f"table must be [B={B}, width] with unit column stride")
-    if lengths.dtype is not torch.int32 or lengths.get_device() != device:
-        _need_cuda("lengths", lengths, torch.int32)
-        _same_device(q, lengths=lengths)
-    if lengths.shape != (B,) or not lengths.is_contiguous():
-        raise ValueError(f"lengths must be a contiguous [B={B}] tensor")
+    _table(q, table, lengths, B, device)
     nbytes = _cache_bytes(cache, device)
     width = table.shape[1]
     stream = _raw_stream(device)
     ws_ptr, ws_bytes = None, 0
     if B > 0:
-        need = attention_workspace_size(B, Hq, kv_heads, D, page_size, width, window, kind)
+        need = attention_workspace_size(B, Hq, kv_heads, D, page_size, width, window, kind, sinks)
         # the first look is _default_workspace's own, without building the device object
         ws = (workspace or _workspaces.get(("attention", device, stream)) or _default_workspace(q.device, "attention")).get(need)
         ws_ptr, ws_bytes = ws.data_ptr(), ws.numel()
-    status = (_lib or load_library()).w4a16_attention(
+    status = (_lib or load_library()).w4a16_attention_sinks(
         q.data_ptr(), q.stride(0), q.stride(1), B, Hq, cache.data_ptr(), nbytes, pages, kv_heads, D, page_size, kind,
-        _DTYPE_CODE[dtype], table.data_ptr(), width, table.stride(0) if B > 1 else width, lengths.data_ptr(), window,
+        _DTYPE_CODE[dtype], table.data_ptr(), width, table.stride(0) if B > 1 else width, lengths.data_ptr(), window, sinks,
         D ** -0.5 if scale is None else scale, out.data_ptr(), out.stride(0), out.stride(1), ws_ptr, ws_bytes, stream)
+    if status:
+        _check(status)
+    return out
+
+
+@functools.lru_cache(maxsize=4096)
+def attention_tokens_workspace_size(T: int, B: int, q_heads: int, kv_heads: int, head_dim: int, page_size: int,
+                                    table_width: int, kind: int) -> int:
+    out = _SZ(0)
+    _check(load_library().w4a16_attention_tokens_workspace_size(T, B, q_heads, kv_heads, head_dim, page_size,
+                                                                table_width, kind, ctypes.byref(out)))
+    return int(out.value)
+
+
+def attention_tokens(q: torch.Tensor, starts: torch.Tensor, cache: torch.Tensor, table: torch.Tensor,
+                     lengths: torch.Tensor, pages: int, kv_heads: int, page_size: int, kind: int,
+                     tree: torch.Tensor | None = None, window: int = 0, sinks: int = 0, scale: float | None = None,
+                     out: torch.Tensor | None = None, workspace: Workspace | None = None) -> torch.Tensor:
+    """Attention of several new tokens per sequence over the cache: q [T, q_heads, head_dim] -> the same shape.
+
+    Sequence b's new tokens are rows ``starts[b]`` .. ``starts[b + 1] - 1`` (``starts`` [B + 1] int32), the last ones
+    of its ``lengths[b]`` cached tokens; rows of no sequence are left as they are. A token sees those up to itself,
+    or, with ``tree`` [T, words] int64, all tokens before the new ones and the new ones whose bits its row has (bit
+    j % 64 of word j // 64; a row without bits sees nothing). ``window`` > 0 sees only the last tokens, and the first
+    ``sinks``. For calls that are captured into a graph see ``Workspace``."""
+    if not q.is_cuda or q.dtype not in _DTYPE_CODE:
+        _need_cuda("q", q, (torch.float16, torch.bfloat16))
+    if q.dim() != 3:
+        raise ValueError("q must be [T, q_heads, head_dim]")
+    T, Hq, D = shape = q.shape
+    device, dtype = q.get_device(), q.dtype
+    _heads("q", q, shape, dtype, device)
+    if starts.dim() != 1 or starts.shape[0] < 1:
+        raise ValueError("starts must be [B + 1]")
+    B = starts.shape[0] - 1
+    _vector("starts", starts, B + 1, torch.int32, device)
+    if out is None:
+        out = _empty(q, shape)
+    else:
+        _heads("out", out, shape, dtype, device)
+    words, tree_ptr, tree_ld = 0, None, 0
+    if tree is not None:
+        if tree.dtype is not torch.int64 or tree.get_device() != device:
+            _need_cuda("tree", tree, torch.int64)
+            _same_device(q, tree=tree)
+        if tree.dim() != 2 or tree.shape[0] != T or tree.shape[1] < 1 or (tree.shape[1] > 1 and tree.stride(1) != 1):
+            raise ValueError(f"tree must be [T={T}, words] with unit column stride")
+        words, tree_ptr = tree.shape[1], tree.data_ptr()
+        tree_ld = tree.stride(0) if T > 1 else words
+    _table(q, table, lengths, B, device)
+    nbytes = _cache_bytes(cache, device)
+    width = table.shape[1]
+    stream = _raw_stream(device)
+    ws_ptr, ws_bytes = None, 0
+    if T > 0 and B > 0:
+        need = attention_tokens_workspace_size(T, B, Hq, kv_heads, D, page_size, width, kind)
+        ws = (workspace or _workspaces.get(("attention_tokens", device, stream))
+              or _default_workspace(q.device, "attention_tokens")).get(need)
+        ws_ptr, ws_bytes = ws.data_ptr(), ws.numel()
+    status = (_lib or load_library()).w4a16_attention_tokens(
+        q.data_ptr(), q.stride(0), q.stride(1), T, Hq, starts.data_ptr(), B, tree_ptr, words, tree_ld, cache.data_ptr(),
+        nbytes, pages, kv_heads, D, page_size, kind, _DTYPE_CODE[dtype], table.data_ptr(), width,
+        table.stride(0) if B > 1 else width, lengths.data_ptr(), window, sinks, D ** -0.5 if scale is None else scale,
+        out.data_ptr(), out.stride(0), out.stride(1), ws_ptr, ws_bytes, stream)
+    if status:
+        _check(status)
+    return out
+
+
+def sample(logits: torch.Tensor, uniforms: torch.Tensor, temperature: torch.Tensor | None = None,
+           top_k: torch.Tensor | None = None, top_p: torch.Tensor | None = None, min_p: torch.Tensor | None = None,
+           out: torch.Tensor | None = None, probs: torch.Tensor | None = None) -> torch.Tensor:
+    """A token [M] int64 from each row of ``logits`` [M, V], by the random numbers ``uniforms`` [M] in [0, 1).
+
+    ``temperature`` (0: the largest logit), ``top_p``, ``min_p`` [M] fp32 and ``top_k`` [M] int32 are each row's own;
+    None is off. ``probs`` [M] fp32 receives each token's probability among those kept. -1 where every logit is
+    -infinity."""
+    if not logits.is_cuda or logits.dtype not in _DTYPE_CODE:
+        _need_cuda("logits", logits, (torch.float16, torch.bfloat16))
+    if logits.dim() != 2 or logits.stride(1) != 1:
+        raise ValueError("logits must be [M, V] with unit column stride")
+    M, V = logits.shape
+    device = logits.get_device()
+    _vector("uniforms", uniforms, M, torch.float32, device)
+    for name, t, dtype in (("temperature", temperature, torch.float32), ("top_k", top_k, torch.int32),
+                           ("top_p", top_p, torch.float32), ("min_p", min_p, torch.float32), ("probs", probs, torch.float32),
+                           ("out", out, torch.int64)):
+        if t is not None:
+            _vector(name, t, M, dtype, device)
+    if out is None:
+        out = torch.empty(M, dtype=torch.int64, device=logits.device)
+    status = (_lib or load_library()).w4a16_sample(
+        logits.data_ptr(), M, V, logits.stride(0) if M > 1 else V, _DTYPE_CODE[logits.dtype], uniforms.data_ptr(),
+        _ptr(temperature), _ptr(top_k), _ptr(top_p), _ptr(min_p), out.data_ptr(), _ptr(probs), _raw_stream(device))
     if status:
         _check(status)
     return out

@@ -52,6 +52,7 @@
 // A short call is bound by its chain of waits: 333 tokens of one sequence
 // 7.35 us, of them 2 before the first instruction and after the last, 1.3 to
 // find its share, 2.9 for three tiles a wave and 1 to join the waves.
+#include "attention_common.h"
 #include "device_common.h"
 #include "exchange.h"
 #include "internal.h"
@@ -69,11 +70,6 @@ constexpr int kHeadBytes = 80 << 10;   // a head's start and end cost a workgrou
 constexpr int kFan = 8;                // partial results joined at once (their loads are in flight together)
 constexpr int kChunkBits = 24;         // a sum over sequences: slots << kChunkBits | chunks, the latter cut to kChunkMost a lane
 constexpr int64_t kChunkMask = ((int64_t)1 << kChunkBits) - 1, kChunkMost = 1 << 16;
-constexpr float kLowest = -3.402823466e38f;
-
-typedef u32x4 u32x4_any __attribute__((aligned(2)));
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-typedef u32x2 u32x2_any __attribute__((aligned(2)));
 
 // How many workgroups of each kernel share a CU. More waves than the bytes in
 // flight need make the reads slower, not faster: int8 D = 128 takes 63 us with
@@ -84,89 +80,9 @@ typedef u32x2 u32x2_any __attribute__((aligned(2)));
 template <int KIND, int D, int HT>
 constexpr int kPerCU = D > 192 || (D > 128 && (HT == 2 || KIND == 0)) || (HT == 2 && KIND == 0) ? 1 : 2;
 
-// The factor on probabilities, and how far (in powers of 2) a score may pass
-// the reference: in fp16 2^13 * 2^2 < 65504.
-template <bool F16P>
-struct Prob {
-    static constexpr float kBias = F16P ? 13.0f : 0.0f;
-    static constexpr float kHeadroom = F16P ? 2.0f : 8.0f;
-};
-
-__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
-
-// Maximum, or sum, over the four lane groups of a column (lanes l, l + 16, ...).
-__device__ __forceinline__ float column_max(float v) {
-    v = fmaxf(v, __shfl_xor(v, 16));
-    return fmaxf(v, __shfl_xor(v, 32));
-}
-__device__ __forceinline__ float column_sum(float v) {
-    v += __shfl_xor(v, 16);
-    return v + __shfl_xor(v, 32);
-}
-
-// Four int8 codes (one word) as two words of exact fp16 pairs.
-__device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
-    const uint32_t x = w ^ 0x80808080u;
-    const half2_t off{(_Float16)-1152.0f, (_Float16)-1152.0f};
-    const half2_t a = __builtin_bit_cast(half2_t, __builtin_amdgcn_perm(0x64646464u, x, 0x04010400u)) + off;
-    const half2_t b = __builtin_bit_cast(half2_t, __builtin_amdgcn_perm(0x64646464u, x, 0x04030402u)) + off;
-    lo = __builtin_bit_cast(uint32_t, a);
-    hi = __builtin_bit_cast(uint32_t, b);
-}
-__device__ __forceinline__ u32x4 codes8_to_f16(uint32_t w0, uint32_t w1) {
-    uint32_t a, b, c, d;
-    codes_to_f16(w0, a, b);
-    codes_to_f16(w1, c, d);
-    return u32x4{a, b, c, d};
-}
-
-// A pointer that is the same on all lanes, in scalar registers.
-__device__ __forceinline__ const float* uniform(const float* p) {
-    const uint64_t v = reinterpret_cast<uint64_t>(p);
-    const uint32_t lo = __builtin_amdgcn_readfirstlane((int)(uint32_t)v), hi = __builtin_amdgcn_readfirstlane((int)(uint32_t)(v >> 32));
-    return reinterpret_cast<const float*>((uint64_t)hi << 32 | lo);
-}
-
-__device__ __forceinline__ int64_t read_lane(int64_t v, int lane) {
-    const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)v, lane);
-    const uint32_t hi = __builtin_amdgcn_readlane((int)(uint32_t)(v >> 32), lane);
-    return (int64_t)((uint64_t)hi << 32 | lo);
-}
-
-// v of the lane that a DPP control names, 0 where there is none.
-template <int CTRL, int ROWS>
-__device__ __forceinline__ int64_t from_lane(int64_t v) {
-    const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)v, CTRL, ROWS, 0xF, false);
-    const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)(v >> 32), CTRL, ROWS, 0xF, false);
-    return (int64_t)((uint64_t)hi << 32 | lo);
-}
-// Sum over lanes 0 .. lane.
-__device__ __forceinline__ int64_t wave_scan(int64_t v) {
-    v += from_lane<0x111, 0xF>(v);  // row_shr:1, 2, 4, 8: within 16 lanes
-    v += from_lane<0x112, 0xF>(v);
-    v += from_lane<0x114, 0xF>(v);
-    v += from_lane<0x118, 0xF>(v);
-    v += from_lane<0x142, 0xA>(v);  // row_bcast:15 into rows 1 and 3
-    v += from_lane<0x143, 0xC>(v);  // row_bcast:31 into rows 2 and 3
-    return v;
-}
-
-// The loads before this are issued before anything after it.
-__device__ __forceinline__ void issue_fence() {
-    asm volatile("" ::: "memory");
-    __builtin_amdgcn_sched_barrier(0);
-}
-
-// a / b of non-negative numbers below 2^53 whose quotient is below 2^20: the
-// product is off by less than 1 before it is cut.
-__device__ __forceinline__ int divide(int64_t a, int64_t b) {
-    const int q = (int)((double)a * __builtin_amdgcn_rcp((double)b));
-    const int64_t r = a - q * b;
-    return r < 0 ? q - 1 : (r >= b ? q + 1 : q);
-}
-
 // What a sequence of a length sees: tokens lo .. n - 1, in the tiles
-// [first, first + count).
+// first + i, i in [0, count).
+template <bool SINKS>
 struct Span {
     int n, lo, first, count;
     __device__ __forceinline__ Span(const AttentionArgs& a, int length) {
@@ -175,33 +91,33 @@ struct Span {
         first = lo / kTile;
         count = n > lo ? (n - 1) / kTile + 1 - first : 0;
     }
+    __device__ __forceinline__ int tile(int i) const { return i; }
+    __device__ __forceinline__ int kept() const { return 0; }
 };
-
-// Two probabilities as NP packed operands, each what the ones before leave.
-// fp16 is cut, not rounded (one instruction a pair): the next operand takes
-// what is cut off.
-template <int PDT, int NP>
-__device__ __forceinline__ void split_pair(float x, float y, uint32_t (&out)[NP]) {
-#pragma unroll
-    for (int i = 0; i < NP; ++i) {
-        if constexpr (PDT == 0 && NP > 1) {
-            const auto h = __builtin_amdgcn_cvt_pkrtz(x, y);
-            out[i] = __builtin_bit_cast(uint32_t, h);
-            x = __builtin_fmaf((float)h[0], -1.0f, x);
-            y = __builtin_fmaf((float)h[1], -1.0f, y);
-        } else {
-            const uint16_t a = to_act_bits<PDT>(x), b = to_act_bits<PDT>(y);
-            out[i] = (uint32_t)a | (uint32_t)b << 16;
-            x -= act_to_float<PDT>(a);
-            y -= act_to_float<PDT>(b);
-        }
+// With first tokens that stay visible: tokens 0 .. sk - 1 too (sk <= lo), whose
+// tiles come first in the list: `head` of them that the window does not touch,
+// then the window's, `skip` tiles further on.
+template <>
+struct Span<true> {
+    static constexpr int first = 0;
+    int n, lo, sk, head, skip, count;
+    __device__ __forceinline__ Span(const AttentionArgs& a, int length) {
+        n = length < 0 ? 0 : (length > a.most ? a.most : length);
+        lo = n > a.reach ? n - a.reach : 0;
+        sk = a.sinks < lo ? a.sinks : lo;
+        const int at = lo / kTile, tiles = (sk + kTile - 1) / kTile;
+        head = tiles < at ? tiles : at;
+        skip = at - head;
+        count = n > lo ? (n - 1) / kTile + 1 - skip : 0;
     }
-}
+    __device__ __forceinline__ int tile(int i) const { return i < head ? i : i + skip; }
+    __device__ __forceinline__ int kept() const { return sk; }
+};
 
 // What a head of n tiles counts for in the two ways to divide the work.
 __device__ __forceinline__ int chunks_of(int n) { return (n + kMinTiles - 1) / kMinTiles; }
 
-template <int DT, int KIND, int D, int HT>
+template <int DT, int KIND, int D, int HT, bool SINKS>
 struct Attend {
     static constexpr int kHeadCost = kHeadBytes / (kTile * D * (KIND == 1 ? 2 : 4));  // in tiles
     static __device__ __forceinline__ int slots_of(int n) { return n > 0 ? n + kHeadCost : 0; }
@@ -331,15 +247,16 @@ struct Attend {
     }
 
     // Scores to base 2, then to the probabilities' operands; `partial` tiles
-    // see only tokens from lo to hi - 1 of the tile.
-    __device__ __forceinline__ void probabilities(float (&s)[HT][8], u32x4 (&p)[HT][NP], bool partial, int lo, int hi) {
+    // see only tokens from lo to hi - 1 of the tile, and those before sk.
+    __device__ __forceinline__ void probabilities(float (&s)[HT][8], u32x4 (&p)[HT][NP], bool partial, int lo, int hi, int sk) {
         uint32_t seen = 0xFFu;
         if (partial) {
             seen = 0u;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const int t = j / 4 * 16 + 4 * g + j % 4;
-                seen |= (uint32_t)(t >= lo && t < hi) << j;
+                if constexpr (SINKS) seen |= (uint32_t)((t >= lo || t < sk) && t < hi) << j;
+                else seen |= (uint32_t)(t >= lo && t < hi) << j;
             }
             if constexpr (kI8) {
 #pragma unroll
@@ -464,7 +381,7 @@ struct Attend {
 
     // This wave's share of tiles [from, to) of sequence b: every kWaves-th,
     // those of missing pages left out.
-    __device__ __forceinline__ void run(int64_t b, int kv_head, const Span& sp, int from, int to) {
+    __device__ __forceinline__ void run(int64_t b, int kv_head, const Span<SINKS>& sp, int from, int to) {
         const int tiles_per_page = a.P / kTile;
         const int whole_shift = (tiles_per_page & (tiles_per_page - 1)) == 0 ? __builtin_ctz(tiles_per_page) : -1;
         int block = from + wave;  // first tile of the 64 in hand, lane i holding block + kWaves * i
@@ -473,9 +390,9 @@ struct Attend {
         int sub_l = 0;
         auto fetch = [&]() {
             while (todo == 0 && block < to) {
-                const int tile = block + kWaves * lane;
+                const int item = block + kWaves * lane, tile = sp.tile(item);
                 int64_t page = -1;
-                if (tile < to) {
+                if (item < to) {
                     const int at = whole_shift >= 0 ? tile >> whole_shift : tile / tiles_per_page;
                     page = a.table[b * a.table_ld + at];
                     sub_l = tile - at * tiles_per_page;
@@ -495,7 +412,7 @@ struct Attend {
             todo &= todo - 1;
             rec = a.cache + read_lane(place, i);
             sub = __builtin_amdgcn_readlane(sub_l, i);
-            tile = block + kWaves * i;
+            tile = sp.tile(block + kWaves * i);
             if (todo == 0) block += 64 * kWaves;
             return true;
         };
@@ -519,8 +436,8 @@ struct Attend {
             issue_fence();
             load_keys(rec, sub, unit);
             issue_fence();
-            const int lo = sp.lo - at, hi = sp.n - at;
-            probabilities(s, p, lo > 0 || hi < kTile, lo, hi);
+            const int lo = sp.lo - at, hi = sp.n - at, sk = sp.kept() - at;
+            probabilities(s, p, (lo > 0 && (!SINKS || sk < kTile)) || hi < kTile, lo, hi, sk);
             accumulate(p);
             issue_fence();
             load_values(rec, sub, unit);
@@ -589,9 +506,10 @@ struct Partial {
     static __device__ __forceinline__ float* at(float* ws, int wg, int slot) { return ws + (2 * wg + slot) * kFloats; }
 };
 
-template <int DT, int KIND, int D, int HT>
+template <int DT, int KIND, int D, int HT, bool SINKS>
 __global__ __launch_bounds__(256, (kPerCU<KIND, D, HT>)) void attention_kernel(AttentionArgs a) {
-    using A = Attend<DT, KIND, D, HT>;
+    using A = Attend<DT, KIND, D, HT, SINKS>;
+    using Sp = Span<SINKS>;
     using Pt = Partial<D, HT>;
     extern __shared__ __align__(16) float lds[];
     __shared__ int s_last;
@@ -610,7 +528,7 @@ __global__ __launch_bounds__(256, (kPerCU<KIND, D, HT>)) void attention_kernel(A
     int length = 0;
     for (int64_t b = lane * run, e = b + run < a.B ? b + run : a.B; b < e; ++b) {
         length = a.lengths[b];
-        const int n = Span(a, length).count;
+        const int n = Sp(a, length).count;
         sums += (int64_t)A::slots_of(n) << kChunkBits;
         if ((sums & kChunkMask) < kChunkMost) sums += chunks_of(n) < kChunkMost ? chunks_of(n) : kChunkMost;
     }
@@ -618,7 +536,7 @@ __global__ __launch_bounds__(256, (kPerCU<KIND, D, HT>)) void attention_kernel(A
     // Sequences that see nothing.
     for (int64_t b = wg; b < a.B; b += wgs) {
         const int len = run == 1 ? __builtin_amdgcn_readlane(length, (int)b) : a.lengths[b];
-        if (Span(a, len).count != 0) continue;
+        if (Sp(a, len).count != 0) continue;
         uint16_t* out = a.out + b * a.o_ts;
         for (int i = threadIdx.x; i < a.H * group * D; i += 256) out[(int64_t)(i / D) * a.o_hs + i % D] = 0;
     }
@@ -636,7 +554,7 @@ __global__ __launch_bounds__(256, (kPerCU<KIND, D, HT>)) void attention_kernel(A
         // fits: a run across two heads starts and ends twice (64 x 4096 tokens
         // of one kv head, 32 query heads: 36 and 32 us; 4 x 9000 of 8 heads of
         // 256 in int8 39 and 33).
-        const int n = Span(a, length).count;
+        const int n = Sp(a, length).count;
         const int most = (int)per + A::kHeadCost / 2, least = (int)per - A::kHeadCost;
         for (int c = most; c >= kMinTiles && c >= least; c -= A::kHeadCost / 2) {
             const int64_t items = (n + c - 1) / c, to = wave_scan(items);
@@ -660,7 +578,7 @@ __global__ __launch_bounds__(256, (kPerCU<KIND, D, HT>)) void attention_kernel(A
     auto block_at = [&](int64_t first, int64_t before) {  // `before`: items of the sequences before it
         base = first;
         length = base + lane < a.B ? a.lengths[base + lane] : 0;
-        const int n = Span(a, length).count;
+        const int n = Sp(a, length).count;
         seq_items = by_chunk ? chunks_of(n) : A::slots_of(n);
         seq_to = before + wave_scan(seq_items);
     };
@@ -676,7 +594,7 @@ __global__ __launch_bounds__(256, (kPerCU<KIND, D, HT>)) void attention_kernel(A
         const int64_t b = base + at;
         const int items = (int)read_lane(seq_items, at);  // of one unit
         const int64_t seq_end = units * read_lane(seq_to, at), seq_begin = seq_end - (int64_t)units * items;
-        const Span sp(a, __builtin_amdgcn_readlane(length, at));
+        const Sp sp(a, __builtin_amdgcn_readlane(length, at));
         int unit = divide(pos - seq_begin, items);
         for (; pos < end && pos < seq_end; ++unit) {
             const int64_t unit_begin = seq_begin + (int64_t)unit * items, unit_end = unit_begin + items;
@@ -828,7 +746,7 @@ Shape plan(const AttentionArgs& a, int kind) {
         s = kind == 0 ? shape_of<0, decltype(d)::value, decltype(ht)::value>() : shape_of<1, decltype(d)::value, decltype(ht)::value>();
     });
     int64_t tokens = a.width * a.P;
-    if (a.window > 0 && a.window < tokens) tokens = a.window + kTile;
+    if (a.window > 0 && a.window + a.sinks < tokens) tokens = a.window + kTile + (a.sinks > 0 ? a.sinks + kTile : 0);
     const int64_t parts = (tokens / kTile + kMinTiles) / kMinTiles;
     const int64_t units = (int64_t)a.H * ((group + s.heads - 1) / s.heads);
     s.wgs = kCUs * s.per_cu;
@@ -836,20 +754,26 @@ Shape plan(const AttentionArgs& a, int kind) {
     return s;
 }
 
-template <int DT, int KIND>
+template <int DT, int KIND, bool SINKS>
 hipError_t launch(const AttentionArgs& a, const Shape& s, hipStream_t stream) {
     hipError_t e = hipSuccess;
     const int group = a.Hq / a.H;
     by_shape(a.D, group, [&](auto d, auto ht) {
         constexpr int D = decltype(d)::value, HT = decltype(ht)::value;
         const int heads = group < 16 * HT ? group : 16 * HT;
-        const size_t lds = (size_t)kWaves * heads * (Attend<DT, KIND, D, HT>::kLd + 2) * 4;
-        e = allow_lds<attention_kernel<DT, KIND, D, HT>>(lds);
+        const size_t lds = (size_t)kWaves * heads * (Attend<DT, KIND, D, HT, SINKS>::kLd + 2) * 4;
+        e = allow_lds<attention_kernel<DT, KIND, D, HT, SINKS>>(lds);
         if (e != hipSuccess) return;
-        hipLaunchKernelGGL((attention_kernel<DT, KIND, D, HT>), dim3((unsigned)s.wgs), dim3(256), lds, stream, a);
+        hipLaunchKernelGGL((attention_kernel<DT, KIND, D, HT, SINKS>), dim3((unsigned)s.wgs), dim3(256), lds, stream, a);
         e = hipGetLastError();
     });
     return e;
+}
+
+template <bool SINKS>
+hipError_t launch_kind(const AttentionArgs& a, const Shape& s, int kind, int dtype, hipStream_t stream) {
+    if (kind == 0) return dtype == 0 ? launch<0, 0, SINKS>(a, s, stream) : launch<1, 0, SINKS>(a, s, stream);
+    return dtype == 0 ? launch<0, 1, SINKS>(a, s, stream) : launch<1, 1, SINKS>(a, s, stream);
 }
 
 }  // namespace
@@ -867,8 +791,7 @@ hipError_t launch_attention(AttentionArgs a, int kind, int dtype, void* workspac
     a.reach = (int)(a.window > 0 && a.window < all ? a.window : all);
     a.counters = static_cast<uint32_t*>(workspace);
     a.partials = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + kCounterRegionBytes);
-    if (kind == 0) return dtype == 0 ? launch<0, 0>(a, s, stream) : launch<1, 0>(a, s, stream);
-    return dtype == 0 ? launch<0, 1>(a, s, stream) : launch<1, 1>(a, s, stream);
+    return a.sinks > 0 ? launch_kind<true>(a, s, kind, dtype, stream) : launch_kind<false>(a, s, kind, dtype, stream);
 }
 
 }  // namespace w4a16

@@ -182,6 +182,20 @@ struct KvArgs {
     int shift = 0;            // set by the launch: log2(P), or -1
 };
 constexpr int kKvMaxD = 256;  // largest head size
+// kv_append: queries and keys turned by their positions.
+struct KvAppendArgs : KvArgs {
+    const uint16_t* q = nullptr;  // optional (Hq = 0)
+    uint16_t* q_out = nullptr;
+    int64_t q_ts = 0, q_hs = 0, o_ts = 0, o_hs = 0;
+    const int32_t* positions = nullptr;
+    const float* rates = nullptr;
+    int Hq = 0, pairs = 0;
+    bool neighbours = false;  // pairs (2 i, 2 i + 1), else (i, i + pairs)
+    // Set by the launch: groups of 32 tokens, heads turned by a workgroup, workgroups per group for them.
+    int groups = 0, per = 0, chunks = 0;
+};
+int64_t kv_append_workgroups(int64_t T, int64_t Hq, int64_t H);  // of launch_kv_append, at most 512 threads each
+hipError_t launch_kv_append(KvAppendArgs a, int kind, int dtype, hipStream_t stream);
 int64_t kv_workgroups(int64_t T, int64_t H);  // of launch_kv_write and launch_kv_read, 256 threads each
 hipError_t launch_kv_write(const KvArgs& a, int kind, int dtype, hipStream_t stream);
 hipError_t launch_kv_read(const KvArgs& a, int kind, int dtype, hipStream_t stream);
@@ -196,6 +210,7 @@ struct AttentionArgs {
     int64_t width = 0, table_ld = 0;
     const int32_t* lengths = nullptr;
     int64_t window = 0;
+    int sinks = 0;  // first tokens that a window leaves visible
     int Hq = 0, H = 0, D = 0, P = 0;
     float scale = 0.0f;
     // Set by launch_attention: Hq / H, the longest length the table allows, the
@@ -208,5 +223,47 @@ struct AttentionArgs {
 // that several workgroups share. Only sizes are read from `a`.
 size_t attention_workspace(const AttentionArgs& a, int kind);
 hipError_t launch_attention(AttentionArgs a, int kind, int dtype, void* workspace, hipStream_t stream);
+
+struct TokensArgs {
+    const uint16_t* q = nullptr;  // [T, Hq, D]: the new tokens of all sequences
+    uint16_t* out = nullptr;
+    int64_t T = 0, B = 0, q_ts = 0, q_hs = 0, o_ts = 0, o_hs = 0;
+    const int32_t* starts = nullptr;  // [B + 1] rows at which sequences begin
+    const uint64_t* tree = nullptr;   // optional: [T, tree_words] masks, rows tree_ld apart
+    int tree_words = 0;
+    int64_t tree_ld = 0;
+    const unsigned char* cache = nullptr;
+    int64_t pages = 0;
+    const int32_t* table = nullptr;  // [B, width], rows table_ld apart
+    int64_t width = 0, table_ld = 0;
+    const int32_t* lengths = nullptr;
+    int64_t window = 0;
+    int sinks = 0;  // first tokens that a window leaves visible
+    int Hq = 0, H = 0, D = 0, P = 0;
+    float scale = 0.0f;
+    // Set by launch_attention_tokens: Hq / H, the longest length the table
+    // allows, the window as a number of tokens, the workspace's parts.
+    int group = 0, most = 0;
+    int64_t reach = 0;
+    void* records = nullptr;
+    float* partials = nullptr;
+};
+size_t attention_tokens_workspace(const TokensArgs& a, int kind);  // only sizes are read
+hipError_t launch_attention_tokens(TokensArgs a, int kind, int dtype, void* workspace, hipStream_t stream);
+
+struct SampleArgs {
+    const uint16_t* logits = nullptr;
+    int64_t M = 0, ldl = 0;  // rows, their stride
+    int V = 0;
+    const float* uniforms = nullptr;
+    const float* temperature = nullptr;  // optional, one a row, as the next three
+    const int32_t* top_k = nullptr;
+    const float* top_p = nullptr;
+    const float* min_p = nullptr;
+    int64_t* tokens = nullptr;
+    float* probs = nullptr;  // optional
+};
+constexpr int64_t kSampleMaxV = (int64_t)1 << 22;  // logits of a row
+hipError_t launch_sample(const SampleArgs& a, int dtype, hipStream_t stream);
 
 }  // namespace w4a16

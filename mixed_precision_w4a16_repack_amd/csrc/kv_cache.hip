@@ -158,77 +158,57 @@ struct Group {
 __device__ __forceinline__ uint32_t lows(uint32_t x, uint32_t y) { return __builtin_amdgcn_perm(y, x, 0x05040100u); }
 __device__ __forceinline__ uint32_t highs(uint32_t x, uint32_t y) { return __builtin_amdgcn_perm(y, x, 0x07060302u); }
 
-// blockIdx.y: keys or values.
+// int8: the coders of a group's rows `src`, by two waves; four lanes hold a
+// row. Keys are written from here; of values it is the scale.
 template <int DT, int KIND, int D>
-__global__ __launch_bounds__(256) void kv_write_tile_kernel(KvArgs a) {
+__device__ __forceinline__ void row_coders(const KvArgs& a, const Group& grp, const uint16_t* src, int64_t ts, bool keys, Coder* s_code) {
     using L = KvPlace<KIND>;
-    __shared__ Coder s_code[32];  // int8: of the values
-    const int64_t t0 = (int64_t)(blockIdx.x / a.H) * 32;
-    const int h = blockIdx.x % a.H;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const bool keys = blockIdx.y == 0;
-    const Group grp(a, t0, h, L::record_bytes(D, a.P));
-    const uint16_t* src = keys ? a.k + t0 * a.k_ts + h * a.k_hs : a.v + t0 * a.v_ts + h * a.v_hs;
-    const int64_t ts = keys ? a.k_ts : a.v_ts;
-
-    if (KIND == 0 && keys) {
-        // 16 tokens x 4 pieces of 8 d a wave and step.
-        for (int i = threadIdx.x; i < 32 * (D / 8); i += 256) {
-            const int j = i % 16 + i / (16 * (D / 8)) * 16, c = i / 16 % (D / 8);
-            const int64_t rec = grp.rec_of(j);
-            const int t = grp.t_of(j);
-            if (rec >= 0)
-                *reinterpret_cast<u32x4*>(a.cache + rec + L::key(t, 8 * c, D)) = *reinterpret_cast<const u32x4_any*>(src + j * ts + 8 * c);
-        }
-        return;
+    const int j = wave * 16 + lane % 16, g = lane / 16;
+    const int64_t rec = grp.rec_of(j);
+    const int t = grp.t_of(j);
+    u32x4 x[D / 32];
+    uint32_t top = 0u;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {
+        x[i] = u32x4{0u, 0u, 0u, 0u};
+        if (rec >= 0) x[i] = *reinterpret_cast<const u32x4_any*>(src + j * ts + 8 * g + 32 * i);
     }
-    if (KIND == 1) {
-        // Four lanes hold a row. Keys are written from here; of values it is the scale.
-        if (wave < 2) {
-            const int j = wave * 16 + lane % 16, g = lane / 16;
-            const int64_t rec = grp.rec_of(j);
-            const int t = grp.t_of(j);
-            u32x4 x[D / 32];
-            uint32_t top = 0u;
 #pragma unroll
-            for (int i = 0; i < D / 32; ++i) {
-                x[i] = u32x4{0u, 0u, 0u, 0u};
-                if (rec >= 0) x[i] = *reinterpret_cast<const u32x4_any*>(src + j * ts + 8 * g + 32 * i);
-            }
+    for (int i = 0; i < D / 32; ++i)
 #pragma unroll
-            for (int i = 0; i < D / 32; ++i)
+        for (int e = 0; e < 4; ++e) top = larger(top, pair_top(x[i][e]));
+    const float amax = act_to_float<DT>((uint16_t)lanes_top(top, 16)), s = amax / 127.0f;
+    const Coder code(amax);
+    if (rec >= 0) {
+        if (g == 0) *reinterpret_cast<float*>(a.cache + rec + L::scale(t, D, a.P, keys ? 0 : 1)) = s;
+        if (keys) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) top = larger(top, pair_top(x[i][e]));
-            const float amax = act_to_float<DT>((uint16_t)lanes_top(top, 16)), s = amax / 127.0f;
-            const Coder code(amax);
-            if (rec >= 0) {
-                if (g == 0) *reinterpret_cast<float*>(a.cache + rec + L::scale(t, D, a.P, keys ? 0 : 1)) = s;
-                if (keys) {
+            for (int i = 0; i < D / 64; ++i) {
+                u32x4 out;
 #pragma unroll
-                    for (int i = 0; i < D / 64; ++i) {
-                        u32x4 out;
-#pragma unroll
-                        for (int w = 0; w < 4; ++w) {
-                            const uint32_t p0 = x[2 * i + w / 2][w % 2 * 2], p1 = x[2 * i + w / 2][w % 2 * 2 + 1];
-                            out[w] = code(low<DT>(p0)) | code(high<DT>(p0)) << 8 | code(low<DT>(p1)) << 16 | code(high<DT>(p1)) << 24;
-                        }
-                        *reinterpret_cast<u32x4*>(a.cache + rec + L::key(t, 64 * i + 8 * g, D)) = out;
-                    }
+                for (int w = 0; w < 4; ++w) {
+                    const uint32_t p0 = x[2 * i + w / 2][w % 2 * 2], p1 = x[2 * i + w / 2][w % 2 * 2 + 1];
+                    out[w] = code(low<DT>(p0)) | code(high<DT>(p0)) << 8 | code(low<DT>(p1)) << 16 | code(high<DT>(p1)) << 24;
                 }
+                *reinterpret_cast<u32x4*>(a.cache + rec + L::key(t, 64 * i + 8 * g, D)) = out;
             }
-            if (!keys && g == 0) s_code[j] = code;
         }
-        if (keys) return;
-        __syncthreads();
     }
+    if (!keys && g == 0) s_code[j] = code;
+}
 
-    // Values.
+// The values of a group, from rows `src` (ts apart), by THREADS threads; int8:
+// s_code holds each row's coder.
+template <int DT, int KIND, int D, int THREADS>
+__device__ __forceinline__ void write_values(const KvArgs& a, const Group& grp, const uint16_t* src, int64_t ts, const Coder* s_code) {
+    using L = KvPlace<KIND>;
     auto pair_at = [&](int j, int d) { return (uint32_t)*reinterpret_cast<const u32_any*>(src + j * ts + d); };
     if (grp.tile) {
         unsigned char* rec = a.cache + grp.rec_of(0);
         const int t = grp.t_of(0);
         if constexpr (KIND == 0) {
-            for (int i = threadIdx.x; i < 4 * (D / 2); i += 256) {
+            for (int i = threadIdx.x; i < 4 * (D / 2); i += THREADS) {
                 const int tg = i / (D / 2), d = i % (D / 2) * 2;
                 uint32_t w[8];
 #pragma unroll
@@ -244,7 +224,7 @@ __global__ __launch_bounds__(256) void kv_write_tile_kernel(KvArgs a) {
                 out[1] = hi;
             }
         } else {
-            for (int i = threadIdx.x; i < 4 * (D / 2); i += 256) {
+            for (int i = threadIdx.x; i < 4 * (D / 2); i += THREADS) {
                 const int tg = i / (D / 2), d = i % (D / 2) * 2;
                 uint32_t w[8];
 #pragma unroll
@@ -265,7 +245,7 @@ __global__ __launch_bounds__(256) void kv_write_tile_kernel(KvArgs a) {
     }
     // Groups of 4 tokens; of a run the aligned ones, from token -phase on.
     const int groups = grp.run ? 9 : 8, f = grp.run ? grp.phase : 0;
-    for (int i = threadIdx.x; i < (groups * (D / 2) + 63) / 64 * 64; i += 256) {  // whole waves
+    for (int i = threadIdx.x; i < (groups * (D / 2) + 63) / 64 * 64; i += THREADS) {  // whole waves
         const int j0 = i / (D / 2) * 4 - f, d = i % (D / 2) * 2;
         int64_t rec[4];
         int t[4];
@@ -308,6 +288,248 @@ __global__ __launch_bounds__(256) void kv_write_tile_kernel(KvArgs a) {
                 out[16] = (unsigned char)(w[j] >> 16);
             }
         }
+    }
+}
+
+// blockIdx.y: keys or values.
+template <int DT, int KIND, int D>
+__global__ __launch_bounds__(256) void kv_write_tile_kernel(KvArgs a) {
+    using L = KvPlace<KIND>;
+    __shared__ Coder s_code[32];  // int8: of the values
+    const int64_t t0 = (int64_t)(blockIdx.x / a.H) * 32;
+    const int h = blockIdx.x % a.H;
+    const int wave = threadIdx.x >> 6;
+    const bool keys = blockIdx.y == 0;
+    const Group grp(a, t0, h, L::record_bytes(D, a.P));
+    const uint16_t* src = keys ? a.k + t0 * a.k_ts + h * a.k_hs : a.v + t0 * a.v_ts + h * a.v_hs;
+    const int64_t ts = keys ? a.k_ts : a.v_ts;
+
+    if (KIND == 0 && keys) {
+        // 16 tokens x 4 pieces of 8 d a wave and step.
+        for (int i = threadIdx.x; i < 32 * (D / 8); i += 256) {
+            const int j = i % 16 + i / (16 * (D / 8)) * 16, c = i / 16 % (D / 8);
+            const int64_t rec = grp.rec_of(j);
+            const int t = grp.t_of(j);
+            if (rec >= 0)
+                *reinterpret_cast<u32x4*>(a.cache + rec + L::key(t, 8 * c, D)) = *reinterpret_cast<const u32x4_any*>(src + j * ts + 8 * c);
+        }
+        return;
+    }
+    if constexpr (KIND == 1) {
+        if (wave < 2) row_coders<DT, KIND, D>(a, grp, src, ts, keys, s_code);
+        if (keys) return;
+        __syncthreads();
+    }
+    write_values<DT, KIND, D, 256>(a, grp, src, ts, s_code);
+}
+
+// ---- kv_append: the same writes with the queries and keys turned by their
+// positions on the way. Pair i of a token's row is turned by the angle
+// position * rate[i], which is reduced to a part of a turn in fp64 (position
+// and rate have 31 and 24 bits: in fp32 a far position would lose the angle);
+// sine and cosine are Taylor sums of an eighth of a turn.
+struct Angle {
+    float c, s;
+};
+__device__ __forceinline__ Angle angle_of(int position, float rate) {
+    double turn = (double)position * ((double)rate * 0.15915494309189533577);
+    turn -= __builtin_rint(turn);
+    const double quarters = __builtin_rint(turn * 4.0);
+    const float x = (float)((turn - quarters * 0.25) * 6.28318530717958647693), y = x * x;  // |x| <= pi / 4
+    float s = __builtin_fmaf(y, 1.0f / 362880.0f, -1.0f / 5040.0f);
+    s = __builtin_fmaf(y, s, 1.0f / 120.0f);
+    s = __builtin_fmaf(y, s, -1.0f / 6.0f);
+    s = __builtin_fmaf(x * y, s, x);
+    float c = __builtin_fmaf(y, -1.0f / 3628800.0f, 1.0f / 40320.0f);
+    c = __builtin_fmaf(y, c, -1.0f / 720.0f);
+    c = __builtin_fmaf(y, c, 1.0f / 24.0f);
+    c = __builtin_fmaf(y, c, -0.5f);
+    c = __builtin_fmaf(y, c, 1.0f);
+    const int k = (int)quarters;
+    const float a = k & 1 ? s : c, b = k & 1 ? c : s;
+    return {(k + 1) & 2 ? -a : a, k & 2 ? -b : b};
+}
+__device__ __forceinline__ void turn(const Angle& w, float& x, float& y) {
+    const float p = __builtin_fmaf(x, w.c, -(y * w.s)), q = __builtin_fmaf(y, w.c, x * w.s);
+    x = p;
+    y = q;
+}
+
+// One wave per (token, query or key or value head); a lane holds pairs.
+template <int DT, int KIND>
+__global__ __launch_bounds__(256) void kv_append_rows_kernel(KvAppendArgs a) {
+    using L = KvPlace<KIND>;
+    const int lane = threadIdx.x & 63;
+    const int unit = blockIdx.x * 4 + (threadIdx.x >> 6), heads = a.Hq + 2 * a.H;
+    const int tok = unit / heads, r = unit - tok * heads;
+    if (tok >= a.T) return;
+    const bool query = r < a.Hq, value = r >= a.Hq + a.H;
+    const int h = query ? r : (value ? r - a.Hq - a.H : r - a.Hq);
+    unsigned char* rec = nullptr;
+    int t = 0;
+    if (!query) {
+        const int64_t slot = a.slots[tok];
+        if (slot < 0 || slot >= a.pages * a.P) return;
+        const Place at = place_of(a, slot);
+        rec = a.cache + (at.page * a.H + h) * L::record_bytes(a.D, a.P);
+        t = at.t;
+    }
+    const uint16_t* src = query ? a.q + tok * a.q_ts + h * a.q_hs : (value ? a.v + tok * a.v_ts + h * a.v_hs : a.k + tok * a.k_ts + h * a.k_hs);
+    const int position = value ? 0 : a.positions[tok];
+    constexpr int N = kKvMaxD / 128;
+    int d[N][2];
+    float x[N][2];
+    uint32_t top = 0u;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const int u = 64 * i + lane;
+        if (u >= a.D / 2) break;
+        const bool turned = !value && u < a.pairs, apart = u < a.pairs && !a.neighbours;
+        d[i][0] = apart ? u : 2 * u;
+        d[i][1] = apart ? u + a.pairs : 2 * u + 1;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) x[i][e] = act_to_float<DT>(src[d[i][e]]);
+        if (turned) turn(angle_of(position, a.rates[u]), x[i][0], x[i][1]);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) top = larger(top, __builtin_bit_cast(uint32_t, x[i][e]) & 0x7FFFFFFFu);
+    }
+    Coder code;
+    if (KIND == 1 && !query) {
+        const float amax = __builtin_bit_cast(float, lanes_top(top, 1));
+        code = Coder(amax);
+        if (lane == 0) *reinterpret_cast<float*>(rec + L::scale(t, a.D, a.P, value ? 1 : 0)) = amax / 127.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        if (64 * i + lane >= a.D / 2) break;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            if (query) {
+                a.q_out[tok * a.o_ts + h * a.o_hs + d[i][e]] = to_act_bits<DT>(x[i][e]);
+                continue;
+            }
+            unsigned char* to = rec + (value ? L::value(t, d[i][e], a.D, a.P) : L::key(t, d[i][e], a.D));
+            if constexpr (KIND == 0) *reinterpret_cast<uint16_t*>(to) = to_act_bits<DT>(x[i][e]);
+            else *to = (unsigned char)code(x[i][e]);
+        }
+    }
+}
+
+// Groups of 32 tokens: first the workgroups that turn `per` query or key heads
+// each, then those that write a head's values. Every thread holds the same
+// 8 pairs of one token in all of its heads, and so their sines once.
+template <int DT, int KIND, int D>
+__global__ __launch_bounds__(2 * D) void kv_append_tile_kernel(KvAppendArgs a) {
+    using L = KvPlace<KIND>;
+    constexpr int kParts = D / 64;  // waves that share a token's row
+    __shared__ Coder s_code[32];
+    __shared__ uint32_t s_top[2][kParts][32];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t record = L::record_bytes(D, a.P);
+    const int turning = a.groups * a.chunks;
+    if ((int)blockIdx.x >= turning) {
+        const int at = blockIdx.x - turning, g = at / a.H, h = at - g * a.H;
+        const int64_t t0 = (int64_t)g * 32;
+        const Group grp(a, t0, h, record);
+        const uint16_t* src = a.v + t0 * a.v_ts + h * a.v_hs;
+        if constexpr (KIND == 1) {
+            if (wave < 2) row_coders<DT, KIND, D>(a, grp, src, a.v_ts, false, s_code);
+            __syncthreads();
+        }
+        write_values<DT, KIND, D, 2 * D>(a, grp, src, a.v_ts, s_code);
+        return;
+    }
+    const int g = blockIdx.x / a.chunks, chunk = blockIdx.x - g * a.chunks;
+    const int64_t t0 = (int64_t)g * 32;
+    const Group grp(a, t0, 0, record);
+    const int part = wave % kParts;
+    const int j = wave / kParts * 16 + lane % 16, pp = 4 * part + lane / 16;
+    const bool in = j < grp.n, turned = 8 * pp < a.pairs, apart = turned && !a.neighbours;
+    const int64_t rec = grp.rec_of(j), tok = t0 + j;
+    const int t = grp.t_of(j);
+    const int c0 = apart ? pp : 2 * pp, c1 = apart ? pp + a.pairs / 8 : 2 * pp + 1;
+    Angle w[8];
+    if (turned) {
+        const int position = in ? a.positions[tok] : 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = angle_of(position, a.rates[8 * pp + i]);
+    }
+    const int first = chunk * a.per, last = first + a.per < a.Hq + a.H ? first + a.per : a.Hq + a.H;
+    auto load = [&](int head, u32x4& lo, u32x4& hi) {
+        const uint16_t* src = head < a.Hq ? a.q + tok * a.q_ts + head * a.q_hs : a.k + tok * a.k_ts + (head - a.Hq) * a.k_hs;
+        lo = hi = u32x4{0u, 0u, 0u, 0u};
+        if (in) {
+            lo = *reinterpret_cast<const u32x4_any*>(src + 8 * c0);
+            hi = *reinterpret_cast<const u32x4_any*>(src + 8 * c1);
+        }
+    };
+    u32x4 lo, hi, next_lo, next_hi;
+    load(first, lo, hi);
+    for (int head = first; head < last; ++head) {
+        if (head + 1 < last) load(head + 1, next_lo, next_hi);
+        float x[2][8];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            x[0][2 * e] = low<DT>(lo[e]);
+            x[0][2 * e + 1] = high<DT>(lo[e]);
+            x[1][2 * e] = low<DT>(hi[e]);
+            x[1][2 * e + 1] = high<DT>(hi[e]);
+        }
+        if (turned) {
+            if (apart) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) turn(w[i], x[0][i], x[1][i]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) turn(w[i], x[i / 4][i % 4 * 2], x[i / 4][i % 4 * 2 + 1]);
+            }
+        }
+        if (KIND == 0 || head < a.Hq) {
+            u32x4 y[2];
+#pragma unroll
+            for (int p = 0; p < 2; ++p)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    y[p][e] = (uint32_t)to_act_bits<DT>(x[p][2 * e]) | (uint32_t)to_act_bits<DT>(x[p][2 * e + 1]) << 16;
+            if (head < a.Hq) {
+                if (in) {
+                    uint16_t* out = a.q_out + tok * a.o_ts + head * a.o_hs;
+                    *reinterpret_cast<u32x4_any*>(out + 8 * c0) = y[0];
+                    *reinterpret_cast<u32x4_any*>(out + 8 * c1) = y[1];
+                }
+            } else if (rec >= 0) {
+                unsigned char* out = a.cache + rec + (head - a.Hq) * record;
+                *reinterpret_cast<u32x4*>(out + L::key(t, 8 * c0, D)) = y[0];
+                *reinterpret_cast<u32x4*>(out + L::key(t, 8 * c1, D)) = y[1];
+            }
+        } else {
+            uint32_t top = 0u;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) top = larger(top, __builtin_bit_cast(uint32_t, x[i / 8][i % 8]) & 0x7FFFFFFFu);
+            top = lanes_top(top, 16);
+            if constexpr (kParts > 1) {  // two buffers: one barrier a head
+                uint32_t(&all)[kParts][32] = s_top[head & 1];
+                if (lane < 16) all[part][j] = top;
+                __syncthreads();
+#pragma unroll
+                for (int p = 0; p < kParts; ++p) top = larger(top, all[p][j]);
+            }
+            const float amax = __builtin_bit_cast(float, top);
+            const Coder code(amax);
+            if (rec >= 0) {
+                unsigned char* out = a.cache + rec + (head - a.Hq) * record;
+                if (pp == 0) *reinterpret_cast<float*>(out + L::scale(t, D, a.P, 0)) = amax / 127.0f;
+#pragma unroll
+                for (int p = 0; p < 2; ++p) {
+                    u32x2 y{0u, 0u};
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) y[i / 4] |= code(x[p][i]) << (8 * (i % 4));
+                    *reinterpret_cast<u32x2*>(out + L::key(t, 8 * (p == 0 ? c0 : c1), D)) = y;
+                }
+            }
+        }
+        lo = next_lo;
+        hi = next_hi;
     }
 }
 
@@ -491,7 +713,41 @@ hipError_t run(KvArgs a, bool write, int kind, int dtype, hipStream_t stream) {
     return hipGetLastError();
 }
 
+// Up to this many (token, head) of queries, keys and values, a wave for each.
+constexpr int64_t kAppendRowsMost = 8192;
+
+template <int DT, int KIND>
+void launch_append(KvAppendArgs& a, hipStream_t stream) {
+    const int64_t rows = a.T * (a.Hq + 2 * (int64_t)a.H);
+    if (rows <= kAppendRowsMost) {
+        hipLaunchKernelGGL((kv_append_rows_kernel<DT, KIND>), dim3((unsigned)((rows + 3) / 4)), dim3(256), 0, stream, a);
+        return;
+    }
+    a.groups = (int)((a.T + 31) / 32);
+    const int heads = a.Hq + a.H;
+    const int64_t want = ((int64_t)a.groups * heads + 1023) / 1024;  // about 1024 workgroups turn
+    a.per = (int)(want < 16 ? want : 16);
+    a.chunks = (heads + a.per - 1) / a.per;
+    const dim3 grid((unsigned)((int64_t)a.groups * (a.chunks + a.H)));
+    by_head_dim(a.D, [&](auto d) {
+        constexpr int D = decltype(d)::value;
+        hipLaunchKernelGGL((kv_append_tile_kernel<DT, KIND, D>), grid, dim3(2 * D), 0, stream, a);
+    });
+}
+
 }  // namespace
+
+int64_t kv_append_workgroups(int64_t T, int64_t Hq, int64_t H) {
+    const int64_t rows = T * (Hq + 2 * H);
+    return rows <= kAppendRowsMost ? (rows + 3) / 4 : (T + 31) / 32 * (Hq + 2 * H);
+}
+
+hipError_t launch_kv_append(KvAppendArgs a, int kind, int dtype, hipStream_t stream) {
+    a.shift = (a.P & (a.P - 1)) == 0 ? __builtin_ctz(a.P) : -1;
+    if (kind == 0) dtype == 0 ? launch_append<0, 0>(a, stream) : launch_append<1, 0>(a, stream);
+    else dtype == 0 ? launch_append<0, 1>(a, stream) : launch_append<1, 1>(a, stream);
+    return hipGetLastError();
+}
 
 int64_t kv_workgroups(int64_t T, int64_t H) { return T * H <= kRowsMost ? (T * H * 2 + 3) / 4 : (T + 31) / 32 * H; }
 

@@ -646,12 +646,14 @@ w4a16_status kv_impl(bool write, const void* k, int64_t k_ts, int64_t k_hs, cons
 }
 
 // Shape rules of the attention calls.
-w4a16_status check_attention(int64_t B, int32_t q_heads, int32_t kv_heads, int32_t page_size, int64_t table_width, int64_t window) {
+w4a16_status check_attention(int64_t B, int32_t q_heads, int32_t kv_heads, int32_t page_size, int64_t table_width, int64_t window,
+                             int64_t sinks) {
     if (B < 0) return fail(W4A16_ERR_INVALID_ARG, "B=%lld must be >= 0", (long long)B);
     if (q_heads <= 0 || q_heads % kv_heads != 0)
         return fail(W4A16_ERR_INVALID_ARG, "q_heads=%d must be a positive multiple of kv_heads=%d", q_heads, kv_heads);
     if (table_width < 0) return fail(W4A16_ERR_INVALID_ARG, "table_width=%lld must be >= 0", (long long)table_width);
     if (window < 0) return fail(W4A16_ERR_INVALID_ARG, "window=%lld must be >= 0", (long long)window);
+    if (sinks < 0) return fail(W4A16_ERR_INVALID_ARG, "sinks=%lld must be >= 0", (long long)sinks);
     if (q_heads > (1 << 20) || B > (int64_t)1 << 31 || B * q_heads >= (int64_t)1 << 31)
         return fail(W4A16_ERR_UNSUPPORTED, "B=%lld sequences of q_heads=%d are too large for one launch", (long long)B, q_heads);
     if (table_width > (((int64_t)1 << 31) + page_size - 1) / page_size)
@@ -660,6 +662,28 @@ w4a16_status check_attention(int64_t B, int32_t q_heads, int32_t kv_heads, int32
     if (B > 0 && table_width > ((int64_t)1 << 43) / page_size / B)
         return fail(W4A16_ERR_UNSUPPORTED, "a table of B=%lld rows of %lld pages holds more than 2^43 tokens", (long long)B,
                     (long long)table_width);
+    return W4A16_OK;
+}
+
+// First tokens that a window leaves visible, as a number that a length is compared with.
+int sinks_of(int64_t window, int64_t sinks) {
+    const int64_t most = ((int64_t)1 << 31) - 1;
+    return window > 0 ? (int)(sinks < most ? sinks : most) : 0;
+}
+
+w4a16_status check_tokens(int64_t T, int32_t q_heads) {
+    if (T < 0) return fail(W4A16_ERR_INVALID_ARG, "T=%lld must be >= 0", (long long)T);
+    if (T > (int64_t)1 << 31 || (q_heads > 0 && T * q_heads >= (int64_t)1 << 31))
+        return fail(W4A16_ERR_UNSUPPORTED, "T=%lld tokens of q_heads=%d are too large for one launch", (long long)T, q_heads);
+    return W4A16_OK;
+}
+
+w4a16_status check_workspace(const void* workspace, size_t workspace_bytes, size_t need) {
+    if (workspace == nullptr || workspace_bytes < need)
+        return fail(W4A16_ERR_SIZE, "workspace of %zu bytes is smaller than the %zu bytes this call needs",
+                    workspace == nullptr ? (size_t)0 : workspace_bytes, need);
+    if (reinterpret_cast<uintptr_t>(workspace) & 255u)
+        return fail(W4A16_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
     return W4A16_OK;
 }
 
@@ -723,16 +747,72 @@ w4a16_status w4a16_kv_read(const int64_t* slots, int64_t T, const void* cache, s
                    page_size, kind, dtype, stream);
 }
 
+w4a16_status w4a16_kv_append(const void* q, int64_t q_ts, int64_t q_hs, int32_t q_heads, void* q_out, int64_t o_ts,
+                             int64_t o_hs, const void* k, int64_t k_ts, int64_t k_hs, const void* v, int64_t v_ts,
+                             int64_t v_hs, int64_t T, const int32_t* positions, const float* rates, int32_t pairs,
+                             int32_t neighbours, const int64_t* slots, void* cache, size_t cache_bytes, int64_t pages,
+                             int32_t kv_heads, int32_t head_dim, int32_t page_size, int32_t kind, int32_t dtype,
+                             hipStream_t stream) {
+    clear_error();
+    size_t need = 0;
+    w4a16_status st = check_cache(pages, kv_heads, head_dim, page_size, kind, &need);
+    if (st != W4A16_OK || (st = check_dtype(dtype)) != W4A16_OK) return st;
+    if (T < 0) return fail(W4A16_ERR_INVALID_ARG, "T=%lld must be >= 0", (long long)T);
+    if (q_heads < 0) return fail(W4A16_ERR_INVALID_ARG, "q_heads=%d must be >= 0", q_heads);
+    if (q_heads > (1 << 20)) return fail(W4A16_ERR_UNSUPPORTED, "q_heads=%d must be at most 2^20", q_heads);
+    if (pairs <= 0 || pairs % 8 != 0 || 2 * (int64_t)pairs > head_dim)
+        return fail(W4A16_ERR_UNSUPPORTED, "pairs=%d must be a positive multiple of 8, at most head_dim / 2 = %d", pairs,
+                    head_dim / 2);
+    if (neighbours != 0 && neighbours != 1) return fail(W4A16_ERR_INVALID_ARG, "neighbours=%d must be 0 or 1", neighbours);
+    if ((st = check_head_strides("k", k_ts, k_hs)) != W4A16_OK || (st = check_head_strides("v", v_ts, v_hs)) != W4A16_OK)
+        return st;
+    if (q_heads > 0 && ((st = check_head_strides("q", q_ts, q_hs)) != W4A16_OK || (st = check_head_strides("q_out", o_ts, o_hs)) != W4A16_OK))
+        return st;
+    if (T == 0) return W4A16_OK;
+    if (T > kMaxThreads / 2 || kv_append_workgroups(T, q_heads, kv_heads) > kMaxThreads / 512)
+        return fail(W4A16_ERR_UNSUPPORTED, "T=%lld is too large for one launch", (long long)T);
+    if (k == nullptr || v == nullptr || slots == nullptr || positions == nullptr || rates == nullptr)
+        return fail(W4A16_ERR_INVALID_ARG, "k, v, positions, rates and slots must not be NULL");
+    if (q_heads > 0 && (q == nullptr || q_out == nullptr)) return fail(W4A16_ERR_INVALID_ARG, "q and q_out must not be NULL");
+    if (!aligned_to(k, 2) || !aligned_to(v, 2) || (q_heads > 0 && (!aligned_to(q, 2) || !aligned_to(q_out, 2))))
+        return fail(W4A16_ERR_INVALID_ARG, "q, q_out, k and v must be 2-byte aligned");
+    if (!aligned_to(slots, 8)) return fail(W4A16_ERR_INVALID_ARG, "slots must be 8-byte aligned");
+    if (!aligned_to(positions, 4) || !aligned_to(rates, 4))
+        return fail(W4A16_ERR_INVALID_ARG, "positions and rates must be 4-byte aligned");
+    if ((st = check_cache_buffer(cache, cache_bytes, need)) != W4A16_OK) return st;
+    KvAppendArgs a;
+    a.q = static_cast<const uint16_t*>(q);
+    a.q_out = static_cast<uint16_t*>(q_out);
+    a.q_ts = q_ts, a.q_hs = q_hs, a.o_ts = o_ts, a.o_hs = o_hs, a.Hq = q_heads;
+    a.k = static_cast<const uint16_t*>(k);
+    a.v = static_cast<const uint16_t*>(v);
+    a.T = T, a.k_ts = k_ts, a.k_hs = k_hs, a.v_ts = v_ts, a.v_hs = v_hs;
+    a.positions = positions, a.rates = rates, a.pairs = pairs, a.neighbours = neighbours != 0;
+    a.slots = slots;
+    a.cache = static_cast<unsigned char*>(cache);
+    a.pages = pages, a.H = kv_heads, a.D = head_dim, a.P = page_size;
+    hipError_t e = launch_kv_append(a, kind, dtype, stream);
+    if (e != hipSuccess) return hip_fail("kv_append kernel launch", e);
+    return W4A16_OK;
+}
+
 w4a16_status w4a16_attention_workspace_size(int64_t B, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
                                             int32_t page_size, int64_t table_width, int64_t window, int32_t kind,
                                             size_t* out_bytes) {
+    return w4a16_attention_sinks_workspace_size(B, q_heads, kv_heads, head_dim, page_size, table_width, window, 0, kind,
+                                                out_bytes);
+}
+
+w4a16_status w4a16_attention_sinks_workspace_size(int64_t B, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
+                                                  int32_t page_size, int64_t table_width, int64_t window, int64_t sinks,
+                                                  int32_t kind, size_t* out_bytes) {
     clear_error();
     if (out_bytes == nullptr) return fail(W4A16_ERR_INVALID_ARG, "out_bytes is NULL");
     size_t unused = 0;
     w4a16_status st = check_cache(0, kv_heads, head_dim, page_size, kind, &unused);
-    if (st != W4A16_OK || (st = check_attention(B, q_heads, kv_heads, page_size, table_width, window)) != W4A16_OK) return st;
+    if (st != W4A16_OK || (st = check_attention(B, q_heads, kv_heads, page_size, table_width, window, sinks)) != W4A16_OK) return st;
     AttentionArgs a;
-    a.B = B, a.width = table_width, a.window = window;
+    a.B = B, a.width = table_width, a.window = window, a.sinks = sinks_of(window, sinks);
     a.Hq = q_heads, a.H = kv_heads, a.D = head_dim, a.P = page_size;
     *out_bytes = B > 0 ? attention_workspace(a, kind) : 0;
     return W4A16_OK;
@@ -743,11 +823,22 @@ w4a16_status w4a16_attention(const void* q, int64_t q_bs, int64_t q_hs, int64_t 
                              int32_t kind, int32_t dtype, const int32_t* table, int64_t table_width, int64_t table_ld,
                              const int32_t* lengths, int64_t window, float scale, void* out, int64_t o_bs, int64_t o_hs,
                              void* workspace, size_t workspace_bytes, hipStream_t stream) {
+    return w4a16_attention_sinks(q, q_bs, q_hs, B, q_heads, cache, cache_bytes, pages, kv_heads, head_dim, page_size, kind,
+                                 dtype, table, table_width, table_ld, lengths, window, 0, scale, out, o_bs, o_hs, workspace,
+                                 workspace_bytes, stream);
+}
+
+w4a16_status w4a16_attention_sinks(const void* q, int64_t q_bs, int64_t q_hs, int64_t B, int32_t q_heads,
+                                   const void* cache, size_t cache_bytes, int64_t pages, int32_t kv_heads,
+                                   int32_t head_dim, int32_t page_size, int32_t kind, int32_t dtype,
+                                   const int32_t* table, int64_t table_width, int64_t table_ld, const int32_t* lengths,
+                                   int64_t window, int64_t sinks, float scale, void* out, int64_t o_bs, int64_t o_hs,
+                                   void* workspace, size_t workspace_bytes, hipStream_t stream) {
     clear_error();
     size_t need = 0;
     w4a16_status st = check_cache(pages, kv_heads, head_dim, page_size, kind, &need);
     if (st != W4A16_OK || (st = check_dtype(dtype)) != W4A16_OK ||
-        (st = check_attention(B, q_heads, kv_heads, page_size, table_width, window)) != W4A16_OK ||
+        (st = check_attention(B, q_heads, kv_heads, page_size, table_width, window, sinks)) != W4A16_OK ||
         (st = check_head_strides("q", q_bs, q_hs)) != W4A16_OK || (st = check_head_strides("out", o_bs, o_hs)) != W4A16_OK)
         return st;
     if ((st = check_row_stride("table_ld", table_ld, "table_width", table_width)) != W4A16_OK) return st;
@@ -768,17 +859,108 @@ w4a16_status w4a16_attention(const void* q, int64_t q_bs, int64_t q_hs, int64_t 
     a.table = table;
     a.width = table_width, a.table_ld = table_ld;
     a.lengths = lengths;
-    a.window = window;
+    a.window = window, a.sinks = sinks_of(window, sinks);
     a.Hq = q_heads, a.H = kv_heads, a.D = head_dim, a.P = page_size;
     a.scale = scale;
-    const size_t ws_need = attention_workspace(a, kind);
-    if (workspace == nullptr || workspace_bytes < ws_need)
-        return fail(W4A16_ERR_SIZE, "workspace of %zu bytes is smaller than the %zu bytes this call needs",
-                    workspace == nullptr ? (size_t)0 : workspace_bytes, ws_need);
-    if (reinterpret_cast<uintptr_t>(workspace) & 255u)
-        return fail(W4A16_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+    if ((st = check_workspace(workspace, workspace_bytes, attention_workspace(a, kind))) != W4A16_OK) return st;
     hipError_t e = launch_attention(a, kind, dtype, workspace, stream);
     if (e != hipSuccess) return hip_fail("attention kernel launch", e);
+    return W4A16_OK;
+}
+
+w4a16_status w4a16_attention_tokens_workspace_size(int64_t T, int64_t B, int32_t q_heads, int32_t kv_heads,
+                                                   int32_t head_dim, int32_t page_size, int64_t table_width,
+                                                   int32_t kind, size_t* out_bytes) {
+    clear_error();
+    if (out_bytes == nullptr) return fail(W4A16_ERR_INVALID_ARG, "out_bytes is NULL");
+    size_t unused = 0;
+    w4a16_status st = check_cache(0, kv_heads, head_dim, page_size, kind, &unused);
+    if (st != W4A16_OK || (st = check_tokens(T, q_heads)) != W4A16_OK ||
+        (st = check_attention(B, q_heads, kv_heads, page_size, table_width, 0, 0)) != W4A16_OK)
+        return st;
+    TokensArgs a;
+    a.T = T, a.B = B, a.width = table_width;
+    a.Hq = q_heads, a.H = kv_heads, a.D = head_dim, a.P = page_size;
+    *out_bytes = T > 0 && B > 0 ? attention_tokens_workspace(a, kind) : 0;
+    return W4A16_OK;
+}
+
+w4a16_status w4a16_attention_tokens(const void* q, int64_t q_ts, int64_t q_hs, int64_t T, int32_t q_heads,
+                                    const int32_t* starts, int64_t B, const int64_t* tree, int64_t tree_words,
+                                    int64_t tree_ld, const void* cache, size_t cache_bytes, int64_t pages,
+                                    int32_t kv_heads, int32_t head_dim, int32_t page_size, int32_t kind, int32_t dtype,
+                                    const int32_t* table, int64_t table_width, int64_t table_ld, const int32_t* lengths,
+                                    int64_t window, int64_t sinks, float scale, void* out, int64_t o_ts, int64_t o_hs,
+                                    void* workspace, size_t workspace_bytes, hipStream_t stream) {
+    clear_error();
+    size_t need = 0;
+    w4a16_status st = check_cache(pages, kv_heads, head_dim, page_size, kind, &need);
+    if (st != W4A16_OK || (st = check_dtype(dtype)) != W4A16_OK || (st = check_tokens(T, q_heads)) != W4A16_OK ||
+        (st = check_attention(B, q_heads, kv_heads, page_size, table_width, window, sinks)) != W4A16_OK ||
+        (st = check_head_strides("q", q_ts, q_hs)) != W4A16_OK || (st = check_head_strides("out", o_ts, o_hs)) != W4A16_OK)
+        return st;
+    if ((st = check_row_stride("table_ld", table_ld, "table_width", table_width)) != W4A16_OK) return st;
+    if (tree != nullptr) {
+        if (tree_words <= 0 || tree_words > (1 << 16))
+            return fail(W4A16_ERR_INVALID_ARG, "tree_words=%lld must be in 1 .. 2^16", (long long)tree_words);
+        if ((st = check_row_stride("tree_ld", tree_ld, "tree_words", tree_words)) != W4A16_OK) return st;
+        if (!aligned_to(tree, 8)) return fail(W4A16_ERR_INVALID_ARG, "tree must be 8-byte aligned");
+    }
+    if (!(scale >= -3.4e38f && scale <= 3.4e38f)) return fail(W4A16_ERR_INVALID_ARG, "scale=%g must be finite", (double)scale);
+    if (T == 0 || B == 0) return W4A16_OK;
+    if (q == nullptr || out == nullptr || starts == nullptr || lengths == nullptr || (table == nullptr && table_width > 0))
+        return fail(W4A16_ERR_INVALID_ARG, "q, starts, table, lengths and out must not be NULL");
+    if (!aligned_to(q, 2) || !aligned_to(out, 2)) return fail(W4A16_ERR_INVALID_ARG, "q and out must be 2-byte aligned");
+    if (!aligned_to(starts, 4) || !aligned_to(table, 4) || !aligned_to(lengths, 4))
+        return fail(W4A16_ERR_INVALID_ARG, "starts, table and lengths must be 4-byte aligned");
+    if ((st = check_cache_buffer(cache, cache_bytes, need)) != W4A16_OK) return st;
+    TokensArgs a;
+    a.q = static_cast<const uint16_t*>(q);
+    a.out = static_cast<uint16_t*>(out);
+    a.T = T, a.B = B, a.q_ts = q_ts, a.q_hs = q_hs, a.o_ts = o_ts, a.o_hs = o_hs;
+    a.starts = starts;
+    a.tree = reinterpret_cast<const uint64_t*>(tree);
+    a.tree_words = (int)(tree != nullptr ? tree_words : 0), a.tree_ld = tree_ld;
+    a.cache = static_cast<const unsigned char*>(cache);
+    a.pages = pages;
+    a.table = table;
+    a.width = table_width, a.table_ld = table_ld;
+    a.lengths = lengths;
+    a.window = window, a.sinks = sinks_of(window, sinks);
+    a.Hq = q_heads, a.H = kv_heads, a.D = head_dim, a.P = page_size;
+    a.scale = scale;
+    if ((st = check_workspace(workspace, workspace_bytes, attention_tokens_workspace(a, kind))) != W4A16_OK) return st;
+    hipError_t e = launch_attention_tokens(a, kind, dtype, workspace, stream);
+    if (e != hipSuccess) return hip_fail("attention_tokens kernel launch", e);
+    return W4A16_OK;
+}
+
+w4a16_status w4a16_sample(const void* logits, int64_t M, int64_t V, int64_t ldl, int32_t dtype, const float* uniforms,
+                          const float* temperature, const int32_t* top_k, const float* top_p, const float* min_p,
+                          int64_t* tokens, float* probs, hipStream_t stream) {
+    clear_error();
+    w4a16_status st = check_dtype(dtype);
+    if (st != W4A16_OK) return st;
+    if (M < 0) return fail(W4A16_ERR_INVALID_ARG, "M=%lld must be >= 0", (long long)M);
+    if (V <= 0) return fail(W4A16_ERR_INVALID_ARG, "V=%lld must be positive", (long long)V);
+    if (V > kSampleMaxV) return fail(W4A16_ERR_UNSUPPORTED, "V=%lld must be at most 2^22", (long long)V);
+    if ((st = check_row_stride("ldl", ldl, "V", V)) != W4A16_OK) return st;
+    if (M == 0) return W4A16_OK;
+    if (M > kMaxThreads / 1024) return fail(W4A16_ERR_UNSUPPORTED, "M=%lld is too large for one launch", (long long)M);
+    if (logits == nullptr || uniforms == nullptr || tokens == nullptr)
+        return fail(W4A16_ERR_INVALID_ARG, "logits, uniforms and tokens must not be NULL");
+    if (!aligned_to(logits, 2)) return fail(W4A16_ERR_INVALID_ARG, "logits must be 2-byte aligned");
+    if (!aligned_to(uniforms, 4) || !aligned_to(temperature, 4) || !aligned_to(top_k, 4) || !aligned_to(top_p, 4) ||
+        !aligned_to(min_p, 4) || !aligned_to(probs, 4))
+        return fail(W4A16_ERR_INVALID_ARG, "uniforms, temperature, top_k, top_p, min_p and probs must be 4-byte aligned");
+    if (!aligned_to(tokens, 8)) return fail(W4A16_ERR_INVALID_ARG, "tokens must be 8-byte aligned");
+    SampleArgs a;
+    a.logits = static_cast<const uint16_t*>(logits);
+    a.M = M, a.V = (int)V, a.ldl = ldl;
+    a.uniforms = uniforms, a.temperature = temperature, a.top_k = top_k, a.top_p = top_p, a.min_p = min_p;
+    a.tokens = tokens, a.probs = probs;
+    hipError_t e = launch_sample(a, dtype, stream);
+    if (e != hipSuccess) return hip_fail("sample kernel launch", e);
     return W4A16_OK;
 }
 
