@@ -6,6 +6,7 @@
 #include "device_common.h"
 #include "internal.h"
 #include "kv_layout.h"
+#include "lds_stage.h"
 
 namespace w4a16 {
 namespace {
@@ -45,8 +46,8 @@ struct Blocks {
         return (int)(((int64_t)m * a.group + ROWS - 1) / ROWS);
     }
     static __device__ __forceinline__ Span span(const TokensArgs& a, int m, int n, int j) {
-        const int64_t first = (int64_t)j * ROWS, last = first + ROWS - 1;
-        const int i0 = (int)(first / a.group), i1 = last / a.group < m ? (int)(last / a.group) : m - 1;
+        const uint32_t first = (uint32_t)j * ROWS, group = (uint32_t)a.group;  // rows are counted in 31 bits
+        const int i0 = (int)(first / group), to = (int)((first + ROWS - 1) / group), i1 = to < m ? to : m - 1;
         Span s;
         const int64_t past = (int64_t)n - m;  // may be negative: new tokens that have no place see nothing
         const int64_t hi = a.tree ? n : past + i1 + 1;
@@ -64,7 +65,59 @@ struct Blocks {
     static __device__ __forceinline__ int cost(const TokensArgs& a, int m, int n, int j) { return span(a, m, n, j).count + kHeadTiles; }
 };
 
+typedef short short2_t __attribute__((ext_vector_type(2)));
+
 __device__ __forceinline__ uint32_t below(int64_t x) { return x <= 0 ? 0u : (x >= 32 ? ~0u : (1u << x) - 1u); }
+
+// A value that is the same on all lanes, so that branches on it are not masked.
+__device__ __forceinline__ int same(int x) { return __builtin_amdgcn_readfirstlane(x); }
+__device__ __forceinline__ int64_t same(int64_t x) { return read_lane(x, 0); }
+
+// N pieces of 1024 bytes from a buffer straight into LDS, 16 bytes a lane. In
+// asm, so that the compiler does not wait for them at every LDS read: the ring's
+// own waits do (wait_vmcnt, then the barrier). They only make the compiler's other
+// waits stricter. s_nop: the descriptor may come from a VALU instruction (5
+// wait states to the load), M0 needs one.
+template <int N>
+__device__ __forceinline__ void load_lds(const u32x4& rsrc, uint32_t lds, uint32_t voff, uint32_t soff) {
+    static_assert(N >= 1, "pieces");
+    if constexpr (N >= 4) {
+        asm volatile(
+            "s_nop 4\n\ts_mov_b32 m0, %0\n\ts_nop 0\n\t"
+            "buffer_load_dwordx4 %1, %2, %3 offen lds\n\t"
+            "buffer_load_dwordx4 %1, %2, %3 offen offset:1024 lds\n\t"
+            "buffer_load_dwordx4 %1, %2, %3 offen offset:2048 lds\n\t"
+            "buffer_load_dwordx4 %1, %2, %3 offen offset:3072 lds" ::"s"(lds), "v"(voff), "s"(rsrc), "s"(soff)
+            : "memory");
+        if constexpr (N > 4) load_lds<N - 4>(rsrc, lds + 4096, voff, soff + 4096);
+    } else if constexpr (N >= 2) {
+        asm volatile(
+            "s_nop 4\n\ts_mov_b32 m0, %0\n\ts_nop 0\n\t"
+            "buffer_load_dwordx4 %1, %2, %3 offen lds\n\t"
+            "buffer_load_dwordx4 %1, %2, %3 offen offset:1024 lds" ::"s"(lds), "v"(voff), "s"(rsrc), "s"(soff)
+            : "memory");
+        if constexpr (N > 2) load_lds<N - 2>(rsrc, lds + 2048, voff, soff + 2048);
+    } else {
+        asm volatile("s_nop 4\n\ts_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(lds), "v"(voff),
+                     "s"(rsrc), "s"(soff)
+                     : "memory");
+    }
+}
+// 4 bytes a lane.
+__device__ __forceinline__ void load_lds_words(const u32x4& rsrc, uint32_t lds, uint32_t voff, uint32_t soff) {
+    asm volatile("s_nop 4\n\ts_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, %3 offen lds" ::"s"(lds), "v"(voff), "s"(rsrc),
+                 "s"(soff)
+                 : "memory");
+}
+
+// A workgroup's part of a block: items [from, upto) of its tiles.
+struct Item {
+    int64_t b, row;
+    int m, n, kv_head, j, from, upto;
+    int parts;  // workgroups that share the block, if it begins here and does not end here
+    int whole;  // it begins and ends here
+};
+constexpr int kItems = 24;  // found at once, in LDS
 
 template <int DT, int KIND, int D, int HT>
 struct Attend {
@@ -75,13 +128,24 @@ struct Attend {
     static constexpr int NQ = D / 32;                  // MFMAs along d
     static constexpr int NO = D / 16;
     static constexpr int kRows = 16 * HT * kWaves;
-    static constexpr int kUnits = 2 * NQ + NO;         // operands of a tile, 1024 bytes each: keys, then values
-    static constexpr int kStage = kUnits * 1024 + (kI8 ? 256 : 0);  // int8: then key scales and value scales
-    static constexpr int kStages = 2;
-    static constexpr int kLoads = (kI8 ? kUnits / 2 : kUnits) / kWaves;  // 16-byte loads a lane for a tile
+    // A tile as loaded: keys, then values, kLoads pieces of 1024 bytes a wave;
+    // int8: codes, then key scales and value scales.
+    static constexpr int kLoads = 2 * D * (kI8 ? 1 : 2) * kTile / 1024 / kWaves;
+    static constexpr int kRaw = kLoads * kWaves * 1024 + (kI8 ? 256 : 0);
+    static constexpr int kTileLoads = kLoads + (kI8 ? 1 : 0);
+    // Operands of a tile's keys, and of its values: 16 bits each. 16-bit tiles
+    // are operands as loaded; int8 ones are turned into them, in two places for
+    // keys, two for values and three for scales.
+    static constexpr int kPart = D * kTile * 2;
+    static constexpr int kOperands = kI8 ? 4 * kPart + 3 * 256 : 0;
+    // Workgroups that share a CU, and tiles in the ring that loads fill.
+    static constexpr int kPerCU = D <= 128 || (D == 192 && HT == 1 && !kI8) ? 2 : 1;
+    static constexpr int kFree = (kPerCU == 2 ? 80 : 160) * 1024 - kItems * (int)sizeof(Item) - kOperands;
+    static constexpr int kStages = kFree / kRaw < 4 ? kFree / kRaw : 4;
+    static constexpr int kBytes = kStages * kRaw + kOperands + kItems * (int)sizeof(Item);
+    static_assert(kStages >= 3, "a tile is loaded while others are worked on");
     using L = KvPlace<KIND>;
     using Pr = Prob<kF16P>;
-    static_assert((kI8 ? kUnits / 2 : kUnits) % kWaves == 0, "each wave loads as much of a tile");
 
     const TokensArgs& a;
     unsigned char* lds;
@@ -90,50 +154,50 @@ struct Attend {
     float factor[HT];
     floatx4 o[HT][NO];
     float m[HT], l[HT], c[HT], f[HT];
-    // Of each column: its row of the sequence's new tokens (-1: none), what it
-    // sees: tokens lo .. hi - 1 and 0 .. sk - 1, and tree bits from `past` on.
-    int64_t out_row[HT];
-    int head[HT];
-    bool valid[HT];
+    // Of each column: what it sees, tokens lo .. hi - 1 and 0 .. sk - 1, and tree bits from `past` on.
     int lo[HT], hi[HT];
-    int64_t past;
-    int full_lo, full_hi;  // tiles in [full_lo, full_hi) are seen whole by every column of the wave
-    u32x4 stage[kLoads];
-    float stage_scale;
+    int64_t row;   // of the block's sequence
+    int past, first, rows;  // tokens before the new ones (may be negative), the block's first row and the sequence's rows
+    int full_lo, full_hi;   // tiles in [full_lo, full_hi) are seen whole by every column of the wave
+    bool busy;     // the wave has a row
 
     __device__ __forceinline__ Attend(const TokensArgs& args, unsigned char* smem)
         : a(args), lds(smem), lane(threadIdx.x & 63), wave(__builtin_amdgcn_readfirstlane(threadIdx.x >> 6)), g(lane >> 4), col(lane & 15) {}
 
-    __device__ __forceinline__ void begin(const Sequence& s, int kv_head, int j) {
-        past = (int64_t)s.n - s.m;
+    // Row (token of the sequence's new ones, query head of the group) of column h.
+    __device__ __forceinline__ int row_at(int h) const { return first + (wave * HT + h) * 16 + col; }
+
+    __device__ __forceinline__ void begin(const Item& it) {
+        const int kv_head = it.kv_head;
+        past = it.n - it.m;
+        row = it.row;
+        first = it.j * kRows;
+        rows = it.m * a.group;
+        busy = same(first + wave * HT * 16) < same(rows);
         int least_hi = 0x7FFFFFFF, most_lo = 0;
 #pragma unroll
         for (int h = 0; h < HT; ++h) {
-            const int64_t r = (int64_t)j * kRows + (wave * HT + h) * 16 + col;
-            const int i = (int)(r / a.group);
-            valid[h] = i < s.m;
-            head[h] = kv_head * a.group + (int)(r - (int64_t)i * a.group);
-            out_row[h] = s.row + i;
+            const int r = row_at(h), i = (int)((uint32_t)r / (uint32_t)a.group), head = kv_head * a.group + r - i * a.group;
             lo[h] = 0;
             hi[h] = 0x7FFFFFFF;  // columns without a row do not count
-            if (valid[h]) {
-                int64_t at = past + i, end = at + 1;
+            if (r < rows) {
+                int at = past + i, end = at + 1;
                 if (a.tree) {
                     int depth = 0;
-                    for (int w = 0; w < a.tree_words; ++w) depth += __builtin_popcountll(a.tree[out_row[h] * a.tree_ld + w]);
+                    for (int w = 0; w < a.tree_words; ++w) depth += __builtin_popcountll(a.tree[(row + i) * a.tree_ld + w]);
                     at = past + depth - 1;
                     end = depth > 0 ? past : 0;  // past tokens; the tree's by their bits
                 }
-                hi[h] = end > 0 ? (int)end : 0;
-                lo[h] = at + 1 > a.reach ? (int)(at + 1 - a.reach) : 0;
+                hi[h] = end > 0 ? end : 0;
+                lo[h] = at >= a.reach ? (int)(at + 1 - a.reach) : 0;
             }
             least_hi = hi[h] < least_hi ? hi[h] : least_hi;
             most_lo = lo[h] > most_lo ? lo[h] : most_lo;
-            const uint16_t* p = a.q + out_row[h] * a.q_ts + (int64_t)head[h] * a.q_hs + 8 * g;
+            const uint16_t* p = a.q + (row + i) * a.q_ts + (int64_t)head * a.q_hs + 8 * g;
 #pragma unroll
             for (int x = 0; x < NQ; ++x) {
                 q[h][x] = u32x4{0u, 0u, 0u, 0u};
-                if (valid[h]) q[h][x] = *reinterpret_cast<const u32x4_any*>(p + 32 * x);
+                if (r < rows) q[h][x] = *reinterpret_cast<const u32x4_any*>(p + 32 * x);
             }
             m[h] = kLowest;
             c[h] = kLowest;
@@ -153,11 +217,19 @@ struct Attend {
         convert_query();
     }
 
-    // bf16 queries over int8: moved by a power of two to the top of fp16's range.
+    // A negative scale's sign goes into the queries, and a scale of 0 (so that a
+    // factor on an unseen score of -infinity is positive): the largest product
+    // has the largest score. bf16 queries over int8 are moved by a power of two to the
+    // top of fp16's range.
     __device__ __forceinline__ void convert_query() {
+        const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u, keep = a.scale == 0.0f ? 0u : ~0u;
 #pragma unroll
         for (int h = 0; h < HT; ++h) {
-            factor[h] = a.scale * 1.44269504088896341f;
+            factor[h] = a.scale == 0.0f ? 1.0f : __builtin_fabsf(a.scale) * 1.44269504088896341f;
+#pragma unroll
+            for (int i = 0; i < NQ; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) q[h][i][e] = (q[h][i][e] ^ flip) & keep;
             if constexpr (kI8 && DT == 1) {
                 uint32_t top = 0u;
 #pragma unroll
@@ -188,133 +260,155 @@ struct Attend {
         }
     }
 
-    // This wave's part of a tile, to registers and from there to a stage in LDS.
-    __device__ __forceinline__ void fetch_tile(const unsigned char* rec, int sub) {
-        constexpr int kKeyLoads = (kI8 ? NQ : 2 * NQ);
+    // This wave's part of a tile on its way to a place of the ring: half the waves load keys, half values.
+    __device__ __forceinline__ void request(const unsigned char* rec, int sub, int place) {
+        constexpr uint32_t kKeys = kLoads * kWaves / 2 * 1024;  // bytes of a tile's keys, and of its values
+        const uint64_t at = reinterpret_cast<uint64_t>(rec);
+        const u32x4 rsrc{(uint32_t)at, (uint32_t)(at >> 32) & 0xFFFFu, (uint32_t)L::record_bytes(D, a.P), 0x00020000u};
+        const uint32_t to = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(__attribute__((address_space(3))) unsigned char*)lds + place * kRaw);
+        const uint32_t part = (uint32_t)(wave % (kWaves / 2)) * kLoads * 1024;
+        const uint32_t from = (wave < kWaves / 2 ? 0u : (uint32_t)L::keys_bytes(D, a.P)) + (uint32_t)sub * kKeys + part;
+        load_lds<kLoads>(rsrc, to + wave * kLoads * 1024, lane * 16, from);
+        // Every wave loads the scales, the same ones: as many loads a wave.
+        if constexpr (kI8)
+            load_lds_words(rsrc, to + kLoads * kWaves * 1024, (lane & 31) * 4 + (lane < 32 ? 0 : a.P * 4),
+                           (uint32_t)(2 * L::keys_bytes(D, a.P)) + sub * kTile * 4);
+    }
+    // Where a tile's operands and scales are: 16 bits, in the ring; int8, tile i's in place i % 2, scales in i % 3.
+    __device__ __forceinline__ const unsigned char* keys_at(int place, int i) const { return lds + (kI8 ? kStages * kRaw + (i & 1) * kPart : place * kRaw); }
+    __device__ __forceinline__ const unsigned char* values_at(int place, int i) const {
+        return lds + (kI8 ? kStages * kRaw + (2 + (i & 1)) * kPart : place * kRaw + kPart);
+    }
+    __device__ __forceinline__ const float* scales_at(int third) const {
+        return reinterpret_cast<const float*>(lds + kStages * kRaw + 4 * kPart + third * 256);
+    }
+    // int8: this wave's part of tile i as operands; half the waves turn keys, half values.
+    __device__ __forceinline__ void convert(int place, int i) {
+        const u32x4* from = reinterpret_cast<const u32x4*>(lds + place * kRaw) + wave * kLoads * 64 + lane;
+        const unsigned char* part = wave < kWaves / 2 ? keys_at(place, i) : values_at(place, i);
+        u32x4* to = reinterpret_cast<u32x4*>(const_cast<unsigned char*>(part)) + wave % (kWaves / 2) * kLoads * 128 + lane;
 #pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
-            const int unit = wave * kLoads + i;
-            const unsigned char* p = unit < kKeyLoads ? rec + (int64_t)sub * kKeyLoads * 1024 + unit * 1024
-                                                      : rec + L::keys_bytes(D, a.P) + (int64_t)sub * kKeyLoads * 1024 + (unit - kKeyLoads) * 1024;
-            stage[i] = *(reinterpret_cast<const u32x4*>(p) + lane);
-        }
-        if constexpr (kI8) {
-            if (wave == 0) stage_scale = reinterpret_cast<const float*>(rec + 2 * L::keys_bytes(D, a.P))[sub * kTile + (lane & 31) + (lane < 32 ? 0 : a.P)];
+        for (int x = 0; x < kLoads; ++x) {
+            const u32x4 v = from[64 * x];
+            to[128 * x] = codes8_to_f16(v[0], v[1]);
+            to[128 * x + 64] = codes8_to_f16(v[2], v[3]);
         }
     }
-    __device__ __forceinline__ void store_tile(int which) {
-        u32x4* to = reinterpret_cast<u32x4*>(lds + which * kStage);
-#pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
-            const int unit = wave * kLoads + i;
-            if constexpr (kI8) {
-                to[(2 * unit) * 64 + lane] = codes8_to_f16(stage[i][0], stage[i][1]);
-                to[(2 * unit + 1) * 64 + lane] = codes8_to_f16(stage[i][2], stage[i][3]);
-            } else {
-                to[unit * 64 + lane] = stage[i];
-            }
-        }
-        if constexpr (kI8) {
-            if (wave == 0) reinterpret_cast<float*>(lds + which * kStage + kUnits * 1024)[lane] = stage_scale;
-        }
+    __device__ __forceinline__ void copy_scales(int place, int third) {
+        if (wave == 0) const_cast<float*>(scales_at(third))[lane] = reinterpret_cast<const float*>(lds + place * kRaw + kLoads * kWaves * 1024)[lane];
     }
 
     // Which of the tile's 32 tokens column h sees.
     __device__ __forceinline__ uint32_t visible(int h, int at, int n) const {
-        const int64_t t = at;
-        uint32_t seen = below(hi[h] - t) & (~below(lo[h] - t) | below((a.sinks < lo[h] ? a.sinks : lo[h]) - t));
-        if (a.tree && valid[h] && at + kTile > past) {
-            const int64_t first = t - past;  // the bit of the tile's first token
-            const uint64_t* words = a.tree + out_row[h] * a.tree_ld;
+        uint32_t seen = below(hi[h] - at) & (~below(lo[h] - at) | below((a.sinks < lo[h] ? a.sinks : lo[h]) - at));
+        const int r = row_at(h);
+        if (a.tree && r < rows && at + kTile > past) {
+            const int64_t bit = (int64_t)at - past;  // of the tile's first token
+            const uint64_t* words = a.tree + (row + (int)((uint32_t)r / (uint32_t)a.group)) * a.tree_ld;
             uint32_t bits = 0u;
-            if (first < 0) {
-                bits = (uint32_t)(words[0] << -first);
-            } else if (first < 64 * (int64_t)a.tree_words) {
-                const int w = (int)(first >> 6), by = (int)(first & 63);
+            if (bit < 0) {
+                bits = (uint32_t)(words[0] << -bit);
+            } else if (bit < 64 * (int64_t)a.tree_words) {
+                const int w = (int)(bit >> 6), by = (int)(bit & 63);
                 uint64_t v = words[w] >> by;
                 if (by > 32 && w + 1 < a.tree_words) v |= words[w + 1] << (64 - by);
                 bits = (uint32_t)v;
             }
-            seen |= bits & below(n - t);
+            seen |= bits & below(n - at);
         }
         return seen;
     }
 
-    __device__ __forceinline__ void work(int which, int at, int n) {
-        const u32x4* tile = reinterpret_cast<const u32x4*>(lds + which * kStage);
-        // s[h][0..3]: tokens 4g .. 4g+3 of the tile, s[h][4..7]: 16 tokens on.
-        floatx4 acc[HT][2];
+    // s[h][0][..]: tokens 4g .. 4g+3 of a tile, s[h][1][..]: 16 tokens on.
+    __device__ __forceinline__ void products(const unsigned char* keys, floatx4 (&s)[HT][2]) const {
+        const u32x4* tile = reinterpret_cast<const u32x4*>(keys) + lane;
 #pragma unroll
         for (int h = 0; h < HT; ++h)
 #pragma unroll
-            for (int t = 0; t < 2; ++t) acc[h][t] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+            for (int t = 0; t < 2; ++t) s[h][t] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int i = 0; i < NQ; ++i)
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
-                const u32x4 k = tile[(t * NQ + i) * 64 + lane];
+                const u32x4 k = tile[(t * NQ + i) * 64];
 #pragma unroll
-                for (int h = 0; h < HT; ++h) acc[h][t] = mfma16x16x32<PDT>(k, q[h][i], acc[h][t]);
+                for (int h = 0; h < HT; ++h) s[h][t] = mfma16x16x32<PDT>(k, q[h][i], s[h][t]);
             }
-        floatx4 ks[2], vs[2];
+    }
+
+    // All bits of the halves of a word that hold finite numbers.
+    static __device__ __forceinline__ uint32_t finite(uint32_t pair) {
+        constexpr uint32_t kInf = DT == 0 ? 0x7C007C00u : 0x7F807F80u;
+        const short2_t x = __builtin_bit_cast(short2_t, pair & kInf) - __builtin_bit_cast(short2_t, kInf);
+        return __builtin_bit_cast(uint32_t, x >> 15);
+    }
+
+    // A tile of tokens from `at` on, whose products with the queries s holds;
+    // whole: every column sees all of them. The next tile's products are made on
+    // the way, so that the matrix cores have work while the probabilities are formed.
+    __device__ __forceinline__ void work(floatx4 (&s)[HT][2], const unsigned char* next_keys, const unsigned char* operands,
+                                         const float* scales, int at, int n, bool whole) {
+        const u32x4* values = reinterpret_cast<const u32x4*>(operands) + lane;
+        floatx4 vs[2];
         if constexpr (kI8) {
-            const float* sc = reinterpret_cast<const float*>(tile + kUnits * 64) + 4 * g;
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
-                ks[t] = *reinterpret_cast<const floatx4*>(sc + 16 * t);
-                vs[t] = *reinterpret_cast<const floatx4*>(sc + 32 + 16 * t);
+                const floatx4 ks = *reinterpret_cast<const floatx4*>(scales + 4 * g + 16 * t);
+                vs[t] = *reinterpret_cast<const floatx4*>(scales + 32 + 4 * g + 16 * t);
+#pragma unroll
+                for (int h = 0; h < HT; ++h)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) s[h][t][r] *= ks[r];
             }
         }
-        const bool partial = !(at + kTile <= full_hi && (at >= full_lo || at + kTile <= a.sinks));
-        float s[HT][8];
         uint32_t seen[HT];
-        float peak[HT];
-        bool above = false;
+        int bad = 0;  // 16 bits: whether the tile holds values that are not finite and some column may not see
+        if (same((int)whole) == 0) {
+            // Unseen scores are -infinity. An unseen value may be anything, and
+            // 0 * NaN is NaN: an int8 value's scale that is not finite gives way
+            // to a score of NaN in the columns that see it.
 #pragma unroll
-        for (int h = 0; h < HT; ++h) {
-            seen[h] = 0xFFu;
-            if (partial) {
+            for (int h = 0; h < HT; ++h) {
                 const uint32_t bits = visible(h, at, n);
                 seen[h] = (bits >> (4 * g) & 0xFu) | (bits >> (16 + 4 * g) & 0xFu) << 4;
-            }
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                s[h][j] = acc[h][j / 4][j % 4] * (kI8 ? ks[j / 4][j % 4] * factor[h] : factor[h]);
-                if (partial && !(seen[h] >> j & 1u)) s[h][j] = -INFINITY;
-            }
-            peak[h] = s[h][0];
-#pragma unroll
-            for (int j = 1; j < 8; ++j) peak[h] = fmaxf(peak[h], s[h][j]);
-            above |= peak[h] > m[h] + Pr::kHeadroom;
-        }
-        float e[HT][8], w[HT][8];
-        auto weigh = [&]() {
-#pragma unroll
-            for (int h = 0; h < HT; ++h) {
-                const float ref = kI8 ? m[h] : m[h] - Pr::kBias;
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    e[h][j] = exp2_fast(s[h][j] - ref);
-                    if constexpr (kI8) {
-                        w[h][j] = e[h][j] * vs[j / 4][j % 4] * f[h];
-                        if (partial && !(seen[h] >> j & 1u)) w[h][j] = 0.0f;  // an unseen scale may be anything
-                    } else {
-                        w[h][j] = e[h][j];
-                    }
+                    const uint32_t mask = (uint32_t)((int32_t)(seen[h] << (31 - j)) >> 31);
+                    float x = s[h][j / 4][j % 4];
+                    if constexpr (kI8) x = __builtin_fabsf(vs[j / 4][j % 4]) < INFINITY ? x : NAN;
+                    s[h][j / 4][j % 4] = __builtin_bit_cast(float, (__builtin_bit_cast(uint32_t, x) & mask) | (0xFF800000u & ~mask));
                 }
             }
-        };
-        if constexpr (kI8) {
-            weigh();
+            if constexpr (kI8) {
 #pragma unroll
-            for (int h = 0; h < HT; ++h) {
-                float top = w[h][0];
+                for (int j = 0; j < 8; ++j) vs[j / 4][j % 4] = __builtin_fabsf(vs[j / 4][j % 4]) < INFINITY ? vs[j / 4][j % 4] : 0.0f;
+            } else {
+                uint32_t all = ~0u;
 #pragma unroll
-                for (int j = 1; j < 8; ++j) top = fmaxf(top, w[h][j]);
-                above |= top > 0x1p15f;
+                for (int i = 0; i < NO; ++i) {
+                    const u32x4 v = values[64 * i];
+                    all &= finite(v[0]) & finite(v[1]) & finite(v[2]) & finite(v[3]);
+                }
+                bad = __builtin_amdgcn_ballot_w64(all != ~0u) != 0;
             }
         }
-        if (__builtin_amdgcn_ballot_w64(above) != 0) {  // move the references: rare after the first tiles
+        float peak[HT];
+        bool above = false;
+        float most_vs = 0.0f;
+        if constexpr (kI8) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) most_vs = fmaxf(most_vs, vs[j / 4][j % 4]);
+        }
+#pragma unroll
+        for (int h = 0; h < HT; ++h) {
+            peak[h] = s[h][0][0];
+#pragma unroll
+            for (int j = 1; j < 8; ++j) peak[h] = fmaxf(peak[h], s[h][j / 4][j % 4]);
+            peak[h] *= factor[h];
+            above |= peak[h] > m[h] + Pr::kHeadroom;
+            if constexpr (kI8) above |= exp2_fast(peak[h] - m[h]) * (most_vs * f[h]) > 0x1p15f;  // no w is larger
+        }
+        if (same((int)(__builtin_amdgcn_ballot_w64(above) != 0)) != 0) {  // move the references: rare after the first tiles
 #pragma unroll
             for (int h = 0; h < HT; ++h) {
                 const float mn = column_max(fmaxf(m[h], peak[h]));
@@ -323,10 +417,8 @@ struct Attend {
                 if constexpr (kI8) {
                     float y = 0.0f;
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const float z = exp2_fast(s[h][j] - mn) * vs[j / 4][j % 4];
-                        y = fmaxf(y, partial && !(seen[h] >> j & 1u) ? 0.0f : z);
-                    }
+                    for (int j = 0; j < 8; ++j)
+                        y = fmaxf(y, exp2_fast(__builtin_fmaf(s[h][j / 4][j % 4], factor[h], -mn)) * vs[j / 4][j % 4]);
                     // f stays within fp32: c is at least mn - 113
                     const float cn = fmaxf(fmaxf(c[h], mn + __builtin_amdgcn_logf(column_max(y))), mn - 113.0f);
                     keep_o = exp2_fast(c[h] - cn);
@@ -340,64 +432,62 @@ struct Attend {
 #pragma unroll
                     for (int r = 0; r < 4; ++r) o[h][i][r] *= keep_o;
             }
-            if constexpr (kI8) weigh();
         }
-        if constexpr (!kI8) weigh();
+        floatx4 ahead[HT][2];
+        products(next_keys, ahead);
         u32x4 p[HT][NP];
 #pragma unroll
         for (int h = 0; h < HT; ++h) {
+            const float ref = kI8 ? m[h] : m[h] - Pr::kBias;
+            float w[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) l[h] += e[h][j];
+            for (int j = 0; j < 8; ++j) {
+                w[j] = exp2_fast(__builtin_fmaf(s[h][j / 4][j % 4], factor[h], -ref));
+                l[h] += w[j];
+                if constexpr (kI8) w[j] *= vs[j / 4][j % 4] * f[h];
+            }
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
                 uint32_t parts[NP];
-                split_pair<PDT, NP>(w[h][2 * x], w[h][2 * x + 1], parts);
+                split_pair<PDT, NP>(w[2 * x], w[2 * x + 1], parts);
 #pragma unroll
                 for (int i = 0; i < NP; ++i) p[h][i][x] = parts[i];
             }
         }
-        const u32x4* values = tile + 2 * NQ * 64 + lane;
-        if (!kI8 && partial) {
-            // 0 * NaN is NaN: values that are not finite are taken out of the
-            // product, and the columns that see one become NaN in its place.
-            constexpr uint32_t kInf = DT == 0 ? 0x7C00u : 0x7F80u, kOne = DT == 0 ? 0x3C00u : 0x3F80u;
-            bool bad = false;
+#pragma unroll
+        for (int h = 0; h < HT; ++h)
+#pragma unroll
+            for (int t = 0; t < 2; ++t) s[h][t] = ahead[h][t];
+        constexpr uint32_t kOne = DT == 0 ? 0x3C003C00u : 0x3F803F80u;
+        bad = same(bad);
+        if (!kI8 && bad) {
+            // The columns that see a value that is not finite become NaN there, and stay so.
+            u32x4 ones[HT];
+#pragma unroll
+            for (int h = 0; h < HT; ++h)
+#pragma unroll
+                for (int x = 0; x < 4; ++x) ones[h][x] = ((seen[h] >> (2 * x) & 1u) | (seen[h] >> (2 * x + 1) & 1u) << 16) * (kOne & 0xFFFFu);
 #pragma unroll
             for (int i = 0; i < NO; ++i) {
-                const u32x4 v = values[64 * i];
+                __builtin_amdgcn_sched_barrier(0);  // one after the other: this is rare, and its registers are everybody's
+                u32x4 is = values[64 * i];
 #pragma unroll
-                for (int x = 0; x < 4; ++x) bad |= (v[x] & kInf) == kInf || (v[x] >> 16 & kInf) == kInf;
-            }
-            if (__builtin_amdgcn_ballot_w64(bad) != 0) {
-                u32x4 sees[HT];
+                for (int x = 0; x < 4; ++x) is[x] = ~finite(is[x]) & kOne;
 #pragma unroll
-                for (int h = 0; h < HT; ++h)
+                for (int h = 0; h < HT; ++h) {
+                    const floatx4 hits = mfma16x16x32<PDT>(is, ones[h], floatx4{0.0f, 0.0f, 0.0f, 0.0f});
 #pragma unroll
-                    for (int x = 0; x < 4; ++x)
-                        sees[h][x] = (seen[h] >> (2 * x) & 1u ? kOne : 0u) | (seen[h] >> (2 * x + 1) & 1u ? kOne << 16 : 0u);
-#pragma unroll
-                for (int i = 0; i < NO; ++i) {
-                    u32x4 v = values[64 * i], is{0u, 0u, 0u, 0u};
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        if ((v[x] & kInf) == kInf) v[x] &= 0xFFFF0000u, is[x] |= kOne;
-                        if ((v[x] >> 16 & kInf) == kInf) v[x] &= 0x0000FFFFu, is[x] |= kOne << 16;
-                    }
-#pragma unroll
-                    for (int h = 0; h < HT; ++h) {
-                        const floatx4 hits = mfma16x16x32<PDT>(is, sees[h], floatx4{0.0f, 0.0f, 0.0f, 0.0f});
-#pragma unroll
-                        for (int j = 0; j < NP; ++j) o[h][i] = mfma16x16x32<PDT>(v, p[h][j], o[h][i]);
-#pragma unroll
-                        for (int r = 0; r < 4; ++r) o[h][i][r] = hits[r] > 0.0f ? NAN : o[h][i][r];
-                    }
+                    for (int r = 0; r < 4; ++r) o[h][i][r] = hits[r] > 0.0f ? NAN : o[h][i][r];
                 }
-                return;
             }
         }
 #pragma unroll
         for (int i = 0; i < NO; ++i) {
-            const u32x4 v = values[64 * i];
+            u32x4 v = values[64 * i];
+            if (!kI8 && bad) {  // they are taken out of the product
+#pragma unroll
+                for (int x = 0; x < 4; ++x) v[x] &= finite(v[x]);
+            }
 #pragma unroll
             for (int j = 0; j < NP; ++j)
 #pragma unroll
@@ -411,49 +501,120 @@ struct Attend {
         const int whole_shift = (tiles_per_page & (tiles_per_page - 1)) == 0 ? __builtin_ctz(tiles_per_page) : -1;
         int block = from;  // first item of the 64 in hand
         uint64_t todo = 0;
-        int64_t place = 0;
+        int64_t place_l = 0;
         int sub_l = 0;
-        const unsigned char* rec = nullptr;
-        int sub = 0, tile = 0;
-        auto next = [&]() -> bool {  // the next tile's place, if there is one
+        // The ring: tile i of those that are there lies in place i % kStages. Their
+        // first tokens, the next one's lowest (an array would lie in scratch memory,
+        // and a load from there wait for the ring's).
+        static_assert(kStages <= 4, "first tokens are kept for four tiles");
+        uint64_t first_lo = 0, first_hi = 0;
+        int there = 0, done = 0;  // tiles requested and worked on
+        int fill = 0, take = 0;   // their places
+        auto more = [&]() -> bool {  // requests the next tile, if there is one
             while (todo == 0 && block < to) {
                 const int item = block + lane, tile_l = sp.tile(item);
                 int64_t page = -1;
                 if (item < to) {
-                    const int at = whole_shift >= 0 ? tile_l >> whole_shift : tile_l / tiles_per_page;
-                    page = a.table[b * a.table_ld + at];
-                    sub_l = tile_l - at * tiles_per_page;
+                    const int i = whole_shift >= 0 ? tile_l >> whole_shift : tile_l / tiles_per_page;
+                    page = a.table[b * a.table_ld + i];
+                    sub_l = tile_l - i * tiles_per_page;
                 }
                 const bool ok = page >= 0 && page < a.pages;
-                place = ok ? (page * a.H + kv_head) * L::record_bytes(D, a.P) : 0;
+                place_l = ok ? (page * a.H + kv_head) * L::record_bytes(D, a.P) : 0;
                 todo = __builtin_amdgcn_ballot_w64(ok);
                 if (todo == 0) block += 64;
             }
             if (todo == 0) return false;
             const int i = __builtin_ctzll(todo);
             todo &= todo - 1;
-            rec = a.cache + read_lane(place, i);
-            sub = __builtin_amdgcn_readlane(sub_l, i);
-            tile = sp.tile(block + i);
+            request(a.cache + read_lane(place_l, i), __builtin_amdgcn_readlane(sub_l, i), fill);
+            const uint64_t first_token = (uint32_t)(sp.tile(block + i) * kTile);
+            const int behind = there - done;
+            if (behind < 2) first_lo |= first_token << (32 * behind);
+            else first_hi |= first_token << (32 * behind - 64);
             if (todo == 0) block += 64;
+            fill = fill + 1 < kStages ? fill + 1 : 0;
+            ++there;
             return true;
         };
-        if (!next()) return;
-        __syncthreads();  // the stages are free
-        fetch_tile(rec, sub);
-        store_tile(0);
-        int at = tile * kTile, which = 0;
-        bool more = next();
-        __syncthreads();
-        while (true) {
-            if (more) fetch_tile(rec, sub);
-            work(which, at, n);
-            if (!more) break;
-            store_tile(which ^ 1);
-            at = tile * kTile;
-            which ^= 1;
-            more = next();
-            __syncthreads();
+        stage_barrier();  // the ring is free
+        bool going = true;
+        // Tile i is worked on when its values and tile i + 1's keys are there.
+        // 16 bits: tiles up to i + kStages - 2 are on their way, and when all waves
+        // have begun tile i, tile i - 1's place takes tile i + kStages - 1. int8: up to
+        // i + kStages - 1; keys become operands two tiles ahead, values one, and the place
+        // that takes tile i + kStages is tile i's own.
+        constexpr int kAhead = kI8 ? kStages : kStages - 1;
+        while (going && there < kAhead) going = more();
+        if (there == 0) return;
+        floatx4 s[HT][2];
+        int third = 0;  // int8: the scales' place
+        auto place_of = [&](int i) { return i < kStages ? i : i - kStages; };  // take + i
+        auto wait_for = [&](int younger) {  // until at most that many tiles are on their way
+            if (younger >= 2) wait_vmcnt<2 * kTileLoads>();
+            else if (younger == 1) wait_vmcnt<kTileLoads>();
+            else wait_vmcnt<0>();
+        };
+        if constexpr (kI8) {
+            wait_for(there - 2 < 0 ? 0 : there - 2);
+            stage_barrier();
+            convert(0, 0);
+            copy_scales(0, 0);
+            if (there > 1) {
+                if (wave < kWaves / 2) convert(1, 1);
+                copy_scales(1, 1);
+            }
+            stage_barrier();
+        } else {
+            wait_for(there - 1);
+            stage_barrier();
+        }
+        if (busy) products(keys_at(0, 0), s);
+        // The next tile to work on: its first token, its place and the next one's.
+        int t = 0, place = 0, next = 0, third_at = 0;
+        auto advance = [&]() -> bool {
+            if (done == there) return false;
+            t = same((int)first_lo);
+            first_lo = first_lo >> 32 | first_hi << 32;
+            first_hi >>= 32;
+            place = take;
+            next = place_of(take + 1);
+            third_at = third;
+            if constexpr (kI8) {
+                const int left = there - done;  // this one, the ones that are there and the ones on their way
+                wait_for(left - 3 < 0 ? 0 : left - 3);
+                stage_barrier();
+                ++done;
+                if (going) going = more();
+                --done;
+                // Into places that were read for tile done - 1, or before.
+                if (wave < kWaves / 2) {
+                    if (left > 2) convert(place_of(take + 2), done + 2);
+                } else {
+                    if (left > 1) convert(next, done + 1);
+                }
+                if (left > 2) copy_scales(place_of(take + 2), third >= 1 ? third - 1 : 2);
+                third = third < 2 ? third + 1 : 0;
+            } else {
+                wait_for(there - done - 2 < 0 ? 0 : there - done - 2);
+                stage_barrier();
+                ++done;
+                if (going) going = more();
+                --done;
+            }
+            take = next;
+            ++done;
+            return true;
+        };
+        auto whole = [&]() { return t + kTile <= full_hi && (t >= full_lo || t + kTile <= a.sinks); };
+        bool have = advance();
+        if (!busy) {
+            while (have) have = advance();
+            return;
+        }
+        while (have) {
+            work(s, keys_at(next, done), values_at(place, done - 1), scales_at(third_at), t, n, whole());
+            have = advance();
         }
     }
 
@@ -471,12 +632,13 @@ struct Attend {
             }
         }
     }
-    __device__ __forceinline__ void store_out() {
+    __device__ __forceinline__ void store_out(int kv_head) {
 #pragma unroll
         for (int h = 0; h < HT; ++h) {
-            if (!valid[h]) continue;
+            const int r = row_at(h), t = (int)((uint32_t)r / (uint32_t)a.group);
+            if (r >= rows) continue;
             const float inv = 1.0f / (l[h] == 0.0f ? 1.0f : l[h]);
-            uint16_t* out = a.out + out_row[h] * a.o_ts + (int64_t)head[h] * a.o_hs + 4 * g;
+            uint16_t* out = a.out + (row + t) * a.o_ts + (int64_t)(kv_head * a.group + r - t * a.group) * a.o_hs + 4 * g;
 #pragma unroll
             for (int i = 0; i < NO; ++i) {
                 u32x2 v;
@@ -492,7 +654,7 @@ struct Attend {
     __device__ __forceinline__ void store_partial(float* to) {
 #pragma unroll
         for (int h = 0; h < HT; ++h) {
-            if (!valid[h]) continue;
+            if (row_at(h) >= rows) continue;
             float* p = to + ((wave * HT + h) * 16 + col) * kStride;
             if (g == 0) p[0] = m[h], p[1] = l[h];
 #pragma unroll
@@ -501,118 +663,136 @@ struct Attend {
     }
 };
 
-// A block that several workgroups share: begun by one, ended by `last`.
+// A block that a workgroup begins and `parts` - 1 next ones go on with (parts 0: none).
 struct Record {
     int64_t b;
-    int kv_head, j, last, parts;
+    int kv_head, j, parts;
 };
 
+// The cost of all blocks of one kv head of the sequences base + lane, and these.
+template <class Bl>
+__device__ __forceinline__ int64_t costs(const TokensArgs& a, int64_t base, int lane, Sequence& seq) {
+    seq = base + lane < a.B ? Sequence(a, base + lane) : Sequence();
+    const int blocks = Bl::count(a, seq.m);
+    int64_t sum = 0;
+    for (int j = 0; j < (blocks < 2 ? blocks : 2); ++j) sum += Bl::cost(a, seq.m, seq.n, j);
+    for (uint64_t todo = __builtin_amdgcn_ballot_w64(blocks > 2); todo != 0; todo &= todo - 1) {
+        const int i = __builtin_ctzll(todo);
+        const int m = __builtin_amdgcn_readlane(seq.m, i), n = __builtin_amdgcn_readlane(seq.n, i);
+        const int all = Bl::count(a, m);
+        int64_t part = 0;
+        for (int j = 2 + lane; j < all; j += 64) part += Bl::cost(a, m, n, j);
+        part = read_lane(wave_scan(part), 63);
+        if (lane == i) sum += part;
+    }
+    return sum;
+}
+
+// The items of positions [pos, end) of the list of all blocks' tiles (sequence,
+// kv head, block; a block's first kHeadTiles positions are its start), at most
+// kItems of them; returns the position behind the last. `per`: positions of a workgroup.
+template <class Bl>
+__device__ __forceinline__ int64_t find_items(const TokensArgs& a, int lane, int64_t pos, int64_t end, int64_t per, int wg, Item* items, int& found) {
+    found = 0;
+    int64_t before = 0;
+    for (int64_t base = 0; base < a.B && pos < end && found < kItems; base += 64) {
+        Sequence seq;
+        const int64_t unit = costs<Bl>(a, base, lane, seq), unit_to = wave_scan(unit);
+        for (uint64_t rest = __builtin_amdgcn_ballot_w64(unit > 0 && before + a.H * unit_to > pos); rest != 0 && pos < end && found < kItems;
+             rest &= rest - 1) {
+            const int at = __builtin_ctzll(rest);
+            Item it;
+            it.b = base + at;
+            it.row = read_lane(seq.row, at);
+            it.m = __builtin_amdgcn_readlane(seq.m, at);
+            it.n = __builtin_amdgcn_readlane(seq.n, at);
+            const int64_t of_unit = read_lane(unit, at), seq_end = before + a.H * read_lane(unit_to, at);
+            const int64_t seq_begin = seq_end - a.H * of_unit;
+            const int blocks = Bl::count(a, it.m);
+            while (pos < end && pos < seq_end && found < kItems) {
+                it.kv_head = (int)((pos - seq_begin) / of_unit);
+                int64_t begin = seq_begin + it.kv_head * of_unit;  // of the kv head, then of block j
+                int j = 0;
+                for (; j < blocks; j += 64) {  // the block that holds pos
+                    const int64_t cost = j + lane < blocks ? Bl::cost(a, it.m, it.n, j + lane) : 0, to = wave_scan(cost);
+                    const uint64_t hit = __builtin_amdgcn_ballot_w64(begin + to > pos);
+                    if (hit != 0) {
+                        const int i = __builtin_ctzll(hit);
+                        j += i;
+                        begin += read_lane(to - cost, i);
+                        break;
+                    }
+                    begin += read_lane(to, 63);
+                }
+                for (; pos < end && j < blocks && found < kItems; ++j) {
+                    const int count = Bl::span(a, it.m, it.n, j).count;
+                    const int64_t stop_at = begin + count + kHeadTiles, stop = stop_at < end ? stop_at : end;
+                    it.j = j;
+                    it.from = (int)(pos - begin) - kHeadTiles;
+                    it.from = it.from > 0 ? it.from : 0;
+                    it.upto = (int)(stop - begin) - kHeadTiles;
+                    it.whole = it.from == 0 && stop == stop_at;
+                    it.parts = it.from == 0 && stop != stop_at ? (int)((stop_at - 1) / per) - wg + 1 : 0;
+                    if (it.upto > 0 || stop == stop_at) {  // else its tiles begin in the next workgroup
+                        if (threadIdx.x == 0) items[found] = it;
+                        ++found;
+                    }
+                    pos = stop;
+                    begin = stop_at;
+                }
+            }
+        }
+        before += a.H * read_lane(unit_to, 63);
+    }
+    return pos;
+}
+
 template <int DT, int KIND, int D, int HT>
-__global__ __launch_bounds__(256, 2) void attention_tokens_kernel(TokensArgs a) {
+__global__ __launch_bounds__(256, (Attend<DT, KIND, D, HT>::kPerCU)) void attention_tokens_kernel(TokensArgs a) {
     using A = Attend<DT, KIND, D, HT>;
     using Bl = Blocks<A::kRows>;
     extern __shared__ __align__(16) unsigned char smem[];
+    Item* items = reinterpret_cast<Item*>(smem + A::kBytes) - kItems;
     const int lane = threadIdx.x & 63;
     const int wgs = gridDim.x;
     // Workgroups are dealt to the 8 dies in turn: neighbours in the list of
     // blocks, which read the same keys, are put on the same one.
     const int wg = wgs % 8 == 0 ? blockIdx.x % 8 * (wgs / 8) + blockIdx.x / 8 : blockIdx.x;
-    Record record{0, 0, 0, 0, 0};
 
-    // Cost of all blocks of one kv head, of the sequences base + lane.
-    Sequence seq;
-    auto costs = [&](int64_t base) -> int64_t {
-        seq = base + lane < a.B ? Sequence(a, base + lane) : Sequence();
-        const int blocks = Bl::count(a, seq.m);
-        int64_t sum = 0;
-        for (int j = 0; j < (blocks < 4 ? blocks : 4); ++j) sum += Bl::cost(a, seq.m, seq.n, j);
-        uint64_t todo = __builtin_amdgcn_ballot_w64(blocks > 4);
-        while (todo != 0) {
-            const int i = __builtin_ctzll(todo);
-            todo &= todo - 1;
-            const int m = __builtin_amdgcn_readlane(seq.m, i), n = __builtin_amdgcn_readlane(seq.n, i);
-            const int all = Bl::count(a, m);
-            int64_t part = 0;
-            for (int j = 4 + lane; j < all; j += 64) part += Bl::cost(a, m, n, j);
-            part = read_lane(wave_scan(part), 63);
-            if (lane == i) sum += part;
-        }
-        return sum;
-    };
-    int64_t unit = 0, unit_to = 0, all = 0, before = 0;
+    int64_t all = 0;
     for (int64_t base = 0; base < a.B; base += 64) {
-        unit = costs(base);
-        unit_to = wave_scan(unit);
-        all += read_lane(unit_to, 63);
+        Sequence seq;
+        all += read_lane(wave_scan(costs<Bl>(a, base, lane, seq)), 63);
     }
     all *= a.H;
     int64_t per = (all + wgs - 1) / wgs;
     if (per < kLeastTiles + kHeadTiles) per = kLeastTiles + kHeadTiles;
     int64_t pos = wg * per;
     const int64_t end = pos + per < all ? pos + per : all;
+    Record record{0, 0, 0, 0};
 
     A w(a, smem);
-    int64_t base = a.B > 64 ? -64 : 0;
-    uint64_t rest = 0;  // sequences of the 64 in hand that hold pos or come behind it
-    if (a.B <= 64) rest = __builtin_amdgcn_ballot_w64(unit > 0 && a.H * unit_to > pos);
     while (pos < end) {
-        while (rest == 0 && base < a.B) {
-            if (base >= 0) before += a.H * read_lane(unit_to, 63);
-            base += 64;
-            unit = costs(base);
-            unit_to = wave_scan(unit);
-            rest = __builtin_amdgcn_ballot_w64(unit > 0 && before + a.H * unit_to > pos);
-        }
-        if (rest == 0) break;
-        const int at = __builtin_ctzll(rest);
-        rest &= rest - 1;
-        const int64_t b = base + at;
-        const int64_t of_unit = read_lane(unit, at), seq_end = before + a.H * read_lane(unit_to, at), seq_begin = seq_end - a.H * of_unit;
-        Sequence s;
-        s.row = read_lane(seq.row, at);
-        s.m = __builtin_amdgcn_readlane(seq.m, at);
-        s.n = __builtin_amdgcn_readlane(seq.n, at);
-        const int blocks = Bl::count(a, s.m);
-        while (pos < end && pos < seq_end) {
-            const int kv_head = (int)((pos - seq_begin) / of_unit);
-            int64_t begin = seq_begin + kv_head * of_unit;  // of the kv head, then of block j
-            int j = 0;
-            for (; j < blocks; j += 64) {  // the block that holds pos
-                const int64_t cost = j + lane < blocks ? Bl::cost(a, s.m, s.n, j + lane) : 0;
-                const int64_t to = wave_scan(cost);
-                const uint64_t hit = __builtin_amdgcn_ballot_w64(begin + to > pos);
-                if (hit != 0) {
-                    const int i = __builtin_ctzll(hit);
-                    j += i;
-                    begin += read_lane(to - cost, i);
-                    break;
-                }
-                begin += read_lane(to, 63);
-            }
-            for (; pos < end && j < blocks; ++j) {
-                const Span sp = Bl::span(a, s.m, s.n, j);
-                const int64_t stop_at = begin + sp.count + kHeadTiles;
-                const int64_t stop = stop_at < end ? stop_at : end;
-                int from = (int)(pos - begin) - kHeadTiles;
-                const int upto = (int)(stop - begin) - kHeadTiles;
-                const bool ends = stop == stop_at;
-                from = from > 0 ? from : 0;
-                pos = stop;
-                if (upto > 0 || ends) {  // else its tiles begin in the next workgroup
-                    w.begin(s, kv_head, j);
-                    w.run(b, kv_head, sp, s.n, from, upto);
-                    w.finish();
-                    if (from == 0 && ends) {
-                        w.store_out();
-                    } else {
-                        w.store_partial(a.partials + (2 * (int64_t)wg + (from == 0 ? 1 : 0)) * A::kPartial);
-                        if (from == 0) {
-                            const int last = (int)((stop_at - 1) / per);
-                            record = {b, kv_head, j, last, last - wg + 1};
-                        }
-                    }
-                }
-                begin = stop_at;
+        int found;
+        __syncthreads();  // the items before these are read
+        pos = same(find_items<Bl>(a, lane, pos, end, per, wg, items, found));
+        __syncthreads();
+        found = same(found);
+        if (found == 0) break;
+        for (int i = 0; i < found; ++i) {
+            Item it = items[i];
+            it = Item{same(it.b), same(it.row), same(it.m), same(it.n), same(it.kv_head), same(it.j), same(it.from), same(it.upto),
+                      same(it.parts), same(it.whole)};
+            w.begin(it);
+            Span sp = Bl::span(a, it.m, it.n, it.j);
+            sp = Span{same(sp.lo), same(sp.hi), same(sp.sk), same(sp.head), same(sp.skip), same(sp.count)};
+            w.run(it.b, it.kv_head, sp, it.n, it.from, it.upto);
+            w.finish();
+            if (it.whole) {
+                w.store_out(it.kv_head);
+            } else {
+                w.store_partial(a.partials + (2 * (int64_t)wg + (it.from == 0 ? 1 : 0)) * A::kPartial);
+                if (it.parts > 0) record = Record{it.b, it.kv_head, it.j, it.parts};
             }
         }
     }
@@ -645,8 +825,8 @@ __global__ __launch_bounds__(256) void attention_join_kernel(TokensArgs a) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) o[i] = o[i] * u + po[i] * v;
         }
-        const int64_t i = (first + row) / a.group;
-        const int head = r.kv_head * a.group + (int)(first + row - i * a.group);
+        const int i = (int)((uint32_t)(first + row) / (uint32_t)a.group);
+        const int head = r.kv_head * a.group + (int)(first + row) - i * a.group;
         const float inv = 1.0f / (l == 0.0f ? 1.0f : l);
         u32x2 y;
 #pragma unroll
@@ -665,8 +845,10 @@ template <class Fn>
 void by_shape(int D, int ht, Fn&& fn) {
     using std::integral_constant;
     auto with = [&](auto d) {
-        if (ht == 1) fn(d, integral_constant<int, 1>{});
-        else fn(d, integral_constant<int, 2>{});
+        if constexpr (decltype(d)::value <= 192) {
+            if (ht == 2) return fn(d, integral_constant<int, 2>{});
+        }
+        fn(d, integral_constant<int, 1>{});
     };
     if (D == 64) with(integral_constant<int, 64>{});
     else if (D == 128) with(integral_constant<int, 128>{});
@@ -677,9 +859,14 @@ void by_shape(int D, int ht, Fn&& fn) {
 Shape plan(const TokensArgs& a, int kind) {
     Shape s{};
     const int64_t group = a.Hq / a.H;
-    s.ht = a.T * group <= 64 * a.B ? 1 : 2;
-    s.wgs = 2 * kCUs;
-    s.partial = 64 * s.ht * (int64_t)(a.D + 4);
+    // Blocks of 128 rows where sequences have more than 64 on average. Heads of 256
+    // keep to 64: the sums and queries of two columns of 256 do not fit the registers.
+    s.ht = a.D <= 192 && a.T * group > 64 * a.B ? 2 : 1;
+    by_shape(a.D, s.ht, [&](auto d, auto ht) {
+        constexpr int D = decltype(d)::value, HT = decltype(ht)::value;
+        s.wgs = kCUs * (kind == 0 ? Attend<0, 0, D, HT>::kPerCU : Attend<0, 1, D, HT>::kPerCU);
+        s.partial = Attend<0, 0, D, HT>::kPartial;
+    });
     return s;
 }
 
@@ -689,7 +876,7 @@ hipError_t launch(const TokensArgs& a, const Shape& s, hipStream_t stream) {
     by_shape(a.D, s.ht, [&](auto d, auto ht) {
         constexpr int D = decltype(d)::value, HT = decltype(ht)::value;
         using A = Attend<DT, KIND, D, HT>;
-        const size_t lds = (size_t)A::kStages * A::kStage;
+        const size_t lds = A::kBytes;
         e = allow_lds<attention_tokens_kernel<DT, KIND, D, HT>>(lds);
         if (e != hipSuccess) return;
         hipLaunchKernelGGL((attention_tokens_kernel<DT, KIND, D, HT>), dim3((unsigned)s.wgs), dim3(256), lds, stream, a);
