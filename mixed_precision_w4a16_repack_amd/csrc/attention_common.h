@@ -106,11 +106,16 @@ __device__ __forceinline__ void split_pair(float x, float y, uint32_t (&out)[NP]
             out[i] = __builtin_bit_cast(uint32_t, h);
             x = __builtin_fmaf((float)h[0], -1.0f, x);
             y = __builtin_fmaf((float)h[1], -1.0f, y);
-        } else {
-            const uint16_t a = to_act_bits<PDT>(x), b = to_act_bits<PDT>(y);
+        } else if constexpr (PDT == 0) {
+            const uint16_t a = to_act_bits<0>(x), b = to_act_bits<0>(y);
             out[i] = (uint32_t)a | (uint32_t)b << 16;
-            x -= act_to_float<PDT>(a);
-            y -= act_to_float<PDT>(b);
+            x -= act_to_float<0>(a);
+            y -= act_to_float<0>(b);
+        } else {  // both rounded by one instruction
+            typedef float float2_t __attribute__((ext_vector_type(2)));
+            out[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector(float2_t{x, y}, bf16x2_t));
+            x -= __builtin_bit_cast(float, out[i] << 16);
+            y -= __builtin_bit_cast(float, out[i] & 0xFFFF0000u);
         }
     }
 }

@@ -139,10 +139,11 @@ struct Attend {
     static constexpr int kPart = D * kTile * 2;
     static constexpr int kOperands = kI8 ? 4 * kPart + 3 * 256 : 0;
     // Workgroups that share a CU, and tiles in the ring that loads fill.
+    static constexpr int kListed = 128;  // tiles in hand: 64 found at once, and a few not yet worked on
     static constexpr int kPerCU = D <= 128 || (D == 192 && HT == 1 && !kI8) ? 2 : 1;
-    static constexpr int kFree = (kPerCU == 2 ? 80 : 160) * 1024 - kItems * (int)sizeof(Item) - kOperands;
+    static constexpr int kFree = (kPerCU == 2 ? 80 : 160) * 1024 - kItems * (int)sizeof(Item) - kListed * 16 - kOperands;
     static constexpr int kStages = kFree / kRaw < 4 ? kFree / kRaw : 4;
-    static constexpr int kBytes = kStages * kRaw + kOperands + kItems * (int)sizeof(Item);
+    static constexpr int kBytes = kStages * kRaw + kOperands + kListed * 16 + kItems * (int)sizeof(Item);
     static_assert(kStages >= 3, "a tile is loaded while others are worked on");
     using L = KvPlace<KIND>;
     using Pr = Prob<kF16P>;
@@ -261,9 +262,8 @@ struct Attend {
     }
 
     // This wave's part of a tile on its way to a place of the ring: half the waves load keys, half values.
-    __device__ __forceinline__ void request(const unsigned char* rec, int sub, int place) {
+    __device__ __forceinline__ void request(uint64_t at, int sub, int place) {
         constexpr uint32_t kKeys = kLoads * kWaves / 2 * 1024;  // bytes of a tile's keys, and of its values
-        const uint64_t at = reinterpret_cast<uint64_t>(rec);
         const u32x4 rsrc{(uint32_t)at, (uint32_t)(at >> 32) & 0xFFFFu, (uint32_t)L::record_bytes(D, a.P), 0x00020000u};
         const uint32_t to = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(__attribute__((address_space(3))) unsigned char*)lds + place * kRaw);
         const uint32_t part = (uint32_t)(wave % (kWaves / 2)) * kLoads * 1024;
@@ -343,12 +343,28 @@ struct Attend {
         return __builtin_bit_cast(uint32_t, x >> 15);
     }
 
+    // Asks for an order of instructions: a column tile's probabilities (8 times
+    // an exponential and its share of the others) between MFMAS matrix products each.
+    static constexpr int kVector = 0x002, kMatrix = 0x008, kLdsReads = 0x100, kExp = 0x400;
+    template <int MFMAS>
+    static __device__ __forceinline__ void take_turns() {
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+            __builtin_amdgcn_sched_group_barrier(kLdsReads, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(kMatrix, MFMAS, 0);
+            __builtin_amdgcn_sched_group_barrier(kVector, 5, 0);
+            __builtin_amdgcn_sched_group_barrier(kExp, 1, 0);
+        }
+    }
+
     // A tile of tokens from `at` on, whose products with the queries s holds;
     // whole: every column sees all of them. The next tile's products are made on
     // the way, so that the matrix cores have work while the probabilities are formed.
     __device__ __forceinline__ void work(floatx4 (&s)[HT][2], const unsigned char* next_keys, const unsigned char* operands,
                                          const float* scales, int at, int n, bool whole) {
-        const u32x4* values = reinterpret_cast<const u32x4*>(operands) + lane;
+        u32x4 v[NO];
+#pragma unroll
+        for (int i = 0; i < NO; ++i) v[i] = reinterpret_cast<const u32x4*>(operands)[64 * i + lane];
         floatx4 vs[2];
         if constexpr (kI8) {
 #pragma unroll
@@ -362,7 +378,6 @@ struct Attend {
             }
         }
         uint32_t seen[HT];
-        int bad = 0;  // 16 bits: whether the tile holds values that are not finite and some column may not see
         if (same((int)whole) == 0) {
             // Unseen scores are -infinity. An unseen value may be anything, and
             // 0 * NaN is NaN: an int8 value's scale that is not finite gives way
@@ -385,11 +400,35 @@ struct Attend {
             } else {
                 uint32_t all = ~0u;
 #pragma unroll
-                for (int i = 0; i < NO; ++i) {
-                    const u32x4 v = values[64 * i];
-                    all &= finite(v[0]) & finite(v[1]) & finite(v[2]) & finite(v[3]);
+                for (int i = 0; i < NO; ++i) all &= finite(v[i][0]) & finite(v[i][1]) & finite(v[i][2]) & finite(v[i][3]);
+                if (same((int)(__builtin_amdgcn_ballot_w64(all != ~0u) != 0)) != 0) {
+                    // Values that are not finite are taken out of the product, and the
+                    // columns that see one become NaN there, and stay so.
+                    constexpr uint32_t kOne = DT == 0 ? 0x3C003C00u : 0x3F803F80u;
+                    u32x4 ones[HT];
+#pragma unroll
+                    for (int h = 0; h < HT; ++h)
+#pragma unroll
+                        for (int x = 0; x < 4; ++x)
+                            ones[h][x] = ((seen[h] >> (2 * x) & 1u) | (seen[h] >> (2 * x + 1) & 1u) << 16) * (kOne & 0xFFFFu);
+#pragma unroll
+                    for (int i = 0; i < NO; ++i) {
+                        __builtin_amdgcn_sched_barrier(0);  // one after the other: this is rare, and its registers are everybody's
+                        u32x4 is;
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            const uint32_t keep = finite(v[i][x]);
+                            v[i][x] &= keep;
+                            is[x] = ~keep & kOne;
+                        }
+#pragma unroll
+                        for (int h = 0; h < HT; ++h) {
+                            const floatx4 hits = mfma16x16x32<PDT>(is, ones[h], floatx4{0.0f, 0.0f, 0.0f, 0.0f});
+#pragma unroll
+                            for (int r = 0; r < 4; ++r) o[h][i][r] = hits[r] > 0.0f ? NAN : o[h][i][r];
+                        }
+                    }
                 }
-                bad = __builtin_amdgcn_ballot_w64(all != ~0u) != 0;
             }
         }
         float peak[HT];
@@ -435,11 +474,11 @@ struct Attend {
         }
         floatx4 ahead[HT][2];
         products(next_keys, ahead);
-        u32x4 p[HT][NP];
 #pragma unroll
         for (int h = 0; h < HT; ++h) {
             const float ref = kI8 ? m[h] : m[h] - Pr::kBias;
             float w[8];
+            u32x4 p[NP];
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 w[j] = exp2_fast(__builtin_fmaf(s[h][j / 4][j % 4], factor[h], -ref));
@@ -451,88 +490,59 @@ struct Attend {
                 uint32_t parts[NP];
                 split_pair<PDT, NP>(w[2 * x], w[2 * x + 1], parts);
 #pragma unroll
-                for (int i = 0; i < NP; ++i) p[h][i][x] = parts[i];
+                for (int i = 0; i < NP; ++i) p[i][x] = parts[i];
             }
+#pragma unroll
+            for (int j = 0; j < NP; ++j)
+#pragma unroll
+                for (int i = 0; i < NO; ++i) o[h][i] = mfma16x16x32<PDT>(v[i], p[j], o[h][i]);
         }
 #pragma unroll
         for (int h = 0; h < HT; ++h)
 #pragma unroll
             for (int t = 0; t < 2; ++t) s[h][t] = ahead[h][t];
-        constexpr uint32_t kOne = DT == 0 ? 0x3C003C00u : 0x3F803F80u;
-        bad = same(bad);
-        if (!kI8 && bad) {
-            // The columns that see a value that is not finite become NaN there, and stay so.
-            u32x4 ones[HT];
-#pragma unroll
-            for (int h = 0; h < HT; ++h)
-#pragma unroll
-                for (int x = 0; x < 4; ++x) ones[h][x] = ((seen[h] >> (2 * x) & 1u) | (seen[h] >> (2 * x + 1) & 1u) << 16) * (kOne & 0xFFFFu);
-#pragma unroll
-            for (int i = 0; i < NO; ++i) {
-                __builtin_amdgcn_sched_barrier(0);  // one after the other: this is rare, and its registers are everybody's
-                u32x4 is = values[64 * i];
-#pragma unroll
-                for (int x = 0; x < 4; ++x) is[x] = ~finite(is[x]) & kOne;
-#pragma unroll
-                for (int h = 0; h < HT; ++h) {
-                    const floatx4 hits = mfma16x16x32<PDT>(is, ones[h], floatx4{0.0f, 0.0f, 0.0f, 0.0f});
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) o[h][i][r] = hits[r] > 0.0f ? NAN : o[h][i][r];
-                }
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < NO; ++i) {
-            u32x4 v = values[64 * i];
-            if (!kI8 && bad) {  // they are taken out of the product
-#pragma unroll
-                for (int x = 0; x < 4; ++x) v[x] &= finite(v[x]);
-            }
-#pragma unroll
-            for (int j = 0; j < NP; ++j)
-#pragma unroll
-                for (int h = 0; h < HT; ++h) o[h][i] = mfma16x16x32<PDT>(v, p[h][j], o[h][i]);
-        }
+        // Products take turns with the probabilities' instructions: the keys'
+        // products with the first column tile's, the values' with the next one's.
+        __builtin_amdgcn_sched_group_barrier(kLdsReads, 4, 0);
+        take_turns<(2 * NQ * HT + 7) / 8>();
+        if constexpr (HT == 2) take_turns<(NO * NP + 7) / 8>();
+        __builtin_amdgcn_sched_group_barrier(kMatrix, NO * NP, 0);
     }
 
     // Items [from, to) of the block's tiles, those of missing pages left out.
     __device__ __forceinline__ void run(int64_t b, int kv_head, const Span& sp, int n, int from, int to) {
         const int tiles_per_page = a.P / kTile;
         const int whole_shift = (tiles_per_page & (tiles_per_page - 1)) == 0 ? __builtin_ctz(tiles_per_page) : -1;
-        int block = from;  // first item of the 64 in hand
-        uint64_t todo = 0;
-        int64_t place_l = 0;
-        int sub_l = 0;
-        // The ring: tile i of those that are there lies in place i % kStages. Their
-        // first tokens, the next one's lowest (an array would lie in scratch memory,
-        // and a load from there wait for the ring's).
-        static_assert(kStages <= 4, "first tokens are kept for four tiles");
-        uint64_t first_lo = 0, first_hi = 0;
+        // The tiles that are there, 64 items looked at at once: where each lies
+        // (two words), its number in the page, its first token. Every wave writes
+        // the same list and reads what it wrote.
+        u32x4* list = reinterpret_cast<u32x4*>(lds + kStages * kRaw + kOperands);
+        int next_item = from, found = 0;
+        auto look = [&]() {
+            const int item = next_item + lane, tile = sp.tile(item);
+            int64_t page = -1;
+            int sub = 0;
+            if (item < to) {
+                const int i = whole_shift >= 0 ? tile >> whole_shift : tile / tiles_per_page;
+                page = a.table[b * a.table_ld + i];
+                sub = tile - i * tiles_per_page;
+            }
+            const bool ok = page >= 0 && page < a.pages;
+            const uint64_t mask = __builtin_amdgcn_ballot_w64(ok);
+            const int at = found + (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0u));
+            const uint64_t place = reinterpret_cast<uint64_t>(a.cache) + (uint64_t)((page * a.H + kv_head) * L::record_bytes(D, a.P));
+            if (ok) list[at % kListed] = u32x4{(uint32_t)place, (uint32_t)(place >> 32), (uint32_t)sub, (uint32_t)tile * kTile};
+            found = same(found + __builtin_popcountll(mask));
+            next_item += 64;
+        };
+        // The ring: tile i of the list lies in place i % kStages.
         int there = 0, done = 0;  // tiles requested and worked on
         int fill = 0, take = 0;   // their places
         auto more = [&]() -> bool {  // requests the next tile, if there is one
-            while (todo == 0 && block < to) {
-                const int item = block + lane, tile_l = sp.tile(item);
-                int64_t page = -1;
-                if (item < to) {
-                    const int i = whole_shift >= 0 ? tile_l >> whole_shift : tile_l / tiles_per_page;
-                    page = a.table[b * a.table_ld + i];
-                    sub_l = tile_l - i * tiles_per_page;
-                }
-                const bool ok = page >= 0 && page < a.pages;
-                place_l = ok ? (page * a.H + kv_head) * L::record_bytes(D, a.P) : 0;
-                todo = __builtin_amdgcn_ballot_w64(ok);
-                if (todo == 0) block += 64;
-            }
-            if (todo == 0) return false;
-            const int i = __builtin_ctzll(todo);
-            todo &= todo - 1;
-            request(a.cache + read_lane(place_l, i), __builtin_amdgcn_readlane(sub_l, i), fill);
-            const uint64_t first_token = (uint32_t)(sp.tile(block + i) * kTile);
-            const int behind = there - done;
-            if (behind < 2) first_lo |= first_token << (32 * behind);
-            else first_hi |= first_token << (32 * behind - 64);
-            if (todo == 0) block += 64;
+            while (there == found && next_item < to) look();
+            if (there == found) return false;
+            const u32x4 e = list[there % kListed];
+            request((uint64_t)(uint32_t)same((int)e[1]) << 32 | (uint32_t)same((int)e[0]), same((int)e[2]), fill);
             fill = fill + 1 < kStages ? fill + 1 : 0;
             ++there;
             return true;
@@ -574,9 +584,7 @@ struct Attend {
         int t = 0, place = 0, next = 0, third_at = 0;
         auto advance = [&]() -> bool {
             if (done == there) return false;
-            t = same((int)first_lo);
-            first_lo = first_lo >> 32 | first_hi << 32;
-            first_hi >>= 32;
+            t = same((int)reinterpret_cast<const uint32_t*>(list)[done % kListed * 4 + 3]);
             place = take;
             next = place_of(take + 1);
             third_at = third;
@@ -584,9 +592,7 @@ struct Attend {
                 const int left = there - done;  // this one, the ones that are there and the ones on their way
                 wait_for(left - 3 < 0 ? 0 : left - 3);
                 stage_barrier();
-                ++done;
                 if (going) going = more();
-                --done;
                 // Into places that were read for tile done - 1, or before.
                 if (wave < kWaves / 2) {
                     if (left > 2) convert(place_of(take + 2), done + 2);
@@ -598,9 +604,7 @@ struct Attend {
             } else {
                 wait_for(there - done - 2 < 0 ? 0 : there - done - 2);
                 stage_barrier();
-                ++done;
                 if (going) going = more();
-                --done;
             }
             take = next;
             ++done;

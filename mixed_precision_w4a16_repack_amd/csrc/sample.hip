@@ -27,21 +27,31 @@ constexpr int kBlocks = kKeys / 64;  // of 64 values each, one a thread in the s
 constexpr uint32_t kCarry = 1u << 15;
 constexpr int kCarries = (int)(kSampleMaxV / kCarry);
 constexpr int kNone = -1;
+constexpr int kListed = 1024;  // tokens of one value that are listed
 
-// Order-preserving key of a logit's bits, 0 for one that is never drawn (-infinity,
-// NaN); -0 counts as 0.
+// Keys order logits as they are ordered: 0x8000 above a positive one's bits,
+// a negative one's bits inverted. -infinity and what lies below it (negative
+// NaN) are never drawn, nor what lies above +infinity; -0's count goes to 0's.
+// The borders are multiples of 64: no block of 64 keys holds a drawn and a
+// forbidden one but +infinity's, of which only the first is drawn.
 template <int DT>
-__device__ __forceinline__ uint32_t key_of(uint32_t b) {
-    constexpr uint32_t inf = DT == 0 ? 0x7C00u : 0x7F80u;
-    const uint32_t mag = b & 0x7FFFu;
-    if (mag > inf || b == (inf | 0x8000u)) return 0;
-    if (mag == 0) return 0x8000u;
-    return b & 0x8000u ? b ^ 0xFFFFu : b | 0x8000u;
+struct Keys {
+    static constexpr uint32_t kInf = DT == 0 ? 0x7C00u : 0x7F80u;
+    static constexpr uint32_t kTop = 0x8000u | kInf, kLow = 0xFFFFu - (0x8000u | kInf);  // +infinity's, -infinity's
+    static constexpr uint32_t kZero = 0x8000u;
+    static constexpr uint32_t kFirst = kLow + 1;
+    static __device__ __forceinline__ float value(uint32_t key) {
+        return act_to_float<DT>((uint16_t)(key & 0x8000u ? key & 0x7FFFu : key ^ 0xFFFFu));
+    }
+};
+typedef short short2_t __attribute__((ext_vector_type(2)));
+// The keys of two logits.
+__device__ __forceinline__ uint32_t two_keys(uint32_t w) {
+    return w ^ (__builtin_bit_cast(uint32_t, __builtin_bit_cast(short2_t, w) >> 15) | 0x80008000u);
 }
-template <int DT>
-__device__ __forceinline__ float value_of(uint32_t key) {
-    return act_to_float<DT>((uint16_t)(key & 0x8000u ? key & 0x7FFFu : key ^ 0xFFFFu));
-}
+// Where a key's count is: words of two keys; the words of block b (64 keys) are
+// turned by b, so that threads that each walk through a block meet no bank twice.
+__device__ __forceinline__ uint32_t word_of(uint32_t key) { return key >> 1 ^ (key >> 6 & 31u); }
 
 // 2^t for t <= 0: e^(f ln 2) of the part below 1/2 as a Taylor sum (its rest is below 2^-47).
 __device__ __forceinline__ double exp2_of(double t) {
@@ -62,21 +72,41 @@ __device__ __forceinline__ double exp2_of(double t) {
     return __builtin_ldexp(e, (int)n);
 }
 
+// v of the lane that a DPP control names, 0 where there is none.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint32_t from_lane(uint32_t v) {
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWS, 0xF, false);
+}
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double from_lane(double v) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = from_lane<CTRL, ROWS>((uint32_t)b), hi = from_lane<CTRL, ROWS>((uint32_t)(b >> 32));
+    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
 // Sum over lanes 0 .. lane.
 template <class T>
-__device__ __forceinline__ T scan(T v, int lane) {
-#pragma unroll
-    for (int off = 1; off < 64; off *= 2) {
-        const T up = __shfl_up(v, off);
-        if (lane >= off) v += up;
-    }
+__device__ __forceinline__ T scan(T v) {
+    v += from_lane<0x111, 0xF>(v);  // row_shr:1, 2, 4, 8: within 16 lanes
+    v += from_lane<0x112, 0xF>(v);
+    v += from_lane<0x114, 0xF>(v);
+    v += from_lane<0x118, 0xF>(v);
+    v += from_lane<0x142, 0xA>(v);  // row_bcast:15 into rows 1 and 3
+    v += from_lane<0x143, 0xC>(v);  // row_bcast:31 into rows 2 and 3
     return v;
 }
+template <class T>
+__device__ __forceinline__ T lane_before(T v) { return from_lane<0x138, 0xF>(v); }  // wave_shr:1
+__device__ __forceinline__ double read_lane(double v, int lane) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)b, lane), hi = __builtin_amdgcn_readlane((int)(uint32_t)(b >> 32), lane);
+    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+__device__ __forceinline__ uint32_t read_lane(uint32_t v, int lane) { return (uint32_t)__builtin_amdgcn_readlane((int)v, lane); }
 
 struct Shared {
     uint32_t counts[kKeys / 2];  // two a word
-    double weight[kBlocks];      // of a block's tokens, then of the blocks before it in the order
-    uint32_t tokens[kBlocks];    // the same for counts
+    double weight[kBlocks];      // of the tokens of the blocks before each in the order
+    uint32_t tokens[kBlocks];    // their number
     uint16_t carried[kCarries];  // values that have kCarry more
     int carries;
     double wave_weight[kWaves];
@@ -87,24 +117,27 @@ struct Shared {
     uint32_t place_tokens; // their number
     uint32_t place_key;
     uint32_t place_count;
+    int found;             // tokens of the drawn value listed
+    uint32_t list[kListed];
 };
 
 template <int DT>
 struct Row {
     const uint16_t* x;
     int V, lane, wave;
-    // fn(index, bits) for this wave's part of the row, 8 a lane: parts are runs in index order.
-    int part, from, to;
+    // This wave's part of the row is a run of 512 logits a step, 8 a lane; as many steps for each wave.
+    int steps, from;
     __device__ __forceinline__ Row(const SampleArgs& a, int row)
         : x(a.logits + row * a.ldl), V(a.V), lane(threadIdx.x & 63), wave(__builtin_amdgcn_readfirstlane(threadIdx.x >> 6)) {
-        part = (V + kWaves * 512 - 1) / (kWaves * 512) * 512;
-        from = wave * part < V ? wave * part : V;
-        to = from + part < V ? from + part : V;
+        steps = (V + kWaves * 512 - 1) / (kWaves * 512);
+        from = wave * steps * 512;
     }
-    // Eight bits patterns at i (-infinity behind the row's end).
-    __device__ __forceinline__ u32x4 load(int i) const {
+    __device__ __forceinline__ int index(int step) const { return from + step * 512 + 8 * lane; }
+    // Eight logits (-infinity behind the part's and the row's end).
+    __device__ __forceinline__ u32x4 load(int step) const {
+        const int i = step < steps ? index(step) : V;
         if (i + 8 <= V) return *reinterpret_cast<const u32x4_any*>(x + i);
-        constexpr uint32_t low = DT == 0 ? 0xFC00u : 0xFF80u;
+        constexpr uint32_t low = 0x8000u | Keys<DT>::kInf;
         u32x4 v;
 #pragma unroll
         for (int e = 0; e < 4; ++e)
@@ -112,11 +145,11 @@ struct Row {
         return v;
     }
 };
-
-__device__ __forceinline__ uint32_t half_of(const u32x4& v, int e) { return v[e / 2] >> (16 * (e % 2)) & 0xFFFFu; }
+constexpr int kAtOnce = 4;  // steps whose loads are in flight together
 
 template <int DT>
 __global__ __launch_bounds__(kThreads) void sample_kernel(SampleArgs a) {
+    using K = Keys<DT>;
     extern __shared__ __align__(16) unsigned char raw[];
     Shared& s = *reinterpret_cast<Shared*>(raw);
     const int tid = threadIdx.x, row_at = blockIdx.x;
@@ -124,133 +157,176 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(SampleArgs a) {
     const int lane = row.lane, wave = row.wave;
     const float temperature = a.temperature ? a.temperature[row_at] : 1.0f;
     const bool greedy = !(temperature > 0.0f);
+    // A key that may be drawn.
+    auto drawn = [](uint32_t key) { return key - K::kFirst <= K::kTop - K::kFirst; };
 
-    // Count the row's values, and its largest.
-    if (!greedy) {
+    uint32_t top = 0;  // the largest logit's key
+    if (greedy) {
+        for (int step = 0; step < row.steps; step += kAtOnce) {
+            u32x4 v[kAtOnce];
+#pragma unroll
+            for (int i = 0; i < kAtOnce; ++i) v[i] = row.load(step + i);
+#pragma unroll
+            for (int i = 0; i < kAtOnce; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    uint32_t k = two_keys(v[i][e]);
+                    const uint32_t lo = drawn(k & 0xFFFFu) ? k & 0xFFFFu : 0u, hi = drawn(k >> 16) ? k >> 16 : 0u;
+                    top = lo > top ? lo : top;
+                    top = hi > top ? hi : top;
+                }
+        }
+        if (top == K::kZero - 1) top = K::kZero;
+#pragma unroll
+        for (int off = 32; off > 0; off /= 2) {
+            const uint32_t o = __shfl_xor(top, off);
+            top = o > top ? o : top;
+        }
+        if (lane == 0) s.wave_top[wave] = top;
+        if (tid == 0) s.found = 0;
+        __syncthreads();
+        for (int i = 0; i < kWaves; ++i) top = s.wave_top[i] > top ? s.wave_top[i] : top;
+    } else {
         for (int i = tid; i < kKeys / 8; i += kThreads) reinterpret_cast<u32x4*>(s.counts)[i] = u32x4{0u, 0u, 0u, 0u};
-        if (tid == 0) s.carries = 0, s.last = 0;
+        if (tid == 0) s.carries = 0, s.last = 0, s.found = 0, s.block = kBlocks;
+        __syncthreads();
+        // Count the row's values.
+        for (int step = 0; step < row.steps; step += kAtOnce) {  // as often for each wave
+            // The one that fills a count's lower 15 bits takes them away again.
+            // Between two barriers there are at most 4 * 8 * kThreads = 2^15 others,
+            // so 16 bits hold them.
+            static_assert(kAtOnce * 8 * kThreads <= (int)kCarry, "counts of 16 bits");
+            if (step != 0) __syncthreads();
+            u32x4 v[kAtOnce];
+#pragma unroll
+            for (int i = 0; i < kAtOnce; ++i) v[i] = row.load(step + i);
+#pragma unroll
+            for (int i = 0; i < kAtOnce; ++i) {
+                uint32_t key[8], old[8];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const uint32_t k = two_keys(v[i][e]);
+                    key[2 * e] = k & 0xFFFFu;
+                    key[2 * e + 1] = k >> 16;
+                }
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    old[e] = 0u;  // forbidden tokens may be most of a row: they are not counted
+                    if (key[e] != K::kLow) old[e] = atomicAdd(&s.counts[word_of(key[e])], 1u << (16 * (key[e] & 1))) >> (16 * (key[e] & 1)) & 0xFFFFu;
+                }
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (old[e] == kCarry - 1) {
+                        atomicSub(&s.counts[word_of(key[e])], kCarry << (16 * (key[e] & 1)));
+                        s.carried[atomicAdd(&s.carries, 1)] = (uint16_t)(key[e] == K::kZero - 1 ? K::kZero : key[e]);
+                    }
+            }
+        }
+        __syncthreads();
+        if (tid == 0) {  // both zeros are one value
+            const uint32_t negative = s.counts[word_of(K::kZero - 1)] >> 16;
+            s.counts[word_of(K::kZero - 1)] &= 0xFFFFu;
+            s.counts[word_of(K::kZero)] += negative;
+        }
         __syncthreads();
     }
-    uint32_t top = 0;
-    for (int base = 0; base < row.part; base += 512) {  // as often for each wave
-        // The one that fills a count's lower 15 bits takes them away again.
-        // Between two barriers there are at most 4 * 8 * kThreads = 2^15 others,
-        // so 16 bits hold them.
-        if (!greedy && base % 2048 == 0 && base != 0) __syncthreads();
-        const int i = row.from + base + 8 * lane;
-        if (i >= row.to) continue;
-        const u32x4 v = row.load(i);
-        uint32_t key[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            key[e] = key_of<DT>(half_of(v, e));
-            top = key[e] > top ? key[e] : top;
-        }
-        if (greedy) continue;
-        uint32_t old[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            old[e] = key[e] != 0 ? atomicAdd(&s.counts[key[e] / 2], 1u << (16 * (key[e] & 1))) >> (16 * (key[e] & 1)) & 0xFFFFu : 0u;
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            if (old[e] == kCarry - 1) {
-                atomicSub(&s.counts[key[e] / 2], kCarry << (16 * (key[e] & 1)));
-                s.carried[atomicAdd(&s.carries, 1)] = (uint16_t)key[e];
-            }
-    }
-#pragma unroll
-    for (int off = 32; off > 0; off /= 2) {
-        const uint32_t o = __shfl_xor(top, off);
-        top = o > top ? o : top;
-    }
-    if (lane == 0) s.wave_top[wave] = top;
-    __syncthreads();
-    top = s.wave_top[lane % kWaves];
-#pragma unroll
-    for (int off = kWaves / 2; off > 0; off /= 2) {
-        const uint32_t o = __shfl_xor(top, off);
-        top = o > top ? o : top;
-    }
-    if (top == 0) {  // nothing to draw
-        if (tid == 0) {
-            a.tokens[row_at] = kNone;
-            if (a.probs) a.probs[row_at] = 0.0f;
-        }
-        return;
-    }
 
-    uint32_t key = top, before = 0;  // the drawn token's value, and how many of that value come before it
+    uint32_t key = top, before = 0, same = ~0u;  // the drawn token's value, how many of that value come before it, how many there are
     double prob = 1.0;
     if (!greedy) {
-        const double most = (double)value_of<DT>(top), per = 1.4426950408889634074 / (double)temperature;
+        // Block b holds the keys kKeys - 1 - 64 b - i, i = 0 .. 63, so that blocks
+        // and i go down the order. Thread b holds block b's counts.
         const int carries = s.carries;
-        // A value's weight and how often it occurs. Block b holds the keys
-        // kKeys - 1 - 64 b - lane, so that lanes and blocks go down the order.
-        auto count_at = [&](int b, int l) {
-            const uint32_t k = kKeys - 1 - 64 * b - l;
-            uint32_t n = s.counts[k / 2] >> (16 * (k & 1)) & 0xFFFFu;
+        auto carried = [&](uint32_t k) {
+            uint32_t n = 0;
             for (int i = 0; i < carries; ++i) n += s.carried[i] == k ? kCarry : 0u;
             return n;
         };
-        auto weight_at = [&](int b, int l) {
-            const uint32_t k = kKeys - 1 - 64 * b - l;
-            return k == top ? 1.0 : exp2_of(((double)value_of<DT>(k) - most) * per);
-        };
+        const uint32_t high = kKeys - 1 - 64 * tid;  // the block's first key
+        uint32_t counts[32];                         // of the keys high - 2 i (upper half) and high - 2 i - 1
+        uint32_t any = 0;
+        const bool forbidden = !drawn(high - 63);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+            counts[i] = forbidden ? 0u : s.counts[word_of(high - 2 * i)];
+            if (high - 63 == K::kTop) counts[i] = i == 31 ? counts[i] & 0xFFFFu : 0u;  // behind +infinity
+            any |= counts[i];
+        }
+        if (carries > 0 && !forbidden)
+            for (int i = 0; i < carries; ++i) any |= (high - s.carried[i]) < 64u;
+        if (any != 0) atomicMin(&s.block, tid);
+        __syncthreads();
+        const int first_block = s.block;
+        if (first_block == kBlocks) {  // nothing to draw
+            if (tid == 0) {
+                a.tokens[row_at] = kNone;
+                if (a.probs) a.probs[row_at] = 0.0f;
+            }
+            return;
+        }
+        if (tid == first_block) {
+            uint32_t k = 0;
+#pragma unroll
+            for (int i = 31; i >= 0; --i) {
+                if (counts[i] & 0xFFFFu) k = high - 2 * i - 1;
+                if (counts[i] >> 16) k = high - 2 * i;
+            }
+            for (int i = 0; i < carries; ++i)
+                if (high - s.carried[i] < 64u && s.carried[i] > k) k = s.carried[i];
+            s.place_key = k;
+        }
+        __syncthreads();
+        top = s.place_key;
+        // A value's weight. Within a block the values are equally far apart, so
+        // its weights are a power series: two exponentials a block.
+        const double most = (double)K::value(top), per = 1.4426950408889634074 / (double)temperature;
+        auto weight_at = [&](uint32_t k) { return k == top ? 1.0 : exp2_of(((double)K::value(k) - most) * per); };
         const float min_p = a.min_p ? a.min_p[row_at] : 0.0f;
         const double least = min_p > 0.0f ? (min_p < 1.0f ? (double)min_p : 1.0) : 0.0;
-        uint32_t kept = 0;  // tokens that min-p keeps
-        for (int b = wave; b < kBlocks; b += kWaves) {
-            const uint32_t n = count_at(b, lane);
-            double w = 0.0;
-            uint32_t sum = 0;
-            if (__builtin_amdgcn_ballot_w64(n != 0) != 0) {
-                const double each = n != 0 ? weight_at(b, lane) : 0.0;
-                w = n * each;
-                sum = n;
-                kept += each >= least ? n : 0u;
+        double own_w = 0.0;
+        uint32_t own_n = 0, kept = 0;  // kept: tokens that min-p keeps
+        if (any != 0) {
+            // From the block's first key on, or the row's largest logit's.
+            const uint32_t from = high < top ? high : top;
+            double w = weight_at(from);
+            const double ratio = exp2_of(((double)K::value(high - 63) - (double)K::value(high - 62)) * per);
+            const bool lists = carries > 0;
 #pragma unroll
-                for (int off = 32; off > 0; off /= 2) {
-                    w += __shfl_xor(w, off);
-                    sum += __shfl_xor(sum, off);
-                }
-            }
-            if (lane == 0) {
-                s.weight[b] = w;
-                s.tokens[b] = sum;
+            for (int i = 0; i < 64; ++i) {
+                if (i % 8 == 0) __builtin_amdgcn_sched_barrier(0);  // 128 registers a thread: no more at once
+                uint32_t n = i % 2 == 0 ? counts[i / 2] >> 16 : counts[i / 2] & 0xFFFFu;
+                if (lists) n += carried(high - i);
+                own_n += n;
+                own_w += (double)n * w;
+                kept += w >= least ? n : 0u;
+                if (high - i <= from) w *= ratio;
             }
         }
-#pragma unroll
-        for (int off = 32; off > 0; off /= 2) kept += __shfl_xor(kept, off);
-        if (lane == 0) s.wave_kept[wave] = kept;
-        __syncthreads();
-        // Sums over the blocks before each: thread b holds block b's.
-        const double own_w = s.weight[tid];
-        const uint32_t own_n = s.tokens[tid];
-        const double scan_w = scan(own_w, lane);
-        const uint32_t scan_n = scan(own_n, lane);
+        // Sums over the blocks before each.
+        const double scan_w = scan(own_w);
+        const uint32_t scan_n = scan(own_n), scan_kept = scan(kept);
         if (lane == 63) {
             s.wave_weight[wave] = scan_w;
             s.wave_tokens[wave] = scan_n;
+            s.wave_kept[wave] = scan_kept;
         }
+        if (own_w > 0.0) atomicMax(&s.last, tid);
         __syncthreads();
-        double to_w = 0.0;
+        double to_w = 0.0, all_w = 0.0;
         uint32_t to_n = 0, all_n = 0, all_kept = 0;
+#pragma unroll
         for (int i = 0; i < kWaves; ++i) {
-            if (i < wave) to_w += s.wave_weight[i], to_n += s.wave_tokens[i];
+            if (i == wave) to_w = all_w, to_n = all_n;
+            all_w += s.wave_weight[i];
             all_n += s.wave_tokens[i];
             all_kept += s.wave_kept[i];
         }
-        double all_w = 0.0;
-        for (int i = 0; i < kWaves; ++i) all_w += s.wave_weight[i];
-        const double up_w = __shfl_up(scan_w, 1);
-        const uint32_t up_n = __shfl_up(scan_n, 1);
-        const double from_w = lane == 0 ? to_w : to_w + up_w;
-        const uint32_t from_n = lane == 0 ? to_n : to_n + up_n;
+        const double from_w = to_w + lane_before(scan_w);  // lane 0: nothing
+        const uint32_t from_n = to_n + lane_before(scan_n);
         to_w += scan_w;
         to_n += scan_n;
         s.weight[tid] = from_w;
         s.tokens[tid] = from_n;
-        if (own_w > 0.0) atomicMax(&s.last, tid);
 
         // Finds the value with the first token at which the number of tokens
         // reaches `tokens` (by_weight false), or their weight reaches or passes
@@ -260,28 +336,31 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(SampleArgs a) {
             if (tid == 0) s.block = kBlocks;
             __syncthreads();
             const bool hit = by_weight ? (pass ? to_w > weight : to_w >= weight) : to_n >= tokens;
-            if (hit && own_n != 0) atomicMin(&s.block, tid);
+            const uint64_t hits = __builtin_amdgcn_ballot_w64(hit && own_n != 0);
+            if (hits != 0 && lane == 0) atomicMin(&s.block, 64 * wave + __builtin_ctzll(hits));
             __syncthreads();
             const int b = s.block < kBlocks ? s.block : s.last;  // a weight that rounding leaves above the sum of all
-            const uint32_t n = count_at(b, lane);
-            const double each = n != 0 ? weight_at(b, lane) : 0.0, w = n * each;
-            const double in_w = scan(w, lane);
-            const uint32_t in_n = scan(n, lane);
-            const double before_w = s.weight[b] + (in_w - w);
-            const uint32_t before_n = s.tokens[b] + (in_n - n);
+            const uint32_t k = kKeys - 1 - 64 * b - lane;
+            uint32_t n = s.counts[word_of(k)] >> (16 * (k & 1)) & 0xFFFFu;
+            if (kKeys - 64 - 64 * b == (int)K::kTop && lane != 63) n = 0;  // behind +infinity
+            if (carries > 0) n += carried(k);
+            const double each = n != 0 ? weight_at(k) : 0.0, w = n * each;
+            const double in_w = scan(w);
+            const uint32_t in_n = scan(n);
+            const double before_w = s.weight[b] + lane_before(in_w);
+            const uint32_t before_n = s.tokens[b] + lane_before(in_n);
             const bool here = by_weight ? (pass ? before_w + w > weight : before_w + w >= weight) : before_n + n >= tokens;
-            uint64_t at = __builtin_amdgcn_ballot_w64(here && n != 0 && (!by_weight || w > 0.0));
-            int l;
-            if (at != 0) l = __builtin_ctzll(at);
-            else l = 63 - __builtin_clzll(__builtin_amdgcn_ballot_w64(n != 0 && (!by_weight || w > 0.0)));
+            const bool some = n != 0 && (!by_weight || w > 0.0);
+            const uint64_t at = __builtin_amdgcn_ballot_w64(here && some);
+            const int l = at != 0 ? __builtin_ctzll(at) : 63 - __builtin_clzll(__builtin_amdgcn_ballot_w64(some) | 1);
             if (wave == 0 && lane == l) {
                 s.place_weight = before_w;
                 s.place_tokens = before_n;
-                s.place_key = kKeys - 1 - 64 * b - l;
+                s.place_key = k;
                 s.place_count = n;
             }
             __syncthreads();
-            return __shfl(each, l);
+            return read_lane(each, l);
         };
         // Weight of the first `tokens` tokens of the order.
         auto weight_of = [&](uint32_t tokens) {
@@ -305,34 +384,90 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(SampleArgs a) {
         const int top_k = a.top_k ? a.top_k[row_at] : 0;
         const float top_p = a.top_p ? a.top_p[row_at] : 1.0f;
         uint32_t most_tokens = top_k > 0 && (uint32_t)top_k < all_n ? (uint32_t)top_k : all_n;
+        double total = weight_of(most_tokens);
         if (top_p < 1.0f) {
-            const double target = top_p > 0.0f ? (double)top_p * weight_of(most_tokens) : 0.0;
+            const double target = top_p > 0.0f ? (double)top_p * total : 0.0;
             uint32_t n = 1;
             if (target > 0.0) {
                 const double each = find(true, 0u, target, false);
-                n = s.place_tokens + needed(each, target, false);
+                const uint32_t r = needed(each, target, false);
+                n = s.place_tokens + r;
+                if (n < most_tokens) total = s.place_weight + r * each;
+            } else {
+                total = 1.0;
             }
             most_tokens = n < most_tokens ? n : most_tokens;
         }
-        if (least > 0.0 && all_kept < most_tokens) most_tokens = all_kept;
-        const double total = weight_of(most_tokens);
+        if (least > 0.0 && all_kept < most_tokens) {
+            most_tokens = all_kept;
+            total = weight_of(most_tokens);
+        }
         const float u = a.uniforms[row_at];
         const double target = (u > 0.0f ? (u < 1.0f ? (double)u : 0x0.ffffffp0) : 0.0) * total;
         const double each = find(true, 0u, target, true);
         key = s.place_key;
+        same = s.place_count;
         before = needed(each, target, true) - 1;
         prob = each / total;
+    } else if (top == 0) {
+        if (tid == 0) {
+            a.tokens[row_at] = kNone;
+            if (a.probs) a.probs[row_at] = 0.0f;
+        }
+        return;
     }
 
     // The token: the one of its value that `before` others precede.
+    const uint32_t bits = key & 0x8000u ? key & 0x7FFFu : key ^ 0xFFFFu, two = bits | bits << 16;
+    const uint32_t sign = key == K::kZero ? 0x7FFF7FFFu : ~0u;  // a zero of either sign
+    auto matches = [&](const u32x4& v) {  // which of the eight
+        uint32_t m = 0;
+        bool some = false;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const uint32_t x = (v[e] & sign) ^ two;
+            some |= (x & 0xFFFFu) == 0 || x < 0x10000u;
+        }
+        if (some) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t x = (v[e] & sign) ^ two;
+                m |= (uint32_t)((x & 0xFFFFu) == 0) << (2 * e) | (uint32_t)(x < 0x10000u) << (2 * e + 1);
+            }
+        }
+        return m;
+    };
+    auto answer = [&](int index) {
+        a.tokens[row_at] = index;
+        if (a.probs) a.probs[row_at] = (float)prob;
+    };
+    // Few of that value: list them, and take the one with `before` smaller ones.
+    const bool listed = same <= kListed;
     uint32_t mine = 0;
-    for (int i = row.from + 8 * lane; i < row.to; i += 512) {
-        const u32x4 v = row.load(i);
+    for (int step = 0; step < row.steps; step += kAtOnce) {
+        u32x4 v[kAtOnce];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) mine += key_of<DT>(half_of(v, e)) == key;
+        for (int i = 0; i < kAtOnce; ++i) v[i] = row.load(step + i);
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) {
+            uint32_t m = step + i < row.steps ? matches(v[i]) : 0u;
+            mine += __builtin_popcount(m);
+            for (; listed && m != 0; m &= m - 1) s.list[atomicAdd(&s.found, 1)] = row.index(step + i) + __builtin_ctz(m);
+        }
     }
-#pragma unroll
-    for (int off = 32; off > 0; off /= 2) mine += __shfl_xor(mine, off);
+    if (listed) {
+        __syncthreads();
+        const int n = s.found;
+        for (int i = tid; i < n; i += kThreads) {
+            const uint32_t index = s.list[i];
+            uint32_t smaller = 0;
+            for (int j = 0; j < n; ++j) smaller += s.list[j] < index;
+            if (smaller == before) answer((int)index);
+        }
+        return;
+    }
+    // Many: the wave's part that holds it, then the step.
+    mine = read_lane(scan(mine), 63);
     __syncthreads();  // the searches' reads of wave_tokens are done
     if (lane == 0) s.wave_tokens[wave] = mine;
     __syncthreads();
@@ -342,23 +477,16 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(SampleArgs a) {
         before -= n;
     }
     if (before >= mine) return;
-    for (int base = row.from; base < row.to; base += 512) {
-        const int i = base + 8 * lane;
-        uint32_t found = 0;
-        if (i < row.to) {
-            const u32x4 v = row.load(i);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) found |= (uint32_t)(key_of<DT>(half_of(v, e)) == key) << e;
-        }
-        const uint32_t n = __builtin_popcount(found), to = scan(n, lane), all = __shfl(to, 63);
+    for (int step = 0; step < row.steps; ++step) {
+        uint32_t m = matches(row.load(step));
+        const uint32_t n = __builtin_popcount(m), to = scan(n), all = read_lane(to, 63);
         if (before >= all) {
             before -= all;
             continue;
         }
         if (before >= to - n && before < to) {
-            for (uint32_t skip = before - (to - n); skip > 0; --skip) found &= found - 1;
-            a.tokens[row_at] = i + __builtin_ctz(found);
-            if (a.probs) a.probs[row_at] = (float)prob;
+            for (uint32_t skip = before - (to - n); skip > 0; --skip) m &= m - 1;
+            answer(row.index(step) + __builtin_ctz(m));
         }
         return;
     }
