@@ -25,7 +25,7 @@ constexpr int kThreads = 1024, kWaves = kThreads / 64;
 constexpr int kKeys = 1 << 16;
 constexpr int kBlocks = kKeys / 64;  // of 64 values each, one a thread in the scan
 constexpr uint32_t kCarry = 1u << 15;
-constexpr int kCarries = (int)(kSampleMaxV / kCarry);
+constexpr int kCarries = (int)(kSampleMaxV / kCarry) + 4;
 constexpr int kNone = -1;
 constexpr int kListed = 1024;  // tokens of one value that are listed
 
@@ -45,6 +45,7 @@ struct Keys {
     }
 };
 typedef short short2_t __attribute__((ext_vector_type(2)));
+typedef unsigned short ushort2_t __attribute__((ext_vector_type(2)));
 // The keys of two logits.
 __device__ __forceinline__ uint32_t two_keys(uint32_t w) {
     return w ^ (__builtin_bit_cast(uint32_t, __builtin_bit_cast(short2_t, w) >> 15) | 0x80008000u);
@@ -144,6 +145,17 @@ struct Row {
             v[e] = (i + 2 * e < V ? x[i + 2 * e] : low) | (i + 2 * e + 1 < V ? (uint32_t)x[i + 2 * e + 1] : low) << 16;
         return v;
     }
+    // Of N steps; a branch for all of them, so that the loads are in flight together.
+    template <int N>
+    __device__ __forceinline__ void load(int step, u32x4 (&v)[N]) const {
+        if (step + N <= steps && from + (step + N) * 512 <= V) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) v[i] = *reinterpret_cast<const u32x4_any*>(x + index(step + i));
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i) v[i] = load(step + i);
+        }
+    }
 };
 constexpr int kAtOnce = 4;  // steps whose loads are in flight together
 
@@ -162,71 +174,74 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(SampleArgs a) {
 
     uint32_t top = 0;  // the largest logit's key
     if (greedy) {
-        for (int step = 0; step < row.steps; step += kAtOnce) {
-            u32x4 v[kAtOnce];
+        // The least distance below +infinity's key, two logits at once: forbidden
+        // tokens' are larger than any that may be drawn.
+        ushort2_t least{0xFFFF, 0xFFFF};
+        for (int step = 0; step < row.steps; step += 2 * kAtOnce) {
+            u32x4 v[2 * kAtOnce];
+            row.load(step, v);
 #pragma unroll
-            for (int i = 0; i < kAtOnce; ++i) v[i] = row.load(step + i);
+            for (int i = 0; i < 2 * kAtOnce; ++i)
 #pragma unroll
-            for (int i = 0; i < kAtOnce; ++i)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    uint32_t k = two_keys(v[i][e]);
-                    const uint32_t lo = drawn(k & 0xFFFFu) ? k & 0xFFFFu : 0u, hi = drawn(k >> 16) ? k >> 16 : 0u;
-                    top = lo > top ? lo : top;
-                    top = hi > top ? hi : top;
-                }
+                for (int e = 0; e < 4; ++e)
+                    least = __builtin_elementwise_min(least, ushort2_t{K::kTop, K::kTop} - __builtin_bit_cast(ushort2_t, two_keys(v[i][e])));
         }
-        if (top == K::kZero - 1) top = K::kZero;
+        uint32_t down = least[0] < least[1] ? least[0] : least[1];
 #pragma unroll
         for (int off = 32; off > 0; off /= 2) {
-            const uint32_t o = __shfl_xor(top, off);
-            top = o > top ? o : top;
+            const uint32_t o = __shfl_xor(down, off);
+            down = o < down ? o : down;
         }
-        if (lane == 0) s.wave_top[wave] = top;
+        if (lane == 0) s.wave_top[wave] = down;
         if (tid == 0) s.found = 0;
         __syncthreads();
-        for (int i = 0; i < kWaves; ++i) top = s.wave_top[i] > top ? s.wave_top[i] : top;
+        for (int i = 0; i < kWaves; ++i) down = s.wave_top[i] < down ? s.wave_top[i] : down;
+        top = down <= K::kTop - K::kFirst ? K::kTop - down : 0u;
+        if (top == K::kZero - 1) top = K::kZero;
     } else {
+        u32x4 next[kAtOnce];  // the next steps' logits are on their way while these are counted
+        row.load(0, next);
         for (int i = tid; i < kKeys / 8; i += kThreads) reinterpret_cast<u32x4*>(s.counts)[i] = u32x4{0u, 0u, 0u, 0u};
         if (tid == 0) s.carries = 0, s.last = 0, s.found = 0, s.block = kBlocks;
         __syncthreads();
         // Count the row's values.
         for (int step = 0; step < row.steps; step += kAtOnce) {  // as often for each wave
-            // The one that fills a count's lower 15 bits takes them away again.
-            // Between two barriers there are at most 4 * 8 * kThreads = 2^15 others,
-            // so 16 bits hold them.
-            static_assert(kAtOnce * 8 * kThreads <= (int)kCarry, "counts of 16 bits");
-            if (step != 0) __syncthreads();
             u32x4 v[kAtOnce];
 #pragma unroll
-            for (int i = 0; i < kAtOnce; ++i) v[i] = row.load(step + i);
+            for (int i = 0; i < kAtOnce; ++i) v[i] = next[i];
+            row.load(step + kAtOnce, next);
+            if (step != 0) {
+                // 2^15 logits raise a count by as much at most: taken out of the
+                // counts that have reached it, the next ones fit too.
+                static_assert(kAtOnce * 8 * kThreads <= (int)kCarry, "counts of 16 bits");
+                __syncthreads();
+                for (int i = 0; i < 32; ++i) {
+                    const uint32_t word = 32 * tid + (i ^ (tid & 31)), n = s.counts[word];
+                    if ((n & 0x80008000u) == 0) continue;
+                    const uint32_t k = 2 * (32 * tid + i);
+                    s.counts[word] = n & 0x7FFF7FFFu;
+                    if (n & 0x8000u) s.carried[atomicAdd(&s.carries, 1)] = (uint16_t)k;
+                    if (n >> 31) s.carried[atomicAdd(&s.carries, 1)] = (uint16_t)(k + 1 == K::kZero - 1 ? K::kZero : k + 1);
+                }
+                __syncthreads();
+            }
 #pragma unroll
-            for (int i = 0; i < kAtOnce; ++i) {
-                uint32_t key[8], old[8];
+            for (int i = 0; i < kAtOnce; ++i)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const uint32_t k = two_keys(v[i][e]);
-                    key[2 * e] = k & 0xFFFFu;
-                    key[2 * e + 1] = k >> 16;
+                    const uint32_t k = two_keys(v[i][e]), lo = k & 0xFFFFu, hi = k >> 16;
+                    // Forbidden tokens may be most of a row: they are not counted.
+                    if (lo != K::kLow) atomicAdd(&s.counts[word_of(lo)], lo & 1 ? 0x10000u : 1u);
+                    if (hi != K::kLow) atomicAdd(&s.counts[word_of(hi)], hi & 1 ? 0x10000u : 1u);
                 }
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    old[e] = 0u;  // forbidden tokens may be most of a row: they are not counted
-                    if (key[e] != K::kLow) old[e] = atomicAdd(&s.counts[word_of(key[e])], 1u << (16 * (key[e] & 1))) >> (16 * (key[e] & 1)) & 0xFFFFu;
-                }
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    if (old[e] == kCarry - 1) {
-                        atomicSub(&s.counts[word_of(key[e])], kCarry << (16 * (key[e] & 1)));
-                        s.carried[atomicAdd(&s.carries, 1)] = (uint16_t)(key[e] == K::kZero - 1 ? K::kZero : key[e]);
-                    }
-            }
         }
         __syncthreads();
-        if (tid == 0) {  // both zeros are one value
-            const uint32_t negative = s.counts[word_of(K::kZero - 1)] >> 16;
-            s.counts[word_of(K::kZero - 1)] &= 0xFFFFu;
-            s.counts[word_of(K::kZero)] += negative;
+        if (tid == 0) {  // both zeros are one value; each may have 2^15 - 1, and 2^15 of the last steps
+            const uint32_t at = word_of(K::kZero), from = word_of(K::kZero - 1);
+            uint32_t both = (s.counts[from] >> 16) + (s.counts[at] & 0xFFFFu);
+            for (; both > 0xFFFFu; both -= kCarry) s.carried[s.carries++] = (uint16_t)K::kZero;
+            s.counts[from] &= 0xFFFFu;
+            s.counts[at] = (s.counts[at] & 0xFFFF0000u) | both;
         }
         __syncthreads();
     }
@@ -286,20 +301,20 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(SampleArgs a) {
         double own_w = 0.0;
         uint32_t own_n = 0, kept = 0;  // kept: tokens that min-p keeps
         if (any != 0) {
-            // From the block's first key on, or the row's largest logit's.
-            const uint32_t from = high < top ? high : top;
-            double w = weight_at(from);
             const double ratio = exp2_of(((double)K::value(high - 63) - (double)K::value(high - 62)) * per);
-            const bool lists = carries > 0;
+            const bool lists = carries > 0, sieve = least > 0.0;
+            // From the block's first key on, or the row's largest logit's.
+            const int skip = high > top ? (int)(high - top) : 0;
+            double w = weight_at(high - skip);
 #pragma unroll
             for (int i = 0; i < 64; ++i) {
                 if (i % 8 == 0) __builtin_amdgcn_sched_barrier(0);  // 128 registers a thread: no more at once
                 uint32_t n = i % 2 == 0 ? counts[i / 2] >> 16 : counts[i / 2] & 0xFFFFu;
                 if (lists) n += carried(high - i);
                 own_n += n;
-                own_w += (double)n * w;
-                kept += w >= least ? n : 0u;
-                if (high - i <= from) w *= ratio;
+                own_w = __builtin_fma((double)n, w, own_w);
+                if (sieve) kept += w >= least ? n : 0u;
+                w = i < skip ? w : w * ratio;
             }
         }
         // Sums over the blocks before each.
@@ -444,12 +459,11 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(SampleArgs a) {
     // Few of that value: list them, and take the one with `before` smaller ones.
     const bool listed = same <= kListed;
     uint32_t mine = 0;
-    for (int step = 0; step < row.steps; step += kAtOnce) {
-        u32x4 v[kAtOnce];
+    for (int step = 0; step < row.steps; step += 2 * kAtOnce) {
+        u32x4 v[2 * kAtOnce];
+        row.load(step, v);
 #pragma unroll
-        for (int i = 0; i < kAtOnce; ++i) v[i] = row.load(step + i);
-#pragma unroll
-        for (int i = 0; i < kAtOnce; ++i) {
+        for (int i = 0; i < 2 * kAtOnce; ++i) {
             uint32_t m = step + i < row.steps ? matches(v[i]) : 0u;
             mine += __builtin_popcount(m);
             for (; listed && m != 0; m &= m - 1) s.list[atomicAdd(&s.found, 1)] = row.index(step + i) + __builtin_ctz(m);
