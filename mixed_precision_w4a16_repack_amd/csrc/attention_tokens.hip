@@ -2,6 +2,8 @@
 // the paged key/value cache (prompts, chunks of them, trees of drafted tokens):
 //   s_t = scale * q . k_t,  o = sum_t exp(s_t - m) v_t / sum_t exp(s_t - m),
 // over the tokens t that a row sees, in one pass with a running reference m.
+#include <cmath>
+
 #include "attention_common.h"
 #include "device_common.h"
 #include "internal.h"
@@ -46,8 +48,8 @@ struct Blocks {
         return (int)(((int64_t)m * a.group + ROWS - 1) / ROWS);
     }
     static __device__ __forceinline__ Span span(const TokensArgs& a, int m, int n, int j) {
-        const uint32_t first = (uint32_t)j * ROWS, group = (uint32_t)a.group;  // rows are counted in 31 bits
-        const int i0 = (int)(first / group), to = (int)((first + ROWS - 1) / group), i1 = to < m ? to : m - 1;
+        const uint32_t first = (uint32_t)j * ROWS;  // rows are counted in 31 bits
+        const int i0 = a.token_of(first), to = a.token_of(first + ROWS - 1), i1 = to < m ? to : m - 1;
         Span s;
         const int64_t past = (int64_t)n - m;  // may be negative: new tokens that have no place see nothing
         const int64_t hi = a.tree ? n : past + i1 + 1;
@@ -154,8 +156,9 @@ struct Attend {
     u32x4 q[HT][NQ];
     float factor[HT];
     floatx4 o[HT][NO];
-    float m[HT], l[HT], c[HT], f[HT];
-    // Of each column: what it sees, tokens lo .. hi - 1 and 0 .. sk - 1, and tree bits from `past` on.
+    float r[HT], l[HT];
+    static constexpr float kFar = 100.0f;  // int8: sums of 2^31 probabilities of 2^kFar are within fp32
+        // Of each column: what it sees, tokens lo .. hi - 1 and 0 .. sk - 1, and tree bits from `past` on.
     int lo[HT], hi[HT];
     int64_t row;   // of the block's sequence
     int past, first, rows;  // tokens before the new ones (may be negative), the block's first row and the sequence's rows
@@ -178,10 +181,10 @@ struct Attend {
         int least_hi = 0x7FFFFFFF, most_lo = 0;
 #pragma unroll
         for (int h = 0; h < HT; ++h) {
-            const int r = row_at(h), i = (int)((uint32_t)r / (uint32_t)a.group), head = kv_head * a.group + r - i * a.group;
+            const int at_row = row_at(h), i = a.token_of(at_row), head = kv_head * a.group + at_row - i * a.group;
             lo[h] = 0;
             hi[h] = 0x7FFFFFFF;  // columns without a row do not count
-            if (r < rows) {
+            if (at_row < rows) {
                 int at = past + i, end = at + 1;
                 if (a.tree) {
                     int depth = 0;
@@ -198,12 +201,10 @@ struct Attend {
 #pragma unroll
             for (int x = 0; x < NQ; ++x) {
                 q[h][x] = u32x4{0u, 0u, 0u, 0u};
-                if (r < rows) q[h][x] = *reinterpret_cast<const u32x4_any*>(p + 32 * x);
+                if (at_row < rows) q[h][x] = *reinterpret_cast<const u32x4_any*>(p + 32 * x);
             }
-            m[h] = kLowest;
-            c[h] = kLowest;
+            r[h] = kLowest;
             l[h] = 0.0f;
-            f[h] = 1.0f;
 #pragma unroll
             for (int x = 0; x < NO; ++x) o[h][x] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
         }
@@ -301,10 +302,10 @@ struct Attend {
     // Which of the tile's 32 tokens column h sees.
     __device__ __forceinline__ uint32_t visible(int h, int at, int n) const {
         uint32_t seen = below(hi[h] - at) & (~below(lo[h] - at) | below((a.sinks < lo[h] ? a.sinks : lo[h]) - at));
-        const int r = row_at(h);
-        if (a.tree && r < rows && at + kTile > past) {
+        const int at_row = row_at(h);
+        if (a.tree && at_row < rows && at + kTile > past) {
             const int64_t bit = (int64_t)at - past;  // of the tile's first token
-            const uint64_t* words = a.tree + (row + (int)((uint32_t)r / (uint32_t)a.group)) * a.tree_ld;
+            const uint64_t* words = a.tree + (row + a.token_of(at_row)) * a.tree_ld;
             uint32_t bits = 0u;
             if (bit < 0) {
                 bits = (uint32_t)(words[0] << -bit);
@@ -431,59 +432,58 @@ struct Attend {
                 }
             }
         }
-        float peak[HT];
-        bool above = false;
-        float most_vs = 0.0f;
+        // The reference r of a column: its sums are relative to 2^r, which keeps
+        // the largest weight (probability, int8 times the value's scale) within the operand's range.
+        float more = 0.0f;  // int8: log2 of the largest scale of the lane's values
         if constexpr (kI8) {
+            float most_vs = 0.0f;
 #pragma unroll
             for (int j = 0; j < 8; ++j) most_vs = fmaxf(most_vs, vs[j / 4][j % 4]);
+            more = __builtin_amdgcn_logf(most_vs);
         }
+        float peak[HT];
+        bool above = false;
 #pragma unroll
         for (int h = 0; h < HT; ++h) {
             peak[h] = s[h][0][0];
 #pragma unroll
             for (int j = 1; j < 8; ++j) peak[h] = fmaxf(peak[h], s[h][j / 4][j % 4]);
             peak[h] *= factor[h];
-            above |= peak[h] > m[h] + Pr::kHeadroom;
-            if constexpr (kI8) above |= exp2_fast(peak[h] - m[h]) * (most_vs * f[h]) > 0x1p15f;  // no w is larger
+            above |= peak[h] + more > r[h] + (Pr::kBias + Pr::kHeadroom);
+            if constexpr (kI8) above |= peak[h] > r[h] + kFar;
         }
         if (same((int)(__builtin_amdgcn_ballot_w64(above) != 0)) != 0) {  // move the references: rare after the first tiles
 #pragma unroll
             for (int h = 0; h < HT; ++h) {
-                const float mn = column_max(fmaxf(m[h], peak[h]));
-                const float keep_l = exp2_fast(m[h] - mn);
-                float keep_o = keep_l;
+                // int8: no further below a score than kFar, however small the scales are.
+                float up = peak[h] - Pr::kBias;
                 if constexpr (kI8) {
                     float y = 0.0f;
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
-                        y = fmaxf(y, exp2_fast(__builtin_fmaf(s[h][j / 4][j % 4], factor[h], -mn)) * vs[j / 4][j % 4]);
-                    // f stays within fp32: c is at least mn - 113
-                    const float cn = fmaxf(fmaxf(c[h], mn + __builtin_amdgcn_logf(column_max(y))), mn - 113.0f);
-                    keep_o = exp2_fast(c[h] - cn);
-                    c[h] = cn;
-                    f[h] = exp2_fast(Pr::kBias - (cn - mn));
+                        y = fmaxf(y, exp2_fast(__builtin_fmaf(s[h][j / 4][j % 4], factor[h], -peak[h])) * vs[j / 4][j % 4]);
+                    up = fmaxf(peak[h] + __builtin_amdgcn_logf(y) - Pr::kBias, peak[h] - kFar);
                 }
-                m[h] = mn;
-                l[h] *= keep_l;
+                const float to = column_max(fmaxf(r[h], up)), keep = exp2_fast(r[h] - to);
+                r[h] = to;
+                l[h] *= keep;
 #pragma unroll
                 for (int i = 0; i < NO; ++i)
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) o[h][i][r] *= keep_o;
+                    for (int e = 0; e < 4; ++e) o[h][i][e] *= keep;
             }
         }
         floatx4 ahead[HT][2];
         products(next_keys, ahead);
 #pragma unroll
         for (int h = 0; h < HT; ++h) {
-            const float ref = kI8 ? m[h] : m[h] - Pr::kBias;
             float w[8];
             u32x4 p[NP];
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                w[j] = exp2_fast(__builtin_fmaf(s[h][j / 4][j % 4], factor[h], -ref));
+                w[j] = exp2_fast(__builtin_fmaf(s[h][j / 4][j % 4], factor[h], -r[h]));
                 l[h] += w[j];
-                if constexpr (kI8) w[j] *= vs[j / 4][j % 4] * f[h];
+                if constexpr (kI8) w[j] *= vs[j / 4][j % 4];
             }
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
@@ -510,14 +510,16 @@ struct Attend {
     }
 
     // Items [from, to) of the block's tiles, those of missing pages left out.
-    __device__ __forceinline__ void run(int64_t b, int kv_head, const Span& sp, int n, int from, int to) {
+    __device__ __forceinline__ void run(const Item& it, const Span& sp) {
+        const int64_t b = it.b;
+        const int kv_head = it.kv_head, n = it.n, to = it.upto;
         const int tiles_per_page = a.P / kTile;
         const int whole_shift = (tiles_per_page & (tiles_per_page - 1)) == 0 ? __builtin_ctz(tiles_per_page) : -1;
         // The tiles that are there, 64 items looked at at once: where each lies
         // (two words), its number in the page, its first token. Every wave writes
         // the same list and reads what it wrote.
         u32x4* list = reinterpret_cast<u32x4*>(lds + kStages * kRaw + kOperands);
-        int next_item = from, found = 0;
+        int next_item = it.from, found = 0;
         auto look = [&]() {
             const int item = next_item + lane, tile = sp.tile(item);
             int64_t page = -1;
@@ -556,6 +558,7 @@ struct Attend {
         // that takes tile i + kStages is tile i's own.
         constexpr int kAhead = kI8 ? kStages : kStages - 1;
         while (going && there < kAhead) going = more();
+        begin(it);  // the queries are on their way too
         if (there == 0) return;
         floatx4 s[HT][2];
         int third = 0;  // int8: the scales' place
@@ -622,27 +625,17 @@ struct Attend {
         }
     }
 
-    // The columns' sums, relative to m.
     __device__ __forceinline__ void finish() {
 #pragma unroll
-        for (int h = 0; h < HT; ++h) {
-            l[h] = column_sum(l[h]);
-            if constexpr (kI8) {
-                const float back = exp2_fast(c[h] - Pr::kBias - m[h]);
-#pragma unroll
-                for (int i = 0; i < NO; ++i)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) o[h][i][r] *= back;
-            }
-        }
+        for (int h = 0; h < HT; ++h) l[h] = column_sum(l[h]);
     }
     __device__ __forceinline__ void store_out(int kv_head) {
 #pragma unroll
         for (int h = 0; h < HT; ++h) {
-            const int r = row_at(h), t = (int)((uint32_t)r / (uint32_t)a.group);
-            if (r >= rows) continue;
+            const int at_row = row_at(h), t = a.token_of(at_row);
+            if (at_row >= rows) continue;
             const float inv = 1.0f / (l[h] == 0.0f ? 1.0f : l[h]);
-            uint16_t* out = a.out + (row + t) * a.o_ts + (int64_t)(kv_head * a.group + r - t * a.group) * a.o_hs + 4 * g;
+            uint16_t* out = a.out + (row + t) * a.o_ts + (int64_t)(kv_head * a.group + at_row - t * a.group) * a.o_hs + 4 * g;
 #pragma unroll
             for (int i = 0; i < NO; ++i) {
                 u32x2 v;
@@ -660,7 +653,7 @@ struct Attend {
         for (int h = 0; h < HT; ++h) {
             if (row_at(h) >= rows) continue;
             float* p = to + ((wave * HT + h) * 16 + col) * kStride;
-            if (g == 0) p[0] = m[h], p[1] = l[h];
+            if (g == 0) p[0] = r[h], p[1] = l[h];
 #pragma unroll
             for (int i = 0; i < NO; ++i) *reinterpret_cast<floatx4*>(p + 4 + 16 * i + 4 * g) = o[h][i];
         }
@@ -694,14 +687,16 @@ __device__ __forceinline__ int64_t costs(const TokensArgs& a, int64_t base, int 
 
 // The items of positions [pos, end) of the list of all blocks' tiles (sequence,
 // kv head, block; a block's first kHeadTiles positions are its start), at most
-// kItems of them; returns the position behind the last. `per`: positions of a workgroup.
+// kItems of them; returns the position behind the last. `per`: positions of a
+// workgroup; seq, unit: the first 64 sequences and their costs.
 template <class Bl>
-__device__ __forceinline__ int64_t find_items(const TokensArgs& a, int lane, int64_t pos, int64_t end, int64_t per, int wg, Item* items, int& found) {
+__device__ __forceinline__ int64_t find_items(const TokensArgs& a, int lane, int64_t pos, int64_t end, int64_t per, int wg, Sequence seq,
+                                              int64_t unit, Item* items, int& found) {
     found = 0;
     int64_t before = 0;
     for (int64_t base = 0; base < a.B && pos < end && found < kItems; base += 64) {
-        Sequence seq;
-        const int64_t unit = costs<Bl>(a, base, lane, seq), unit_to = wave_scan(unit);
+        if (a.B > 64) unit = costs<Bl>(a, base, lane, seq);
+        const int64_t unit_to = wave_scan(unit);
         for (uint64_t rest = __builtin_amdgcn_ballot_w64(unit > 0 && before + a.H * unit_to > pos); rest != 0 && pos < end && found < kItems;
              rest &= rest - 1) {
             const int at = __builtin_ctzll(rest);
@@ -714,7 +709,7 @@ __device__ __forceinline__ int64_t find_items(const TokensArgs& a, int lane, int
             const int64_t seq_begin = seq_end - a.H * of_unit;
             const int blocks = Bl::count(a, it.m);
             while (pos < end && pos < seq_end && found < kItems) {
-                it.kv_head = (int)((pos - seq_begin) / of_unit);
+                it.kv_head = divide(pos - seq_begin, of_unit);
                 int64_t begin = seq_begin + it.kv_head * of_unit;  // of the kv head, then of block j
                 int j = 0;
                 for (; j < blocks; j += 64) {  // the block that holds pos
@@ -736,7 +731,7 @@ __device__ __forceinline__ int64_t find_items(const TokensArgs& a, int lane, int
                     it.from = it.from > 0 ? it.from : 0;
                     it.upto = (int)(stop - begin) - kHeadTiles;
                     it.whole = it.from == 0 && stop == stop_at;
-                    it.parts = it.from == 0 && stop != stop_at ? (int)((stop_at - 1) / per) - wg + 1 : 0;
+                    it.parts = it.from == 0 && stop != stop_at ? divide(stop_at - 1, per) - wg + 1 : 0;
                     if (it.upto > 0 || stop == stop_at) {  // else its tiles begin in the next workgroup
                         if (threadIdx.x == 0) items[found] = it;
                         ++found;
@@ -761,15 +756,17 @@ __global__ __launch_bounds__(256, (Attend<DT, KIND, D, HT>::kPerCU)) void attent
     const int wgs = gridDim.x;
     // Workgroups are dealt to the 8 dies in turn: neighbours in the list of
     // blocks, which read the same keys, are put on the same one.
-    const int wg = wgs % 8 == 0 ? blockIdx.x % 8 * (wgs / 8) + blockIdx.x / 8 : blockIdx.x;
+    const int wg = blockIdx.x % 8 * (wgs / 8) + blockIdx.x / 8;
 
     int64_t all = 0;
+    Sequence seq;
+    int64_t unit = 0;
     for (int64_t base = 0; base < a.B; base += 64) {
-        Sequence seq;
-        all += read_lane(wave_scan(costs<Bl>(a, base, lane, seq)), 63);
+        unit = costs<Bl>(a, base, lane, seq);
+        all += read_lane(wave_scan(unit), 63);
     }
     all *= a.H;
-    int64_t per = (all + wgs - 1) / wgs;
+    int64_t per = (all + wgs - 1) >> __builtin_ctz(wgs);
     if (per < kLeastTiles + kHeadTiles) per = kLeastTiles + kHeadTiles;
     int64_t pos = wg * per;
     const int64_t end = pos + per < all ? pos + per : all;
@@ -779,7 +776,7 @@ __global__ __launch_bounds__(256, (Attend<DT, KIND, D, HT>::kPerCU)) void attent
     while (pos < end) {
         int found;
         __syncthreads();  // the items before these are read
-        pos = same(find_items<Bl>(a, lane, pos, end, per, wg, items, found));
+        pos = same(find_items<Bl>(a, lane, pos, end, per, wg, seq, unit, items, found));
         __syncthreads();
         found = same(found);
         if (found == 0) break;
@@ -787,10 +784,9 @@ __global__ __launch_bounds__(256, (Attend<DT, KIND, D, HT>::kPerCU)) void attent
             Item it = items[i];
             it = Item{same(it.b), same(it.row), same(it.m), same(it.n), same(it.kv_head), same(it.j), same(it.from), same(it.upto),
                       same(it.parts), same(it.whole)};
-            w.begin(it);
             Span sp = Bl::span(a, it.m, it.n, it.j);
             sp = Span{same(sp.lo), same(sp.hi), same(sp.sk), same(sp.head), same(sp.skip), same(sp.count)};
-            w.run(it.b, it.kv_head, sp, it.n, it.from, it.upto);
+            w.run(it, sp);
             w.finish();
             if (it.whole) {
                 w.store_out(it.kv_head);
@@ -829,7 +825,7 @@ __global__ __launch_bounds__(256) void attention_join_kernel(TokensArgs a) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) o[i] = o[i] * u + po[i] * v;
         }
-        const int i = (int)((uint32_t)(first + row) / (uint32_t)a.group);
+        const int i = a.token_of((uint32_t)(first + row));
         const int head = r.kv_head * a.group + (int)(first + row) - i * a.group;
         const float inv = 1.0f / (l == 0.0f ? 1.0f : l);
         u32x2 y;
@@ -902,6 +898,7 @@ size_t attention_tokens_workspace(const TokensArgs& a, int kind) {
 hipError_t launch_attention_tokens(TokensArgs a, int kind, int dtype, void* workspace, hipStream_t stream) {
     const Shape s = plan(a, kind);
     a.group = a.Hq / a.H;
+    a.one_by_group = std::nextafter(1.0 / a.group, 2.0);
     const int64_t most = a.width * a.P, all = ((int64_t)1 << 31) - 1;
     a.most = (int)(most < all ? most : all);
     a.reach = a.window > 0 ? a.window : (int64_t)1 << 32;

@@ -244,6 +244,9 @@ struct TokensArgs {
     // Set by launch_attention_tokens: Hq / H, the longest length the table
     // allows, the window as a number of tokens, the workspace's parts.
     int group = 0, most = 0;
+    double one_by_group = 0.0;  // rounded up
+    // row / group of a row below 2^31 (group below 2^20: the product is too large by less than 1 / group).
+    __device__ __forceinline__ int token_of(uint32_t row) const { return (int)((double)row * one_by_group); }
     int64_t reach = 0;
     void* records = nullptr;
     float* partials = nullptr;
