@@ -283,16 +283,19 @@ struct Attend {
     __device__ __forceinline__ const float* scales_at(int third) const {
         return reinterpret_cast<const float*>(lds + kStages * kRaw + 4 * kPart + third * 256);
     }
-    // int8: this wave's part of tile i as operands; half the waves turn keys, half values.
-    __device__ __forceinline__ void convert(int place, int i) {
+    // int8: this wave's part of a tile in the ring, and as operands of tile i; half the waves turn keys, half values.
+    __device__ __forceinline__ void read_codes(int place, u32x4 (&v)[kLoads]) const {
         const u32x4* from = reinterpret_cast<const u32x4*>(lds + place * kRaw) + wave * kLoads * 64 + lane;
-        const unsigned char* part = wave < kWaves / 2 ? keys_at(place, i) : values_at(place, i);
+#pragma unroll
+        for (int x = 0; x < kLoads; ++x) v[x] = from[64 * x];
+    }
+    __device__ __forceinline__ void convert(const u32x4 (&v)[kLoads], int i) {
+        const unsigned char* part = wave < kWaves / 2 ? keys_at(0, i) : values_at(0, i);
         u32x4* to = reinterpret_cast<u32x4*>(const_cast<unsigned char*>(part)) + wave % (kWaves / 2) * kLoads * 128 + lane;
 #pragma unroll
         for (int x = 0; x < kLoads; ++x) {
-            const u32x4 v = from[64 * x];
-            to[128 * x] = codes8_to_f16(v[0], v[1]);
-            to[128 * x + 64] = codes8_to_f16(v[2], v[3]);
+            to[128 * x] = codes8_to_f16(v[x][0], v[x][1]);
+            to[128 * x + 64] = codes8_to_f16(v[x][2], v[x][3]);
         }
     }
     __device__ __forceinline__ void copy_scales(int place, int third) {
@@ -358,26 +361,49 @@ struct Attend {
         }
     }
 
-    // A tile of tokens from `at` on, whose products with the queries s holds;
-    // whole: every column sees all of them. The next tile's products are made on
-    // the way, so that the matrix cores have work while the probabilities are formed.
-    __device__ __forceinline__ void work(floatx4 (&s)[HT][2], const unsigned char* next_keys, const unsigned char* operands,
-                                         const float* scales, int at, int n, bool whole) {
+    // int8: scores from a tile's products, and its values' scales.
+    __device__ __forceinline__ void apply_scales(const float* scales, floatx4 (&s)[HT][2], floatx4 (&vs)[2]) const {
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            const floatx4 ks = *reinterpret_cast<const floatx4*>(scales + 4 * g + 16 * t);
+            vs[t] = *reinterpret_cast<const floatx4*>(scales + 32 + 4 * g + 16 * t);
+#pragma unroll
+            for (int h = 0; h < HT; ++h)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[h][t][e] *= ks[e];
+        }
+    }
+    __device__ __forceinline__ float largest(const floatx4 (&s)[2]) const {
+        float x = s[0][0];
+#pragma unroll
+        for (int j = 1; j < 8; ++j) x = fmaxf(x, s[j / 4][j % 4]);
+        return x;
+    }
+    // Whether a score is so far above its column's reference r that this has to
+    // move. Sums are relative to 2^r, which keeps the largest weight (a probability,
+    // int8 times the value's scale) within the operand's range.
+    __device__ __forceinline__ int above(const floatx4 (&s)[HT][2], const floatx4 (&vs)[2]) const {
+        float more = 0.0f;  // int8: log2 of the largest scale of the lane's values
+        if constexpr (kI8) more = __builtin_amdgcn_logf(fmaxf(largest(vs), 0.0f));
+        bool is = false;
+#pragma unroll
+        for (int h = 0; h < HT; ++h) {
+            const float peak = largest(s[h]) * factor[h];
+            is |= peak + more > r[h] + (Pr::kBias + Pr::kHeadroom);
+            if constexpr (kI8) is |= peak > r[h] + kFar;
+        }
+        return __builtin_amdgcn_ballot_w64(is) != 0;
+    }
+
+    // A tile of tokens from `at` on, whose scores s holds (before the scale's
+    // factor), `move` above()'s answer; whole: every column sees all of them. The next
+    // tile's products and answer are made on the way, so that the matrix cores have work
+    // while the probabilities are formed, and nothing waits for the answer.
+    __device__ __forceinline__ void work(floatx4 (&s)[HT][2], floatx4 (&vs)[2], int& move, const unsigned char* next_keys,
+                                         const float* next_scales, const unsigned char* operands, int at, int n, bool whole) {
         u32x4 v[NO];
 #pragma unroll
         for (int i = 0; i < NO; ++i) v[i] = reinterpret_cast<const u32x4*>(operands)[64 * i + lane];
-        floatx4 vs[2];
-        if constexpr (kI8) {
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                const floatx4 ks = *reinterpret_cast<const floatx4*>(scales + 4 * g + 16 * t);
-                vs[t] = *reinterpret_cast<const floatx4*>(scales + 32 + 4 * g + 16 * t);
-#pragma unroll
-                for (int h = 0; h < HT; ++h)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) s[h][t][r] *= ks[r];
-            }
-        }
         uint32_t seen[HT];
         if (same((int)whole) == 0) {
             // Unseen scores are -infinity. An unseen value may be anything, and
@@ -432,37 +458,18 @@ struct Attend {
                 }
             }
         }
-        // The reference r of a column: its sums are relative to 2^r, which keeps
-        // the largest weight (probability, int8 times the value's scale) within the operand's range.
-        float more = 0.0f;  // int8: log2 of the largest scale of the lane's values
-        if constexpr (kI8) {
-            float most_vs = 0.0f;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) most_vs = fmaxf(most_vs, vs[j / 4][j % 4]);
-            more = __builtin_amdgcn_logf(most_vs);
-        }
-        float peak[HT];
-        bool above = false;
-#pragma unroll
-        for (int h = 0; h < HT; ++h) {
-            peak[h] = s[h][0][0];
-#pragma unroll
-            for (int j = 1; j < 8; ++j) peak[h] = fmaxf(peak[h], s[h][j / 4][j % 4]);
-            peak[h] *= factor[h];
-            above |= peak[h] + more > r[h] + (Pr::kBias + Pr::kHeadroom);
-            if constexpr (kI8) above |= peak[h] > r[h] + kFar;
-        }
-        if (same((int)(__builtin_amdgcn_ballot_w64(above) != 0)) != 0) {  // move the references: rare after the first tiles
+        move = above(s, vs);
+        if (same(move) != 0) {  // rare after the first tiles
 #pragma unroll
             for (int h = 0; h < HT; ++h) {
-                // int8: no further below a score than kFar, however small the scales are.
-                float up = peak[h] - Pr::kBias;
-                if constexpr (kI8) {
+                const float peak = largest(s[h]) * factor[h];
+                float up = peak - Pr::kBias;
+                if constexpr (kI8) {  // no further below a score than kFar, however small the scales are
                     float y = 0.0f;
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
-                        y = fmaxf(y, exp2_fast(__builtin_fmaf(s[h][j / 4][j % 4], factor[h], -peak[h])) * vs[j / 4][j % 4]);
-                    up = fmaxf(peak[h] + __builtin_amdgcn_logf(y) - Pr::kBias, peak[h] - kFar);
+                        y = fmaxf(y, exp2_fast(__builtin_fmaf(s[h][j / 4][j % 4], factor[h], -peak)) * vs[j / 4][j % 4]);
+                    up = fmaxf(peak + __builtin_amdgcn_logf(y) - Pr::kBias, peak - kFar);
                 }
                 const float to = column_max(fmaxf(r[h], up)), keep = exp2_fast(r[h] - to);
                 r[h] = to;
@@ -501,6 +508,7 @@ struct Attend {
         for (int h = 0; h < HT; ++h)
 #pragma unroll
             for (int t = 0; t < 2; ++t) s[h][t] = ahead[h][t];
+        if constexpr (kI8) apply_scales(next_scales, s, vs);
         // Products take turns with the probabilities' instructions: the keys'
         // products with the first column tile's, the values' with the next one's.
         __builtin_amdgcn_sched_group_barrier(kLdsReads, 4, 0);
@@ -540,24 +548,24 @@ struct Attend {
         // The ring: tile i of the list lies in place i % kStages.
         int there = 0, done = 0;  // tiles requested and worked on
         int fill = 0, take = 0;   // their places
-        auto more = [&]() -> bool {  // requests the next tile, if there is one
+        auto list_more = [&]() {  // so that an entry is there for the next request, if any is left
             while (there == found && next_item < to) look();
-            if (there == found) return false;
-            const u32x4 e = list[there % kListed];
+        };
+        auto request_listed = [&](const u32x4& e) {  // e: list[there % kListed]
             request((uint64_t)(uint32_t)same((int)e[1]) << 32 | (uint32_t)same((int)e[0]), same((int)e[2]), fill);
             fill = fill + 1 < kStages ? fill + 1 : 0;
             ++there;
-            return true;
+            list_more();
         };
+        list_more();
         stage_barrier();  // the ring is free
-        bool going = true;
         // Tile i is worked on when its values and tile i + 1's keys are there.
         // 16 bits: tiles up to i + kStages - 2 are on their way, and when all waves
         // have begun tile i, tile i - 1's place takes tile i + kStages - 1. int8: up to
         // i + kStages - 1; keys become operands two tiles ahead, values one, and the place
         // that takes tile i + kStages is tile i's own.
         constexpr int kAhead = kI8 ? kStages : kStages - 1;
-        while (going && there < kAhead) going = more();
+        while (there < found && there < kAhead) request_listed(list[there % kListed]);
         begin(it);  // the queries are on their way too
         if (there == 0) return;
         floatx4 s[HT][2];
@@ -571,10 +579,15 @@ struct Attend {
         if constexpr (kI8) {
             wait_for(there - 2 < 0 ? 0 : there - 2);
             stage_barrier();
-            convert(0, 0);
+            u32x4 codes[kLoads];
+            read_codes(0, codes);
+            convert(codes, 0);
             copy_scales(0, 0);
             if (there > 1) {
-                if (wave < kWaves / 2) convert(1, 1);
+                if (wave < kWaves / 2) {
+                    read_codes(1, codes);
+                    convert(codes, 1);
+                }
                 copy_scales(1, 1);
             }
             stage_barrier();
@@ -582,32 +595,36 @@ struct Attend {
             wait_for(there - 1);
             stage_barrier();
         }
-        if (busy) products(keys_at(0, 0), s);
+        floatx4 vs[2];
+        int move = 0;
+        if (busy) {
+            products(keys_at(0, 0), s);
+            if constexpr (kI8) apply_scales(scales_at(0), s, vs);
+            move = above(s, vs);
+        }
         // The next tile to work on: its first token, its place and the next one's.
-        int t = 0, place = 0, next = 0, third_at = 0;
+        int t = 0, place = 0, next = 0;
         auto advance = [&]() -> bool {
             if (done == there) return false;
-            t = same((int)reinterpret_cast<const uint32_t*>(list)[done % kListed * 4 + 3]);
+            // Read before the wait, needed behind it.
+            const u32x4 e = list[there % kListed];
+            const uint32_t first_token = reinterpret_cast<const uint32_t*>(list)[done % kListed * 4 + 3];
             place = take;
             next = place_of(take + 1);
-            third_at = third;
+            const int left = there - done;  // this one, the ones that are there and the ones on their way
+            wait_for(left - (kI8 ? 3 : 2) < 0 ? 0 : left - (kI8 ? 3 : 2));
+            stage_barrier();
+            u32x4 codes[kLoads];
+            // int8: into places that were read for tile done - 1, or before.
+            const bool turns = kI8 && left > (wave < kWaves / 2 ? 2 : 1);
+            const int from = place_of(take + (wave < kWaves / 2 ? 2 : 1));
+            if (kI8 && turns) read_codes(from, codes);
+            t = same((int)first_token);
+            if (there < found) request_listed(e);
             if constexpr (kI8) {
-                const int left = there - done;  // this one, the ones that are there and the ones on their way
-                wait_for(left - 3 < 0 ? 0 : left - 3);
-                stage_barrier();
-                if (going) going = more();
-                // Into places that were read for tile done - 1, or before.
-                if (wave < kWaves / 2) {
-                    if (left > 2) convert(place_of(take + 2), done + 2);
-                } else {
-                    if (left > 1) convert(next, done + 1);
-                }
+                if (turns) convert(codes, done + (wave < kWaves / 2 ? 2 : 1));
                 if (left > 2) copy_scales(place_of(take + 2), third >= 1 ? third - 1 : 2);
-                third = third < 2 ? third + 1 : 0;
-            } else {
-                wait_for(there - done - 2 < 0 ? 0 : there - done - 2);
-                stage_barrier();
-                if (going) going = more();
+                third = third < 2 ? third + 1 : 0;  // the next tile's
             }
             take = next;
             ++done;
@@ -620,7 +637,7 @@ struct Attend {
             return;
         }
         while (have) {
-            work(s, keys_at(next, done), values_at(place, done - 1), scales_at(third_at), t, n, whole());
+            work(s, vs, move, keys_at(next, done), scales_at(third), values_at(place, done - 1), t, n, whole());
             have = advance();
         }
     }
