@@ -16,7 +16,7 @@ namespace {
 constexpr int kWaves = 4;
 constexpr int kTile = 32;       // tokens
 constexpr int kHeadTiles = 6;   // a block's start and end cost about as much as this many tiles
-constexpr int kLeastTiles = 8;  // a workgroup's least share: a split costs a join
+constexpr int kLeastTiles = 3;  // a workgroup's least share: a split costs a join
 
 // What the rows of a block see together: tokens lo .. hi - 1 and 0 .. sk - 1
 // (sk <= lo), in `count` tiles: `head` of them before the window's, which lie
@@ -347,20 +347,6 @@ struct Attend {
         return __builtin_bit_cast(uint32_t, x >> 15);
     }
 
-    // Asks for an order of instructions: a column tile's probabilities (8 times
-    // an exponential and its share of the others) between MFMAS matrix products each.
-    static constexpr int kVector = 0x002, kMatrix = 0x008, kLdsReads = 0x100, kExp = 0x400;
-    template <int MFMAS>
-    static __device__ __forceinline__ void take_turns() {
-#pragma unroll
-        for (int x = 0; x < 8; ++x) {
-            __builtin_amdgcn_sched_group_barrier(kLdsReads, 1, 0);
-            __builtin_amdgcn_sched_group_barrier(kMatrix, MFMAS, 0);
-            __builtin_amdgcn_sched_group_barrier(kVector, 5, 0);
-            __builtin_amdgcn_sched_group_barrier(kExp, 1, 0);
-        }
-    }
-
     // int8: scores from a tile's products, and its values' scales.
     __device__ __forceinline__ void apply_scales(const float* scales, floatx4 (&s)[HT][2], floatx4 (&vs)[2]) const {
 #pragma unroll
@@ -480,41 +466,53 @@ struct Attend {
                     for (int e = 0; e < 4; ++e) o[h][i][e] *= keep;
             }
         }
+        // The next tile's products take turns with the first column tile's
+        // probabilities, and a column tile's sums with the next one's.
         floatx4 ahead[HT][2];
-        products(next_keys, ahead);
-#pragma unroll
-        for (int h = 0; h < HT; ++h) {
-            float w[8];
-            u32x4 p[NP];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                w[j] = exp2_fast(__builtin_fmaf(s[h][j / 4][j % 4], factor[h], -r[h]));
-                l[h] += w[j];
-                if constexpr (kI8) w[j] *= vs[j / 4][j % 4];
-            }
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
+        u32x4 p[HT][NP];
+        float w[2];
+        auto probability = [&](int h, int j) {
+            w[j % 2] = exp2_fast(__builtin_fmaf(s[h][j / 4][j % 4], factor[h], -r[h]));
+            l[h] += w[j % 2];
+            if constexpr (kI8) w[j % 2] *= vs[j / 4][j % 4];
+            if (j % 2 == 1) {
                 uint32_t parts[NP];
-                split_pair<PDT, NP>(w[2 * x], w[2 * x + 1], parts);
+                split_pair<PDT, NP>(w[0], w[1], parts);
 #pragma unroll
-                for (int i = 0; i < NP; ++i) p[i][x] = parts[i];
+                for (int i = 0; i < NP; ++i) p[h][i][j / 2] = parts[i];
             }
+        };
+        constexpr int kKeys = 2 * NQ, kInHand = 4;
+        const u32x4* tile = reinterpret_cast<const u32x4*>(next_keys) + lane;
+        auto key_at = [&](int i) { return tile[(i % 2 * NQ + i / 2) * 64]; };
+        u32x4 k[kInHand];
 #pragma unroll
-            for (int j = 0; j < NP; ++j)
+        for (int i = 0; i < kInHand; ++i) k[i] = key_at(i);
 #pragma unroll
-                for (int i = 0; i < NO; ++i) o[h][i] = mfma16x16x32<PDT>(v[i], p[j], o[h][i]);
+        for (int i = 0; i < kKeys; ++i) {
+#pragma unroll
+            for (int h = 0; h < HT; ++h)
+                ahead[h][i % 2] = mfma16x16x32<PDT>(k[i % kInHand], q[h][i / 2], i < 2 ? floatx4{0.0f, 0.0f, 0.0f, 0.0f} : ahead[h][i % 2]);
+            if (i + kInHand < kKeys) k[i % kInHand] = key_at(i + kInHand);
+#pragma unroll
+            for (int j = i * 8 / kKeys; j < (i + 1) * 8 / kKeys; ++j) probability(0, j);
+            __builtin_amdgcn_sched_barrier(0);
         }
+#pragma unroll
+        for (int h = 0; h < HT; ++h)
+#pragma unroll
+            for (int x = 0; x < 8; ++x) {
+#pragma unroll
+                for (int i = x * NO * NP / 8; i < (x + 1) * NO * NP / 8; ++i)
+                    o[h][i % NO] = mfma16x16x32<PDT>(v[i % NO], p[h][i / NO], o[h][i % NO]);
+                if (h + 1 < HT) probability(h + 1, x);
+                __builtin_amdgcn_sched_barrier(0);
+            }
 #pragma unroll
         for (int h = 0; h < HT; ++h)
 #pragma unroll
             for (int t = 0; t < 2; ++t) s[h][t] = ahead[h][t];
         if constexpr (kI8) apply_scales(next_scales, s, vs);
-        // Products take turns with the probabilities' instructions: the keys'
-        // products with the first column tile's, the values' with the next one's.
-        __builtin_amdgcn_sched_group_barrier(kLdsReads, 4, 0);
-        take_turns<(2 * NQ * HT + 7) / 8>();
-        if constexpr (HT == 2) take_turns<(NO * NP + 7) / 8>();
-        __builtin_amdgcn_sched_group_barrier(kMatrix, NO * NP, 0);
     }
 
     // Items [from, to) of the block's tiles, those of missing pages left out.
