@@ -143,9 +143,9 @@ struct Attend {
     // Workgroups that share a CU, and tiles in the ring that loads fill.
     static constexpr int kListed = 128;  // tiles in hand: 64 found at once, and a few not yet worked on
     static constexpr int kPerCU = D <= 128 || (D == 192 && HT == 1 && !kI8) ? 2 : 1;
-    static constexpr int kFree = (kPerCU == 2 ? 80 : 160) * 1024 - kItems * (int)sizeof(Item) - kListed * 16 - kOperands;
+    static constexpr int kFree = (kPerCU == 2 ? 80 : 160) * 1024 - kItems * (int)sizeof(Item) - (kListed + 1) * 16 - kOperands;
     static constexpr int kStages = kFree / kRaw < 4 ? kFree / kRaw : 4;
-    static constexpr int kBytes = kStages * kRaw + kOperands + kListed * 16 + kItems * (int)sizeof(Item);
+    static constexpr int kBytes = kStages * kRaw + kOperands + (kListed + 1) * 16 + kItems * (int)sizeof(Item);
     static_assert(kStages >= 3, "a tile is loaded while others are worked on");
     using L = KvPlace<KIND>;
     using Pr = Prob<kF16P>;
@@ -305,20 +305,20 @@ struct Attend {
     // Which of the tile's 32 tokens column h sees.
     __device__ __forceinline__ uint32_t visible(int h, int at, int n) const {
         uint32_t seen = below(hi[h] - at) & (~below(lo[h] - at) | below((a.sinks < lo[h] ? a.sinks : lo[h]) - at));
-        const int at_row = row_at(h);
-        if (a.tree && at_row < rows && at + kTile > past) {
+        if (same((int)(a.tree != nullptr && at + (int64_t)kTile > past)) != 0) {  // no branch that lanes take differently
+            const int at_row = row_at(h);
             const int64_t bit = (int64_t)at - past;  // of the tile's first token
-            const uint64_t* words = a.tree + (row + a.token_of(at_row)) * a.tree_ld;
+            const uint64_t* words = a.tree + (row + a.token_of(at_row < rows ? at_row : rows - 1)) * a.tree_ld;
             uint32_t bits = 0u;
-            if (bit < 0) {
+            if (same((int)(bit < 0)) != 0) {
                 bits = (uint32_t)(words[0] << -bit);
-            } else if (bit < 64 * (int64_t)a.tree_words) {
+            } else if (same((int)(bit < 64 * (int64_t)a.tree_words)) != 0) {
                 const int w = (int)(bit >> 6), by = (int)(bit & 63);
-                uint64_t v = words[w] >> by;
-                if (by > 32 && w + 1 < a.tree_words) v |= words[w + 1] << (64 - by);
-                bits = (uint32_t)v;
+                const int next = w + 1 < a.tree_words ? w + 1 : w;
+                const uint64_t more = next > w && by > 32 ? words[next] << (64 - by) : 0u;
+                bits = (uint32_t)(words[w] >> by | more);
             }
-            seen |= bits & below(n - at);
+            seen |= at_row < rows ? bits & below(n - at) : 0u;
         }
         return seen;
     }
@@ -365,27 +365,27 @@ struct Attend {
         for (int j = 1; j < 8; ++j) x = fmaxf(x, s[j / 4][j % 4]);
         return x;
     }
-    // Whether a score is so far above its column's reference r that this has to
+    // Above 0: a score is so far above its column's reference r that this has to
     // move. Sums are relative to 2^r, which keeps the largest weight (a probability,
     // int8 times the value's scale) within the operand's range.
-    __device__ __forceinline__ int above(const floatx4 (&s)[HT][2], const floatx4 (&vs)[2]) const {
+    __device__ __forceinline__ float above(const floatx4 (&s)[HT][2], const floatx4 (&vs)[2]) const {
         float more = 0.0f;  // int8: log2 of the largest scale of the lane's values
         if constexpr (kI8) more = __builtin_amdgcn_logf(fmaxf(largest(vs), 0.0f));
-        bool is = false;
+        float by = kLowest;
 #pragma unroll
         for (int h = 0; h < HT; ++h) {
             const float peak = largest(s[h]) * factor[h];
-            is |= peak + more > r[h] + (Pr::kBias + Pr::kHeadroom);
-            if constexpr (kI8) is |= peak > r[h] + kFar;
+            by = fmaxf(by, peak + more - (r[h] + (Pr::kBias + Pr::kHeadroom)));
+            if constexpr (kI8) by = fmaxf(by, peak - (r[h] + kFar));
         }
-        return __builtin_amdgcn_ballot_w64(is) != 0;
+        return by;
     }
 
     // A tile of tokens from `at` on, whose scores s holds (before the scale's
-    // factor), `move` above()'s answer; whole: every column sees all of them. The next
+    // factor), `over` above()'s answer; whole: every column sees all of them. The next
     // tile's products and answer are made on the way, so that the matrix cores have work
     // while the probabilities are formed, and nothing waits for the answer.
-    __device__ __forceinline__ void work(floatx4 (&s)[HT][2], floatx4 (&vs)[2], int& move, const unsigned char* next_keys,
+    __device__ __forceinline__ void work(floatx4 (&s)[HT][2], floatx4 (&vs)[2], float& over, const unsigned char* next_keys,
                                          const float* next_scales, const unsigned char* operands, int at, int n, bool whole) {
         u32x4 v[NO];
 #pragma unroll
@@ -413,7 +413,10 @@ struct Attend {
             } else {
                 uint32_t all = ~0u;
 #pragma unroll
-                for (int i = 0; i < NO; ++i) all &= finite(v[i][0]) & finite(v[i][1]) & finite(v[i][2]) & finite(v[i][3]);
+                for (int i = 0; i < NO; ++i) {
+                    const u32x4 x = v[i];
+                    all &= finite(x[0]) & finite(x[1]) & finite(x[2]) & finite(x[3]);
+                }
                 if (same((int)(__builtin_amdgcn_ballot_w64(all != ~0u) != 0)) != 0) {
                     // Values that are not finite are taken out of the product, and the
                     // columns that see one become NaN there, and stay so.
@@ -427,13 +430,9 @@ struct Attend {
 #pragma unroll
                     for (int i = 0; i < NO; ++i) {
                         __builtin_amdgcn_sched_barrier(0);  // one after the other: this is rare, and its registers are everybody's
-                        u32x4 is;
-#pragma unroll
-                        for (int x = 0; x < 4; ++x) {
-                            const uint32_t keep = finite(v[i][x]);
-                            v[i][x] &= keep;
-                            is[x] = ~keep & kOne;
-                        }
+                        const u32x4 was = v[i], keep{finite(was[0]), finite(was[1]), finite(was[2]), finite(was[3])};
+                        const u32x4 is = ~keep & kOne;
+                        v[i] = was & keep;
 #pragma unroll
                         for (int h = 0; h < HT; ++h) {
                             const floatx4 hits = mfma16x16x32<PDT>(is, ones[h], floatx4{0.0f, 0.0f, 0.0f, 0.0f});
@@ -443,9 +442,9 @@ struct Attend {
                     }
                 }
             }
+            over = above(s, vs);
         }
-        move = above(s, vs);
-        if (same(move) != 0) {  // rare after the first tiles
+        if (same((int)(__builtin_amdgcn_ballot_w64(over > 0.0f) != 0)) != 0) {  // rare after the first tiles
 #pragma unroll
             for (int h = 0; h < HT; ++h) {
                 const float peak = largest(s[h]) * factor[h];
@@ -483,6 +482,7 @@ struct Attend {
             }
         };
         constexpr int kKeys = 2 * NQ, kInHand = 4;
+        constexpr int kShare = (8 + kKeys - 1) / kKeys, kSums = (NO * NP + 7) / 8;  // of a turn
         const u32x4* tile = reinterpret_cast<const u32x4*>(next_keys) + lane;
         auto key_at = [&](int i) { return tile[(i % 2 * NQ + i / 2) * 64]; };
         u32x4 k[kInHand];
@@ -495,7 +495,8 @@ struct Attend {
                 ahead[h][i % 2] = mfma16x16x32<PDT>(k[i % kInHand], q[h][i / 2], i < 2 ? floatx4{0.0f, 0.0f, 0.0f, 0.0f} : ahead[h][i % 2]);
             if (i + kInHand < kKeys) k[i % kInHand] = key_at(i + kInHand);
 #pragma unroll
-            for (int j = i * 8 / kKeys; j < (i + 1) * 8 / kKeys; ++j) probability(0, j);
+            for (int j = 0; j < kShare; ++j)
+                if (i * kShare + j < 8) probability(0, i * kShare + j);
             __builtin_amdgcn_sched_barrier(0);
         }
 #pragma unroll
@@ -503,16 +504,21 @@ struct Attend {
 #pragma unroll
             for (int x = 0; x < 8; ++x) {
 #pragma unroll
-                for (int i = x * NO * NP / 8; i < (x + 1) * NO * NP / 8; ++i)
-                    o[h][i % NO] = mfma16x16x32<PDT>(v[i % NO], p[h][i / NO], o[h][i % NO]);
+                for (int y = 0; y < kSums; ++y) {
+                    const int i = x * kSums + y;
+                    if (i < NO * NP) o[h][i % NO] = mfma16x16x32<PDT>(v[i % NO], p[h][i / NO], o[h][i % NO]);
+                }
                 if (h + 1 < HT) probability(h + 1, x);
-                __builtin_amdgcn_sched_barrier(0);
+                else if (x == 0) {
+#pragma unroll
+                    for (int y = 0; y < HT; ++y)
+#pragma unroll
+                        for (int t = 0; t < 2; ++t) s[y][t] = ahead[y][t];
+                    if constexpr (kI8) apply_scales(next_scales, s, vs);
+                    over = above(s, vs);
+                }
+                if (h + 1 < HT) __builtin_amdgcn_sched_barrier(0);
             }
-#pragma unroll
-        for (int h = 0; h < HT; ++h)
-#pragma unroll
-            for (int t = 0; t < 2; ++t) s[h][t] = ahead[h][t];
-        if constexpr (kI8) apply_scales(next_scales, s, vs);
     }
 
     // Items [from, to) of the block's tiles, those of missing pages left out.
@@ -527,19 +533,15 @@ struct Attend {
         u32x4* list = reinterpret_cast<u32x4*>(lds + kStages * kRaw + kOperands);
         int next_item = it.from, found = 0;
         auto look = [&]() {
-            const int item = next_item + lane, tile = sp.tile(item);
-            int64_t page = -1;
-            int sub = 0;
-            if (item < to) {
-                const int i = whole_shift >= 0 ? tile >> whole_shift : tile / tiles_per_page;
-                page = a.table[b * a.table_ld + i];
-                sub = tile - i * tiles_per_page;
-            }
-            const bool ok = page >= 0 && page < a.pages;
+            // No branch that lanes take differently: one here makes the compiler keep two copies of the sums.
+            const int item = next_item + lane, tile = sp.tile(item < to ? item : to - 1);
+            const int i = whole_shift >= 0 ? tile >> whole_shift : tile / tiles_per_page, sub = tile - i * tiles_per_page;
+            const int64_t page = a.table[b * a.table_ld + i];
+            const bool ok = item < to && page >= 0 && page < a.pages;
             const uint64_t mask = __builtin_amdgcn_ballot_w64(ok);
             const int at = found + (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0u));
             const uint64_t place = reinterpret_cast<uint64_t>(a.cache) + (uint64_t)((page * a.H + kv_head) * L::record_bytes(D, a.P));
-            if (ok) list[at % kListed] = u32x4{(uint32_t)place, (uint32_t)(place >> 32), (uint32_t)sub, (uint32_t)tile * kTile};
+            list[ok ? at % kListed : kListed] = u32x4{(uint32_t)place, (uint32_t)(place >> 32), (uint32_t)sub, (uint32_t)tile * kTile};
             found = same(found + __builtin_popcountll(mask));
             next_item += 64;
         };
@@ -594,11 +596,11 @@ struct Attend {
             stage_barrier();
         }
         floatx4 vs[2];
-        int move = 0;
+        float over = 0.0f;
         if (busy) {
             products(keys_at(0, 0), s);
             if constexpr (kI8) apply_scales(scales_at(0), s, vs);
-            move = above(s, vs);
+            over = above(s, vs);
         }
         // The next tile to work on: its first token, its place and the next one's.
         int t = 0, place = 0, next = 0;
@@ -635,7 +637,7 @@ struct Attend {
             return;
         }
         while (have) {
-            work(s, vs, move, keys_at(next, done), scales_at(third), values_at(place, done - 1), t, n, whole());
+            work(s, vs, over, keys_at(next, done), scales_at(third), values_at(place, done - 1), t, n, whole());
             have = advance();
         }
     }
