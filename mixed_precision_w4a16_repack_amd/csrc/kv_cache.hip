@@ -421,7 +421,9 @@ __global__ __launch_bounds__(256) void kv_append_rows_kernel(KvAppendArgs a) {
 template <int DT, int KIND, int D>
 __global__ __launch_bounds__(2 * D) void kv_append_tile_kernel(KvAppendArgs a) {
     using L = KvPlace<KIND>;
-    constexpr int kParts = D / 64;  // waves that share a token's row
+    // Lanes side by side hold a token's row, so that loads and stores are whole
+    // lines; with 192 elements, 4 of them in each of three waves.
+    constexpr int kWide = D == 192 ? 4 : D / 16, kParts = D / 16 / kWide;
     __shared__ Coder s_code[32];
     __shared__ uint32_t s_top[2][kParts][32];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -443,7 +445,7 @@ __global__ __launch_bounds__(2 * D) void kv_append_tile_kernel(KvAppendArgs a) {
     const int64_t t0 = (int64_t)g * 32;
     const Group grp(a, t0, 0, record);
     const int part = wave % kParts;
-    const int j = wave / kParts * 16 + lane % 16, pp = 4 * part + lane / 16;
+    const int j = wave / kParts * (64 / kWide) + lane / kWide, pp = kWide * part + lane % kWide;
     const bool in = j < grp.n, turned = 8 * pp < a.pairs, apart = turned && !a.neighbours;
     const int64_t rec = grp.rec_of(j), tok = t0 + j;
     const int t = grp.t_of(j);
@@ -506,10 +508,11 @@ __global__ __launch_bounds__(2 * D) void kv_append_tile_kernel(KvAppendArgs a) {
             uint32_t top = 0u;
 #pragma unroll
             for (int i = 0; i < 16; ++i) top = larger(top, __builtin_bit_cast(uint32_t, x[i / 8][i % 8]) & 0x7FFFFFFFu);
-            top = lanes_top(top, 16);
+#pragma unroll
+            for (int off = 1; off < kWide; off *= 2) top = larger(top, __shfl_xor(top, off));
             if constexpr (kParts > 1) {  // two buffers: one barrier a head
                 uint32_t(&all)[kParts][32] = s_top[head & 1];
-                if (lane < 16) all[part][j] = top;
+                if (lane % kWide == 0) all[part][j] = top;
                 __syncthreads();
 #pragma unroll
                 for (int p = 0; p < kParts; ++p) top = larger(top, all[p][j]);
