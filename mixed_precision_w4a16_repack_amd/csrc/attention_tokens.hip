@@ -832,15 +832,33 @@ __global__ __launch_bounds__(256) void attention_join_kernel(TokensArgs a) {
         const int64_t at = (int64_t)row * A::kStride;
         float m = begun[at], l = begun[at + 1];
         floatx4 o = *reinterpret_cast<const floatx4*>(begun + at + 4 + d);
-        for (int p = 0; p + 1 < r.parts; ++p) {
-            const float* x = next + 2 * p * A::kPartial + at;
-            const float pm = x[0], pl = x[1];
-            const floatx4 po = *reinterpret_cast<const floatx4*>(x + 4 + d);
-            const float to = fmaxf(m, pm), u = exp2_fast(m - to), v = exp2_fast(pm - to);
-            m = to;
-            l = l * u + pl * v;
+        constexpr int kAtOnce = 4;  // parts whose loads are on their way together
+        for (int p = 0; p + 1 < r.parts; p += kAtOnce) {
+            float pm[kAtOnce], pl[kAtOnce], to = m;
+            floatx4 po[kAtOnce];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) o[i] = o[i] * u + po[i] * v;
+            for (int y = 0; y < kAtOnce; ++y) {
+                const bool is = p + y + 1 < r.parts;
+                const float* x = next + 2 * (is ? p + y : p) * A::kPartial + at;
+                pm[y] = is ? x[0] : kLowest;
+                pl[y] = is ? x[1] : 0.0f;
+                po[y] = *reinterpret_cast<const floatx4*>(x + 4 + d);
+                if (!is) po[y] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+            }
+#pragma unroll
+            for (int y = 0; y < kAtOnce; ++y) to = fmaxf(to, pm[y]);
+            const float u = exp2_fast(m - to);
+            m = to;
+            l *= u;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[i] *= u;
+#pragma unroll
+            for (int y = 0; y < kAtOnce; ++y) {
+                const float v = exp2_fast(pm[y] - to);
+                l += pl[y] * v;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) o[i] += po[y][i] * v;
+            }
         }
         const int i = a.token_of((uint32_t)(first + row));
         const int head = r.kv_head * a.group + (int)(first + row) - i * a.group;
@@ -899,7 +917,7 @@ hipError_t launch(const TokensArgs& a, const Shape& s, hipStream_t stream) {
         hipLaunchKernelGGL((attention_tokens_kernel<DT, KIND, D, HT>), dim3((unsigned)s.wgs), dim3(256), lds, stream, a);
         e = hipGetLastError();
         if (e != hipSuccess) return;
-        hipLaunchKernelGGL((attention_join_kernel<DT, KIND, D, HT>), dim3((unsigned)s.wgs, 4), dim3(256), 0, stream, a);
+        hipLaunchKernelGGL((attention_join_kernel<DT, KIND, D, HT>), dim3((unsigned)s.wgs, 8), dim3(256), 0, stream, a);
         e = hipGetLastError();
     });
     return e;
