@@ -387,6 +387,7 @@ struct Attend {
     // while the probabilities are formed, and nothing waits for the answer.
     __device__ __forceinline__ void work(floatx4 (&s)[HT][2], floatx4 (&vs)[2], float& over, const unsigned char* next_keys,
                                          const float* next_scales, const unsigned char* operands, int at, int n, bool whole) {
+        __builtin_amdgcn_s_setprio(0);
         u32x4 v[NO];
 #pragma unroll
         for (int i = 0; i < NO; ++i) v[i] = reinterpret_cast<const u32x4*>(operands)[64 * i + lane];
@@ -604,7 +605,10 @@ struct Attend {
         }
         // The next tile to work on: its first token, its place and the next one's.
         int t = 0, place = 0, next = 0;
+        // A wave between two tiles goes before the CU's others, which the next barrier
+        // or its next loads wait for (3 % of the time of prompts, 4 % of long int8 ones).
         auto advance = [&]() -> bool {
+            __builtin_amdgcn_s_setprio(3);
             if (done == there) return false;
             // Read before the wait, needed behind it.
             const u32x4 e = list[there % kListed];
@@ -876,11 +880,18 @@ struct Shape {
     int64_t wgs, partial;  // workgroups, floats of a partial result
 };
 
-template <class Fn>
+// Blocks of 128 rows rather than 64, a tile's operands read once for two columns of
+// each lane, where their sums and queries fit the registers of two workgroups a
+// CU. int8 tiles, which are turned into operands once a block, gain from them at
+// heads of 192 too: prompts of 2048 tokens 656 us and 890 with 64 rows; 16 bits 539 and 389.
+template <int KIND>
+constexpr int kMostWide = KIND == 1 ? 192 : 128;
+
+template <int KIND, class Fn>
 void by_shape(int D, int ht, Fn&& fn) {
     using std::integral_constant;
     auto with = [&](auto d) {
-        if constexpr (decltype(d)::value <= 192) {
+        if constexpr (decltype(d)::value <= kMostWide<KIND>) {
             if (ht == 2) return fn(d, integral_constant<int, 2>{});
         }
         fn(d, integral_constant<int, 1>{});
@@ -891,24 +902,24 @@ void by_shape(int D, int ht, Fn&& fn) {
     else with(integral_constant<int, 256>{});
 }
 
-Shape plan(const TokensArgs& a, int kind) {
+template <int KIND>
+Shape plan(const TokensArgs& a) {
     Shape s{};
     const int64_t group = a.Hq / a.H;
-    // Blocks of 128 rows where sequences have more than 64 on average. Heads of 256
-    // keep to 64: the sums and queries of two columns of 256 do not fit the registers.
-    s.ht = a.D <= 192 && a.T * group > 64 * a.B ? 2 : 1;
-    by_shape(a.D, s.ht, [&](auto d, auto ht) {
-        constexpr int D = decltype(d)::value, HT = decltype(ht)::value;
-        s.wgs = kCUs * (kind == 0 ? Attend<0, 0, D, HT>::kPerCU : Attend<0, 1, D, HT>::kPerCU);
-        s.partial = Attend<0, 0, D, HT>::kPartial;
+    s.ht = a.D <= kMostWide<KIND> && a.T * group > 64 * a.B ? 2 : 1;  // where sequences have more than 64 rows on average
+    by_shape<KIND>(a.D, s.ht, [&](auto d, auto ht) {
+        using A = Attend<0, KIND, decltype(d)::value, decltype(ht)::value>;
+        s.wgs = kCUs * A::kPerCU;
+        s.partial = A::kPartial;
     });
     return s;
 }
+Shape plan(const TokensArgs& a, int kind) { return kind == 0 ? plan<0>(a) : plan<1>(a); }
 
 template <int DT, int KIND>
 hipError_t launch(const TokensArgs& a, const Shape& s, hipStream_t stream) {
     hipError_t e = hipSuccess;
-    by_shape(a.D, s.ht, [&](auto d, auto ht) {
+    by_shape<KIND>(a.D, s.ht, [&](auto d, auto ht) {
         constexpr int D = decltype(d)::value, HT = decltype(ht)::value;
         using A = Attend<DT, KIND, D, HT>;
         const size_t lds = A::kBytes;
