@@ -161,6 +161,20 @@ def _stream(t: torch.Tensor):
     return _raw_stream(t.get_device())
 
 
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _call(device: int, entry, *args):
+    """A C entry with the tensors' device as the current one, which its launches go to."""
+    if _current_device() == device:
+        status = entry(*args)
+    else:
+        with torch.cuda.device(device):
+            status = entry(*args)
+    if status:
+        _check(status)
+
+
 def _ptr(t: torch.Tensor | None):
     return None if t is None else t.data_ptr()
 
@@ -751,12 +765,10 @@ def kv_append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, position
     nbytes = _cache_bytes(cache, device)
     if slots.get_device() != device:
         _same_device(k, slots=slots)
-    status = (_lib or load_library()).w4a16_kv_append(
-        *queries, k.data_ptr(), k.stride(0), k.stride(1), v.data_ptr(), v.stride(0), v.stride(1), T,
-        positions.data_ptr(), rates.data_ptr(), pairs, 1 if interleaved else 0, slots.data_ptr(), cache.data_ptr(),
-        nbytes, pages, H, D, page_size, kind, _DTYPE_CODE[dtype], _raw_stream(device))
-    if status:
-        _check(status)
+    _call(device, (_lib or load_library()).w4a16_kv_append,
+          *queries, k.data_ptr(), k.stride(0), k.stride(1), v.data_ptr(), v.stride(0), v.stride(1), T,
+          positions.data_ptr(), rates.data_ptr(), pairs, 1 if interleaved else 0, slots.data_ptr(), cache.data_ptr(),
+          nbytes, pages, H, D, page_size, kind, _DTYPE_CODE[dtype], _raw_stream(device))
     return out
 
 
@@ -812,12 +824,10 @@ def attention(q: torch.Tensor, cache: torch.Tensor, table: torch.Tensor, lengths
         # the first look is _default_workspace's own, without building the device object
         ws = (workspace or _workspaces.get(("attention", device, stream)) or _default_workspace(q.device, "attention")).get(need)
         ws_ptr, ws_bytes = ws.data_ptr(), ws.numel()
-    status = (_lib or load_library()).w4a16_attention_sinks(
-        q.data_ptr(), q.stride(0), q.stride(1), B, Hq, cache.data_ptr(), nbytes, pages, kv_heads, D, page_size, kind,
-        _DTYPE_CODE[dtype], table.data_ptr(), width, table.stride(0) if B > 1 else width, lengths.data_ptr(), window, sinks,
-        D ** -0.5 if scale is None else scale, out.data_ptr(), out.stride(0), out.stride(1), ws_ptr, ws_bytes, stream)
-    if status:
-        _check(status)
+    _call(device, (_lib or load_library()).w4a16_attention_sinks,
+          q.data_ptr(), q.stride(0), q.stride(1), B, Hq, cache.data_ptr(), nbytes, pages, kv_heads, D, page_size, kind,
+          _DTYPE_CODE[dtype], table.data_ptr(), width, table.stride(0) if B > 1 else width, lengths.data_ptr(), window, sinks,
+          D ** -0.5 if scale is None else scale, out.data_ptr(), out.stride(0), out.stride(1), ws_ptr, ws_bytes, stream)
     return out
 
 
@@ -875,13 +885,11 @@ def attention_tokens(q: torch.Tensor, starts: torch.Tensor, cache: torch.Tensor,
         ws = (workspace or _workspaces.get(("attention_tokens", device, stream))
               or _default_workspace(q.device, "attention_tokens")).get(need)
         ws_ptr, ws_bytes = ws.data_ptr(), ws.numel()
-    status = (_lib or load_library()).w4a16_attention_tokens(
-        q.data_ptr(), q.stride(0), q.stride(1), T, Hq, starts.data_ptr(), B, tree_ptr, words, tree_ld, cache.data_ptr(),
-        nbytes, pages, kv_heads, D, page_size, kind, _DTYPE_CODE[dtype], table.data_ptr(), width,
-        table.stride(0) if B > 1 else width, lengths.data_ptr(), window, sinks, D ** -0.5 if scale is None else scale,
-        out.data_ptr(), out.stride(0), out.stride(1), ws_ptr, ws_bytes, stream)
-    if status:
-        _check(status)
+    _call(device, (_lib or load_library()).w4a16_attention_tokens,
+          q.data_ptr(), q.stride(0), q.stride(1), T, Hq, starts.data_ptr(), B, tree_ptr, words, tree_ld, cache.data_ptr(),
+          nbytes, pages, kv_heads, D, page_size, kind, _DTYPE_CODE[dtype], table.data_ptr(), width,
+          table.stride(0) if B > 1 else width, lengths.data_ptr(), window, sinks, D ** -0.5 if scale is None else scale,
+          out.data_ptr(), out.stride(0), out.stride(1), ws_ptr, ws_bytes, stream)
     return out
 
 
@@ -907,9 +915,7 @@ def sample(logits: torch.Tensor, uniforms: torch.Tensor, temperature: torch.Tens
             _vector(name, t, M, dtype, device)
     if out is None:
         out = torch.empty(M, dtype=torch.int64, device=logits.device)
-    status = (_lib or load_library()).w4a16_sample(
-        logits.data_ptr(), M, V, logits.stride(0) if M > 1 else V, _DTYPE_CODE[logits.dtype], uniforms.data_ptr(),
-        _ptr(temperature), _ptr(top_k), _ptr(top_p), _ptr(min_p), out.data_ptr(), _ptr(probs), _raw_stream(device))
-    if status:
-        _check(status)
+    _call(device, (_lib or load_library()).w4a16_sample,
+          logits.data_ptr(), M, V, logits.stride(0) if M > 1 else V, _DTYPE_CODE[logits.dtype], uniforms.data_ptr(),
+          _ptr(temperature), _ptr(top_k), _ptr(top_p), _ptr(min_p), out.data_ptr(), _ptr(probs), _raw_stream(device))
     return out

@@ -190,3 +190,18 @@ def test_sample_repeats_in_a_graph_and_on_another_stream():
         got = y.clone()
         assert torch.equal(got, w4.sample(x, u, **kw))
     assert np.unique(got.cpu().numpy()).size > 1
+
+
+@pytest.mark.parametrize("dtype", BOTH)
+def test_both_zeros_are_one_value_however_many_they_are(dtype):
+    """More than 2^15 of each sign, and of one of them."""
+    V = 150000
+    g = gen("zeros")
+    sign = torch.rand(3, V, generator=g)
+    x = torch.zeros(3, V)
+    x[0] = torch.where(sign[0] < 0.5, -0.0, 0.0)
+    x[1] = torch.where(sign[1] < 0.4, -0.0, torch.where(sign[1] < 0.8, 0.0, 1.0))
+    x[2, ::3] = -0.0
+    x[2, 7] = 3.0
+    check(x.to(DTYPES[dtype]), torch.tensor([0.61, 0.1, 0.83]))
+    check(x.to(DTYPES[dtype]), torch.tensor([0.3, 0.97, 0.5]), top_k=[40000, 100000, 70000], top_p=[0.9, 0.5, 1.0])

@@ -416,3 +416,37 @@ def test_tokens_of_nothing():
     w4.attention_tokens(q, torch.tensor([0], dtype=torch.int32, device=DEV), batch.cache, batch.dev_table[:0], batch.lengths[:0],
                         batch.pages, 1, 32, ref.KV_ACT, out=out)
     assert bool((out == 7).all())
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("Hq,H,D", [(6, 2, 192), (4, 2, 256), (16, 2, 192), (16, 2, 64)])
+def test_tokens_several_blocks_a_workgroup(Hq, H, D, kind):
+    """More blocks than workgroups: each goes from one to the next, and blocks begin and end in different ones."""
+    r = np.random.default_rng(D + Hq)
+    news = r.integers(100, 330, 40)
+    lens = news + (r.random(40) < 0.5) * r.integers(0, 200, 40)
+    tokens(Batch("tokens blocks", lens.tolist(), H, D, 32, kind, "bf16"), news.tolist(), Hq)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("D", [64, 192, 256])
+def test_tree_values_that_are_not_finite_in_the_tree(D, kind):
+    """A drafted token's value that is not finite reaches its descendants only."""
+    past, m, bad = 40, 30, 4
+    r = np.random.default_rng(D)
+    words = step.random_tree(r, m, 1)
+    sees, _ = step.bits(words, m)
+    batch = Batch("tree bad", [past + m], 1, D, 32, kind, "f16")
+    n = past + m
+    q = randn(batch.g, m, 4, D, dtype=torch.float16)
+    k, v = randn(batch.g, n, 1, D, dtype=torch.float16), randn(batch.g, n, 1, D, dtype=torch.float16)
+    args = (q.to(DEV), torch.tensor([0, m], dtype=torch.int32, device=DEV), batch.cache, batch.dev_table, batch.lengths,
+            batch.pages, 1, 32, kind)
+    write(batch, 0, k, v)
+    before = w4.attention_tokens(*args, tree=words.to(DEV)).cpu()
+    v[past + bad, 0, 3] = float("inf")
+    write(batch, 0, k, v)
+    got = w4.attention_tokens(*args, tree=words.to(DEV)).cpu()
+    below = sees[:, bad]
+    assert bool(below.any()) and not bool(below.all())
+    assert torch.equal(got[~below], before[~below]) and not bool(got[below][..., 3].isfinite().any())

@@ -268,3 +268,32 @@ def test_sample_reference_by_hand():
     assert step.sample(x, 0.99, min_p=0.3)[0] == 4 and step.sample(x, 0.99, min_p=0.5)[0] == 2
     assert step.sample(x, 0.9, temperature=0.0) == (1, 1.0, 1.0)
     assert step.sample(torch.full((3,), -float("inf")), 0.5)[0] == -1
+
+
+def test_calls_run_with_their_tensors_device_current(monkeypatch):
+    """Where another device is current, the entry runs inside a switch to the tensors' one, errors included."""
+    current = [0]
+
+    class Switch:
+        def __init__(self, index):
+            self.index = index
+
+        def __enter__(self):
+            self.former, current[0] = current[0], self.index
+
+        def __exit__(self, *_):
+            current[0] = self.former
+
+    monkeypatch.setattr(w4, "_current_device", lambda: current[0])
+    monkeypatch.setattr(w4.torch.cuda, "device", Switch)
+    ran = []
+
+    def entry(status):
+        ran.append(current[0])
+        return status
+
+    w4._call(0, entry, 0)
+    w4._call(1, entry, 0)
+    with pytest.raises(RuntimeError, match="w4a16 status 1"):
+        w4._call(2, entry, 1)
+    assert ran == [0, 1, 2] and current == [0]
