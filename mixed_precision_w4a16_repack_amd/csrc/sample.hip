@@ -13,6 +13,11 @@
 //
 // One workgroup of 16 waves a row; 128 KB of LDS hold the counts, 16 bits each
 // (kCarry of a value that is more frequent go to a list).
+//
+// Bound by one CU's LDS atomics and the chain of its stages (clear, count, weights,
+// sums, three searches, the token's place): 64 rows of 128000 take 44 us, one of
+// 32003 8 to 18 (the most probable tokens alone, without the histogram, less). Rows
+// over several CUs would have to exchange histograms of 128 KB.
 #include "device_common.h"
 #include "internal.h"
 
