@@ -493,9 +493,9 @@ w4a16_status w4a16_attention_sinks(const void *q, int64_t q_bs, int64_t q_hs, in
                                    void *workspace, size_t workspace_bytes, hipStream_t stream);
 
 /* Bytes of device workspace w4a16_attention_tokens needs (0 if T or B is 0).
- * The workspace need not be cleared; calls that share one must be ordered. A
- * buffer that it shares with a call that needs a zero counter region must have
- * that region zeroed again. out_bytes is a host pointer. */
+ * The workspace need not be cleared; calls that share one must be ordered. Its
+ * first w4a16_workspace_counter_bytes() bytes are not touched, so that calls that need
+ * them zero may share it. out_bytes is a host pointer. */
 w4a16_status w4a16_attention_tokens_workspace_size(int64_t T, int64_t B, int32_t q_heads, int32_t kv_heads,
                                                    int32_t head_dim, int32_t page_size, int64_t table_width,
                                                    int32_t kind, size_t *out_bytes);
@@ -525,7 +525,7 @@ w4a16_status w4a16_attention_tokens_workspace_size(int64_t T, int64_t B, int32_t
  * NaN or an infinity among the values that it sees gives it one (either).
  * Probabilities enter the products as in w4a16_attention; scores, maxima and
  * sums are fp32. The result does not depend on the workspace's contents or on
- * earlier calls. T * q_heads must be below 2^31. */
+ * earlier calls. T * q_heads must be at most 2^31 - 256. */
 w4a16_status w4a16_attention_tokens(const void *q, int64_t q_ts, int64_t q_hs, int64_t T, int32_t q_heads,
                                     const int32_t *starts, int64_t B, const int64_t *tree, int64_t tree_words,
                                     int64_t tree_ld, const void *cache, size_t cache_bytes, int64_t pages,

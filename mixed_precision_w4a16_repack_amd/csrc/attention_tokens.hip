@@ -671,7 +671,7 @@ struct Attend {
             ++done;
             return true;
         };
-        auto whole = [&]() { return t + kTile <= full_hi && (t >= full_lo || t + kTile <= a.sinks); };
+        auto whole = [&]() { return t <= full_hi - kTile && (t >= full_lo || t <= a.sinks - kTile); };
         bool have = advance();
         if (!busy) {
             while (have) have = advance();
@@ -978,7 +978,7 @@ hipError_t launch(const TokensArgs& a, const Shape& s, hipStream_t stream) {
 
 size_t attention_tokens_workspace(const TokensArgs& a, int kind) {
     const Shape s = plan(a, kind);
-    return align256((size_t)s.wgs * sizeof(Record)) + (size_t)s.wgs * 2 * s.partial * 4;
+    return kCounterRegionBytes + align256((size_t)s.wgs * sizeof(Record)) + (size_t)s.wgs * 2 * s.partial * 4;
 }
 
 hipError_t launch_attention_tokens(TokensArgs a, int kind, int dtype, void* workspace, hipStream_t stream) {
@@ -988,8 +988,10 @@ hipError_t launch_attention_tokens(TokensArgs a, int kind, int dtype, void* work
     const int64_t most = a.width * a.P, all = ((int64_t)1 << 31) - 1;
     a.most = (int)(most < all ? most : all);
     a.reach = a.window > 0 ? a.window : (int64_t)1 << 32;
-    a.records = workspace;
-    a.partials = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + align256((size_t)s.wgs * sizeof(Record)));
+    // Behind the counters of other calls that a caller lets share the workspace.
+    unsigned char* at = static_cast<unsigned char*>(workspace) + kCounterRegionBytes;
+    a.records = at;
+    a.partials = reinterpret_cast<float*>(at + align256((size_t)s.wgs * sizeof(Record)));
     if (kind == 0) return dtype == 0 ? launch<0, 0>(a, s, stream) : launch<1, 0>(a, s, stream);
     return dtype == 0 ? launch<0, 1>(a, s, stream) : launch<1, 1>(a, s, stream);
 }

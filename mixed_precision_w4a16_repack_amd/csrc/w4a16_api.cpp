@@ -671,9 +671,10 @@ int sinks_of(int64_t window, int64_t sinks) {
     return window > 0 ? (int)(sinks < most ? sinks : most) : 0;
 }
 
+// Rows (token, query head) are counted in 31 bits, whole blocks of up to 128 of them.
 w4a16_status check_tokens(int64_t T, int32_t q_heads) {
     if (T < 0) return fail(W4A16_ERR_INVALID_ARG, "T=%lld must be >= 0", (long long)T);
-    if (T > (int64_t)1 << 31 || (q_heads > 0 && T * q_heads >= (int64_t)1 << 31))
+    if (T > (int64_t)1 << 31 || (q_heads > 0 && T * q_heads > ((int64_t)1 << 31) - 256))
         return fail(W4A16_ERR_UNSUPPORTED, "T=%lld tokens of q_heads=%d are too large for one launch", (long long)T, q_heads);
     return W4A16_OK;
 }

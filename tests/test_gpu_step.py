@@ -262,3 +262,21 @@ def test_two_streams_at_once():
     torch.cuda.synchronize()
     for result in got:
         assert all(torch.equal(x, y) for x, y in zip(result, want))
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_one_workspace_for_all_calls(kind):
+    """Products and both attentions share one: none leaves the others' counters changed."""
+    chain, twin = Chain([3000, 900], [60, 40], kind, 6), Chain([3000, 900], [60, 40], kind, 6)
+    ws = w4.Workspace(DEV)
+    chain.ws = {"gemm": ws, "attention": ws}
+    for _ in range(3):
+        want, got = twin.step(), chain.step()
+        assert all(torch.equal(x, y) for x, y in zip(got, want))
+        c = chain.cache
+        q = want[3][:2].contiguous()
+        one = [w4.attention(q, x.cache.data, x.cache.dev_table, x.lengths, c.pages, c.H, c.P, c.kind, workspace=w)
+               for x, w in ((chain, ws), (twin, None))]
+        assert torch.equal(*one)
+        for x in (chain, twin):
+            x.feed(want[0])
