@@ -26,10 +26,11 @@
 // cut into equal runs, one a workgroup, from the lengths, on the device; a
 // block that lies in several leaves partial results, which a second kernel joins.
 //
-// What bounds it: not the matrix cores (29 % busy) nor the vector ALUs (45 %), but
-// that a wave's step, 48 matrix products and 150 other instructions for 32 rows and 32
-// tokens, hides little behind the other wave of its SIMD: times without the products,
-// without the exponentials or without the loads fall by nearly the sum of these.
+// What bounds it: the SIMDs' instructions. A wave's step of 32 rows and 32 tokens is 48
+// matrix products (16 cycles each), 180 other vector instructions (16 of them
+// exponentials) and 68 scalar ones; the matrix cores are busy for 42 % of the time and the
+// other vector instructions take as much again, and the two waves of a SIMD overlap little of it:
+// without the products, the exponentials or the loads the time falls by about that part's own.
 // Four prompts of 2048 tokens, 32 heads of 128 over 8, bf16: 230 us, 600 TFLOP/s
 // (the two-operand products counted once); 24 trees of 32 tokens over 3000 on average: 79 us;
 // two trees of 80 tokens over 50000 of int8, 64 heads: 454 us, 577 TFLOP/s; one tree of 16
