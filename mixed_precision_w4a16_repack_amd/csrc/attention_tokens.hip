@@ -31,9 +31,9 @@
 // exponentials) and 68 scalar ones; the matrix cores are busy for 42 % of the time and the
 // other vector instructions take as much again, and the two waves of a SIMD overlap little of it:
 // without the products, the exponentials or the loads the time falls by about that part's own.
-// Four prompts of 2048 tokens, 32 heads of 128 over 8, bf16: 230 us, 600 TFLOP/s
+// Four prompts of 2048 tokens, 32 heads of 128 over 8, bf16: 228 us, 605 TFLOP/s
 // (the two-operand products counted once); 24 trees of 32 tokens over 3000 on average: 79 us;
-// two trees of 80 tokens over 50000 of int8, 64 heads: 454 us, 577 TFLOP/s; one tree of 16
+// two trees of 80 tokens over 50000 of int8, 64 heads: 435 us, 602 TFLOP/s; one tree of 16
 // tokens over 700: 20 us, of which 4 find the share and 4 join.
 // Columns of 64 rows a wave with one workgroup a CU: 702 us for the 255 of then.
 #include <cmath>
