@@ -205,3 +205,26 @@ def test_both_zeros_are_one_value_however_many_they_are(dtype):
     x[2, 7] = 3.0
     check(x.to(DTYPES[dtype]), torch.tensor([0.61, 0.1, 0.83]))
     check(x.to(DTYPES[dtype]), torch.tensor([0.3, 0.97, 0.5]), top_k=[40000, 100000, 70000], top_p=[0.9, 0.5, 1.0])
+
+
+@pytest.mark.parametrize("V", [70000, 200000])
+@pytest.mark.parametrize("dtype", BOTH)
+def test_sample_nans_of_any_pattern_that_are_most_of_a_row(V, dtype):
+    """A NaN pattern of either sign, beside the infinities' in the order and far from them, more than 2^15 times: never
+    drawn, counted nowhere, alone, under one finite logit, among others and beside an infinite one."""
+    inf = 0x7C00 if dtype == "f16" else 0x7F80
+    g = gen("nan", V, dtype)
+    for payload in (1, 2, 62, 63, 64, 0x7FFF - inf):
+        for sign in (0, 0x8000):
+            bits = torch.full((5, V), (sign | inf | payload) - (0x10000 if sign else 0), dtype=torch.int16)
+            x = bits.view(DTYPES[dtype])
+            assert bool(x.isnan().all())
+            x[1, 12345] = 1.0
+            x[2, ::7] = rows(g, 1, len(range(0, V, 7)), dtype)[0]
+            x[3, V - 1] = float("inf")
+            x[3, 5] = 2.0
+            x[4, ::2] = -3.0
+            u = torch.rand(5, generator=g)
+            for kw in ({}, dict(top_k=[40] * 5, top_p=[0.9] * 5, min_p=[0.05] * 5), dict(temperature=[0.0] * 5)):
+                got = check(x, u, **kw)
+                assert got[0] == -1 and got[1] == 12345 and got[3] == V - 1
