@@ -748,7 +748,9 @@ Shape plan(const AttentionArgs& a, int kind) {
         s = kind == 0 ? shape_of<0, decltype(d)::value, decltype(ht)::value>() : shape_of<1, decltype(d)::value, decltype(ht)::value>();
     });
     int64_t tokens = a.width * a.P;
-    if (a.window > 0 && a.window + a.sinks < tokens) tokens = a.window + kTile + (a.sinks > 0 ? a.sinks + kTile : 0);
+    // Written without the sum of window and first tokens, which may leave 64 bits.
+    if (a.window > 0 && a.window < tokens && a.sinks < tokens - a.window)
+        tokens = a.window + kTile + (a.sinks > 0 ? a.sinks + kTile : 0);
     const int64_t parts = (tokens / kTile + kMinTiles) / kMinTiles;
     const int64_t units = (int64_t)a.H * ((group + s.heads - 1) / s.heads);
     s.wgs = kCUs * s.per_cu;

@@ -118,6 +118,17 @@ def test_sinks_workspace_size(lib):
     assert w4.attention_workspace_size(1, 32, 8, 128, 64, 1 << 20, 100, 0, 3000) > w4.attention_workspace_size(1, 32, 8, 128, 64, 1 << 20, 100, 0)
 
 
+@pytest.mark.parametrize("kind", [0, 1])
+@pytest.mark.parametrize("B,width", [(1, 64), (1, 1 << 20), (9, 3)])
+def test_sinks_workspace_of_windows_near_2_63(lib, B, width, kind):
+    """Their sum with the first tokens leaves 64 bits: as without a window."""
+    every = w4.attention_workspace_size(B, 32, 8, 128, 64, width, 0, kind)
+    most = (1 << 63) - 1
+    for window in (most, most - 1, most - 4, most - 32, most - 64, most - 100, 1 << 62, 1 << 40):
+        for sinks in (0, 1, 4, 64, 1 << 30, 1 << 31, most):
+            assert w4.attention_workspace_size(B, 32, 8, 128, 64, width, window, kind, sinks) == every, (window, sinks)
+
+
 def _tokens(lib, **kw):
     a = dict(q=P, qts=4096, qhs=128, T=8, Hq=32, starts=P, B=2, tree=P, words=1, tld=1, cache=P, nbytes=1 << 40, pages=4,
              H=8, D=128, P=64, kind=0, dtype=0, table=P, width=2, ld=2, lengths=P, window=0, sinks=0, scale=0.1, out=P,
