@@ -988,7 +988,9 @@ hipError_t launch_attention_tokens(TokensArgs a, int kind, int dtype, void* work
     a.one_by_group = std::nextafter(1.0 / a.group, 2.0);
     const int64_t most = a.width * a.P, all = ((int64_t)1 << 31) - 1;
     a.most = (int)(most < all ? most : all);
-    a.reach = a.window > 0 ? a.window : (int64_t)1 << 32;
+    // A position, 2^31 below 0 at the least, minus the window stays within 64 bits.
+    const int64_t every = (int64_t)1 << 32;
+    a.reach = a.window > 0 && a.window < every ? a.window : every;
     // Behind the counters of other calls that a caller lets share the workspace.
     unsigned char* at = static_cast<unsigned char*>(workspace) + kCounterRegionBytes;
     a.records = at;

@@ -450,3 +450,21 @@ def test_tree_values_that_are_not_finite_in_the_tree(D, kind):
     below = sees[:, bad]
     assert bool(below.any()) and not bool(below.all())
     assert torch.equal(got[~below], before[~below]) and not bool(got[below][..., 3].isfinite().any())
+
+
+@pytest.mark.parametrize("tree", [False, True])
+def test_tokens_windows_near_2_63(tree):
+    """As without a window, also at positions below 0 (more tokens new than cached), and with an empty table."""
+    batch = Batch("huge window", [64, 3], 1, 64, 32, ref.KV_ACT, "f16")
+    q = randn(batch.g, 130, 4, 64, dtype=torch.float16).to(DEV)
+    starts = torch.tensor([0, 30, 130], dtype=torch.int32, device=DEV)
+    words = torch.randint(-(2**63), 2**63 - 1, (130, 2), generator=batch.g).to(DEV) if tree else None
+
+    def run(table, **kw):
+        return w4.attention_tokens(q, starts, batch.cache, table, batch.lengths, batch.pages, 1, 32, ref.KV_ACT, tree=words, **kw)
+
+    want = run(batch.dev_table)
+    for window in (1 << 32, 1 << 62, 2**63 - 100, 2**63 - 4, 2**63 - 1):
+        for sinks in (0, 4, 2**63 - 1):
+            assert torch.equal(run(batch.dev_table, window=window, sinks=sinks), want)
+            assert not bool(run(batch.dev_table[:, :0], window=window, sinks=sinks).any())
