@@ -508,19 +508,22 @@ w4a16_status w4a16_attention_tokens_workspace_size(int64_t T, int64_t B, int32_t
  * starts[b] + i is token n - m + i. Without a tree that token sees the tokens
  * 0 .. n - m + i, with window > 0 the last `window` of them and the first
  * `sinks`. With a tree, tree[row * tree_ld + j / 64] bit j % 64 says whether the
- * row sees its sequence's new token j (itself as well, if the bit is set; bits
- * from m on do not count); of the tokens before the new ones it sees all, or
- * with window > 0 those less than `window` before its position and the first
- * `sinks`, its position being n - m + (set bits) - 1, that is its depth behind
- * the past. A row without a set bit (padding) sees nothing.
+ * row sees its sequence's new token j (itself as well, if the bit is set); of
+ * the tokens before the new ones it sees all, or with window > 0 those less than
+ * `window` before its position and the first `sinks`, its position being
+ * n - m + (set bits below bit m) - 1, that is its depth behind the past (n - m
+ * where none is set). Bits from m on stand for no token and do not count in
+ * the position. A row whose words are all 0 (padding) sees nothing; any bit,
+ * one from m on too, lets it see the tokens before the new ones.
  *   q, out   element (row, head, d) at row * ts + head * hs + d, act dtype;
  *            rows of no sequence are neither read nor written
  *   starts   [B + 1] int32 (device), not decreasing, cut to 0 .. T
  *   tree     [T, tree_ld] int64 (device), tree_ld >= tree_words >= 1, or NULL
  *   table, lengths, heads, the cache and its missing pages as for
- *            w4a16_attention; a new token that has no place (m > n) sees
- *            nothing. Rows that see nothing, or only scores of -infinity, are
- *            zeros
+ *            w4a16_attention. Where m > n, the first m - n new tokens have no
+ *            place: no row sees them, and without a tree their own rows see
+ *            nothing (with one, the tokens of their bits that have a place).
+ *            Rows that see nothing, or only scores of -infinity, are zeros
  * Memory of tokens that a row does not see may hold anything, NaN included; a
  * NaN or an infinity among the values that it sees gives it one (either).
  * Probabilities enter the products as in w4a16_attention; scores, maxima and

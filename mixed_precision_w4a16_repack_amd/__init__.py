@@ -849,7 +849,7 @@ def attention_tokens(q: torch.Tensor, starts: torch.Tensor, cache: torch.Tensor,
     Sequence b's new tokens are rows ``starts[b]`` .. ``starts[b + 1] - 1`` (``starts`` [B + 1] int32), the last ones
     of its ``lengths[b]`` cached tokens; rows of no sequence are left as they are. A token sees those up to itself,
     or, with ``tree`` [T, words] int64, all tokens before the new ones and the new ones whose bits its row has (bit
-    j % 64 of word j // 64; a row without bits sees nothing). ``window`` > 0 sees only the last tokens, and the first
+    j % 64 of word j // 64; a row of zeros sees nothing, bits past its sequence's new tokens stand for none). ``window`` > 0 sees only the last tokens, and the first
     ``sinks``. For calls that are captured into a graph see ``Workspace``."""
     if not q.is_cuda or q.dtype not in _DTYPE_CODE:
         _need_cuda("q", q, (torch.float16, torch.bfloat16))

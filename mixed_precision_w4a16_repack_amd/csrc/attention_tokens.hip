@@ -225,10 +225,16 @@ struct Attend {
             if (at_row < rows) {
                 int at = past + i, end = at + 1;
                 if (a.tree) {
-                    int depth = 0;
-                    for (int w = 0; w < a.tree_words; ++w) depth += __builtin_popcountll(a.tree[(row + i) * a.tree_ld + w]);
-                    at = past + depth - 1;
-                    end = depth > 0 ? past : 0;  // past tokens; the tree's by their bits
+                    int depth = 0;  // set bits of the it.m new tokens: those behind them stand for no token
+                    uint64_t any = 0;
+                    for (int w = 0; w < a.tree_words; ++w) {
+                        const uint64_t word = a.tree[(row + i) * a.tree_ld + w];
+                        const int left = it.m - 64 * w;
+                        depth += __builtin_popcountll(left >= 64 ? word : (left > 0 ? word & (((uint64_t)1 << left) - 1) : 0));
+                        any |= word;
+                    }
+                    at = past + (depth > 0 ? depth - 1 : 0);
+                    end = any != 0 ? past : 0;  // past tokens; the tree's by their bits
                 }
                 hi[h] = end > 0 ? end : 0;
                 lo[h] = at >= a.reach ? (int)(at + 1 - a.reach) : 0;

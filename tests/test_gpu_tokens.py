@@ -468,3 +468,51 @@ def test_tokens_windows_near_2_63(tree):
         for sinks in (0, 4, 2**63 - 1):
             assert torch.equal(run(batch.dev_table, window=window, sinks=sinks), want)
             assert not bool(run(batch.dev_table[:, :0], window=window, sinks=sinks).any())
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("window,sinks", [(0, 0), (5, 0), (40, 3), (100, 0), (300, 40)])
+def test_tree_bits_past_the_new_tokens_change_nothing(window, sinks, kind):
+    """Words padded with ones, or with any bits, behind a sequence's new tokens: neither the tokens that a row sees nor
+    its position in a window depend on them."""
+    r = np.random.default_rng(6)
+    lens, news, words = [200, 333, 64, 700, 65], [5, 40, 64, 130, 65], 3
+    tree = [step.random_tree(r, m, words) for m in news]
+    batch = Batch("tree padding", lens, 2, 128, 64, kind, "bf16")
+    q = randn(batch.g, sum(news), 8, 128, dtype=torch.bfloat16)
+    clean = tokens(batch, news, 8, tree=tree, window=window, sinks=sinks, q=q, spare=0)
+    starts = torch.tensor(np.concatenate([[0], np.cumsum(news)]), dtype=torch.int32, device=DEV)
+    for fill in ("ones", "any"):
+        padded = []
+        for m, t in zip(news, tree):
+            past = torch.zeros(words, 64, dtype=torch.bool)
+            past.view(-1)[m:] = True
+            mask = torch.from_numpy(np.packbits(past.numpy(), axis=1, bitorder="little").view("<i8")[:, 0].copy())
+            some = -1 if fill == "ones" else torch.from_numpy(r.integers(-(2**63), 2**63 - 1, t.shape))
+            padded.append(t | (mask & some))
+        assert any(bool((p != t).any()) for p, t in zip(padded, tree))
+        got = w4.attention_tokens(q.to(DEV), starts, batch.cache, batch.dev_table, batch.lengths, batch.pages, 2, 64, kind,
+                                  tree=torch.cat(padded).to(DEV), window=window, sinks=sinks)
+        assert torch.equal(got, clean)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("window,sinks", [(0, 0), (7, 0), (40, 3), (64, 0)])
+def test_tree_rows_of_bits_past_the_new_tokens_only(window, sinks, kind):
+    """They see what lies before the new tokens, as at the first new one's position; a row of zeros sees nothing."""
+    lens, news, Hq = [90, 129], [6, 33], 4
+    batch = Batch("tree past only", lens, 2, 64, 32, kind, "f16")
+    q = randn(batch.g, sum(news), Hq, 64, dtype=torch.float16)
+    tree = torch.zeros(sum(news), 2, dtype=torch.int64)
+    for row, words in ((1, [1 << 6, 0]), (2, [-64, -1]), (4, [0, 1]), (8, [1 << 33, 0]), (30, [0, -1])):
+        tree[row] = torch.tensor(words)
+    starts = torch.tensor([0, 6, 39], dtype=torch.int32, device=DEV)
+    o = w4.attention_tokens(q.to(DEV), starts, batch.cache, batch.dev_table, batch.lengths, batch.pages, 2, 32, kind,
+                            tree=tree.to(DEV), window=window, sinks=sinks).cpu()
+    for row in range(sum(news)):
+        b = int(row >= 6)
+        n, past = lens[b], lens[b] - news[b]
+        t = torch.arange(n)
+        seen = (t < past) & ((t > past - window) | (t < sinks) | (window == 0)) & bool(tree[row].any())
+        want, A, S = ref.attention(q[row], batch.k[b], batch.v[b], seen, 64**-0.5)
+        within(o[row], want, ref.attention_tolerance(want, A, S, "f16", kind, n), f"row {row}")
