@@ -301,7 +301,9 @@ struct Attend {
                         const float y = __builtin_ldexpf(__builtin_bit_cast(float, bits & 0xFFFF0000u), up);
                         q[h][i][w] = (uint32_t)to_act_bits<0>(x) | (uint32_t)to_act_bits<0>(y) << 16;
                     }
-                factor[h] = __builtin_ldexpf(factor[h], -up);
+                // Never 0, which times an unseen score's -infinity is NaN: the least number in its
+                // place moves a score by less than 2^-21, since products are below 2^128.
+                factor[h] = fmaxf(__builtin_ldexpf(factor[h], -up), 0x1p-149f);
             }
         }
     }

@@ -516,3 +516,14 @@ def test_tree_rows_of_bits_past_the_new_tokens_only(window, sinks, kind):
         seen = (t < past) & ((t > past - window) | (t < sinks) | (window == 0)) & bool(tree[row].any())
         want, A, S = ref.attention(q[row], batch.k[b], batch.v[b], seen, 64**-0.5)
         within(o[row], want, ref.attention_tolerance(want, A, S, "f16", kind, n), f"row {row}")
+
+
+
+def test_tokens_int8_tiny_scales_of_queries_and_scores():
+    """A factor on the scores below fp32's range, from the scale or the queries: unseen tokens stay unseen."""
+    batch = Batch("tiny factor", [100, 40], 2, 64, 32, ref.KV_INT8, "bf16")
+    tokens(batch, [70, 40], 8, scale=1e-42)
+    tokens(batch, [70, 40], 8, scale=-1e-40, window=20, sinks=2)
+    q = (randn(batch.g, 113, 8, 64, dtype=torch.bfloat16).float() * 2.0**-129).to(torch.bfloat16)
+    assert bool((q != 0).any())
+    tokens(batch, [70, 40], 8, q=q, scale=1e-4)
