@@ -195,8 +195,8 @@ struct Attend {
     float factor[HT];
     floatx4 o[HT][NO];
     float r[HT], l[HT];
-    static constexpr float kFar = 100.0f;  // int8: sums of 2^31 probabilities of 2^kFar are within fp32
-        // Of each column: what it sees, tokens lo .. hi - 1 and 0 .. sk - 1, and tree bits from `past` on.
+    static constexpr float kFar = 96.0f;  // int8: sums of 2^31 probabilities of 2^kFar, 2^127, are within fp32
+    // Of each column: what it sees, tokens lo .. hi - 1 and 0 .. sk - 1, and tree bits from `past` on.
     int lo[HT], hi[HT];
     int64_t row;   // of the block's sequence
     int past, first, rows;  // tokens before the new ones (may be negative), the block's first row and the sequence's rows

@@ -527,3 +527,25 @@ def test_tokens_int8_tiny_scales_of_queries_and_scores():
     q = (randn(batch.g, 113, 8, 64, dtype=torch.bfloat16).float() * 2.0**-129).to(torch.bfloat16)
     assert bool((q != 0).any())
     tokens(batch, [70, 40], 8, q=q, scale=1e-4)
+
+
+
+def test_tokens_int8_sums_over_2_28_tokens_of_tiny_values():
+    """Values with scales far below the others' range, one page 2^20 times: the sum of the probabilities, which are
+    relative to a low reference then, stays within fp32."""
+    P, pages = 256, 1 << 20
+    n = P * pages
+    cache = torch.zeros(w4.kv_cache_size(1, 1, 64, P, ref.KV_INT8), dtype=torch.uint8, device=DEV)
+    g = gen("tiny values")
+    k = randn(g, P, 1, 64, dtype=torch.bfloat16).to(DEV)
+    v = torch.full((P, 1, 64), 2.0**-103, dtype=torch.bfloat16, device=DEV)
+    w4.kv_write(k, v, torch.arange(P, device=DEV), cache, 1, P, ref.KV_INT8)
+    q = torch.zeros(2, 1, 64, dtype=torch.bfloat16, device=DEV)
+    o = w4.attention_tokens(q, torch.tensor([0, 2], dtype=torch.int32, device=DEV), cache,
+                            torch.zeros(1, pages, dtype=torch.int32, device=DEV), torch.tensor([n], dtype=torch.int32, device=DEV),
+                            1, 1, P, ref.KV_INT8)
+    # Scores of 0: every probability is 1 / n, and the mean of equal values is that value. A probability's operand is
+    # rounded by 2^-11, a workgroup's fp32 sums of 2^28 / 32 / 512 = 2^14 tiles by 2^-23 each at most, the join's of 512
+    # by less than 2^-13, the output by 2^-8.
+    within(o.cpu(), torch.full(o.shape, 2.0**-103, dtype=torch.float64),
+           2.0**-103 * (2.0**-8 + 2.0**-9 + 2.0**-11 + 2.0**-13 + 2.0**-23))
