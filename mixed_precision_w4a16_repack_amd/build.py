@@ -29,7 +29,7 @@ CEILING_LIB = os.path.join(PKG, "libw4a16_ceiling.so")
 SOURCES = ["w4a16_api.cpp", "repack.hip", "skinny.hip", "mfma.hip", "dense.hip", "w4a8.hip", "scratch.hip",
            "row_ops.hip", "kv_cache.hip", "attention.hip", "attention_tokens.hip", "sample.hip"]
 STAGED = ["mfma.hip", "w4a8.hip"]  # kernels with hand-counted waits (wait_check)
-ASSEMBLED = STAGED + ["skinny.hip", "attention.hip", "attention_tokens.hip"]  # every source with MFMA kernels (operand hazard check)
+ASSEMBLED = STAGED + ["skinny.hip", "attention.hip", "attention_tokens.hip"]  # every source with MFMA kernels (checks of operand hazards and of M0)
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
@@ -100,6 +100,19 @@ def check_mfma_operands(asm_paths) -> None:
         raise RuntimeError("MFMA operand check failed:\n" + "\n".join(problems[:20]))
 
 
+def check_m0(asm_paths) -> None:
+    """Fails when the compiler uses M0 in a kernel whose inline asm writes it
+    (see wait_check.m0_conflicts)."""
+    from . import wait_check
+
+    problems = []
+    for p in asm_paths:
+        with open(p) as f:
+            problems += wait_check.m0_conflicts(f.read())
+    if problems:
+        raise RuntimeError("M0 check failed:\n" + "\n".join(problems[:20]))
+
+
 def _build_ceiling() -> None:
     tmp = CEILING_LIB + ".tmp"
     cmd = [HIPCC, "-x", "hip", *FLAGS, "-shared", os.path.join(CSRC, CEILING_SRC), "-o", tmp]
@@ -119,6 +132,7 @@ def build(verbose: bool = False) -> str:
         asm_paths = {s: f.result() for s, f in asm.items()}
     check_waits([asm_paths[s] for s in STAGED])
     check_mfma_operands(list(asm_paths.values()))
+    check_m0(list(asm_paths.values()))
     _build_ceiling()
     tmp = LIB + ".tmp"
     cmd = [HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp, *objs, "-L/opt/rocm/lib", "-lhipblaslt"]

@@ -117,7 +117,8 @@ __device__ __forceinline__ int64_t same(int64_t x) { return read_lane(x, 0); }
 // asm, so that the compiler does not wait for them at every LDS read: the ring's
 // own waits do (wait_vmcnt, then the barrier). They only make the compiler's other
 // waits stricter. s_nop: the descriptor may come from a VALU instruction (5
-// wait states to the load), M0 needs one.
+// wait states to the load), M0 needs one. M0 is reserved and cannot be named as
+// changed: the build checks that the compiler itself uses it in none of these kernels.
 template <int N>
 __device__ __forceinline__ void load_lds(const u32x4& rsrc, uint32_t lds, uint32_t voff, uint32_t soff) {
     static_assert(N >= 1, "pieces");

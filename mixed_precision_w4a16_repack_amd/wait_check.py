@@ -1,4 +1,5 @@
-"""Build check of the hand-counted memory waits of the staged GEMM kernels.
+"""Build checks: the hand-counted memory waits of the staged GEMM kernels, the
+operands of MFMAs beside inline asm, and M0 beside inline asm.
 
 The tiled kernels (mfma_ring_kernel, mfma_lds_kernel, w4a8_ring_kernel) load
 operand tiles straight into LDS with buffer loads that no register tracks,
@@ -306,6 +307,30 @@ def mfma_operand_hazards(text: str) -> list[str]:
                     ws += w
             hist.append((1, written, asm_valu, read))
             hist = hist[-40:]
+    return problems
+
+
+def m0_conflicts(text: str) -> list[str]:
+    """Instructions of the compiler's own that use M0 in a kernel whose inline
+    asm writes it. M0 is reserved: an asm statement cannot name it as changed,
+    and the compiler may keep a value there from one block to the next."""
+    problems = []
+    for name, lines in _functions(text):
+        written, own, in_asm = False, [], False
+        for raw in lines:
+            t = raw.strip()
+            if t.startswith(";;#ASMSTART") or t.startswith(";;#ASMEND"):
+                in_asm = t.startswith(";;#ASMSTART")
+                continue
+            t = t.split(";")[0].strip()
+            if not re.search(r"\bm0\b", t):
+                continue
+            if not in_asm:
+                own.append(t)
+            elif re.match(r"s_\w+\s+m0\b", t):
+                written = True
+        if written:
+            problems += [f"{name}: '{t}' beside inline asm that writes m0" for t in own]
     return problems
 
 

@@ -165,3 +165,26 @@ def test_committed_kernels_pass(committed_assembly):
 @needs_hipcc
 def test_committed_kernels_have_no_mfma_operand_hazard(committed_assembly):
     lib_build.check_mfma_operands(list(committed_assembly.values()))
+
+
+M0 = "\t;;#ASMSTART\n\ts_nop 4\n\ts_mov_b32 m0, s6\n\ts_nop 0\n" + LDS + "\t;;#ASMEND\n"
+OWN_M0 = "\ts_mov_b32 m0, s7\n"
+
+
+def test_m0_of_inline_asm_and_of_the_compiler():
+    def found(body):
+        return wait_check.m0_conflicts(listing("_Z6kernelv", body))
+
+    assert found(M0) == [] and found(OWN_M0 + LDS) == []
+    assert len(found(M0 + OWN_M0 + LDS)) == 1
+    assert len(found(OWN_M0 + ".LBB0_1:\n" + M0 + "\tv_movrels_b32 v1, v2, m0\n")) == 2
+    # another kernel's own is its business
+    assert wait_check.m0_conflicts(listing("_Z1av", M0) + listing("_Z1bv", OWN_M0)) == []
+
+
+@needs_hipcc
+def test_committed_kernels_leave_m0_to_inline_asm(committed_assembly):
+    written = [name for p in committed_assembly.values() for name, lines in wait_check._functions(open(p).read())
+               if "attention_tokens_kernel" in name and any("s_mov_b32 m0" in t for t in lines)]
+    assert len(written) == 26  # one for each type, kind, head size and block size
+    lib_build.check_m0(list(committed_assembly.values()))
