@@ -1,12 +1,13 @@
 """Host sanitizer builds (CPU only): the oracle, and the library's argument
 checks, built with AddressSanitizer and UndefinedBehaviorSanitizer and run by
-small C drivers (tests/sanitize_oracle.c, tests/sanitize_abi.c). Any
+small C drivers (tests/sanitize_oracle.c, tests/sanitize_abi.c, tests/sanitize_operators.c). Any
 out-of-bounds access, integer overflow or undefined shift aborts a driver.
 Only host code is instrumented: the library's device code is compiled
-normally, and the ABI driver makes no call that reaches a GPU."""
+normally, and the ABI drivers make no call that reaches a GPU."""
 
 from __future__ import annotations
 
+import concurrent.futures
 import os
 import shutil
 import subprocess
@@ -57,5 +58,37 @@ def test_library_argument_checks_under_sanitizers():
     others = [o for name, o in objs.items() if name != "w4a16_api"]
     _run([lib_build.HIPCC, f"--offload-arch={lib_build.ARCH}", "-Xarch_host", "-fsanitize=address", "-Xarch_host",
           "-fsanitize=undefined", "-o", exe, drv, api, *others, "-L/opt/rocm/lib", "-lhipblaslt"])
+    res = _run([exe], env=ENV)
+    assert res.stdout.strip().endswith("ok")
+
+
+@pytest.mark.skipif(not os.path.exists(lib_build.HIPCC) or shutil.which("gcc") is None, reason="needs hipcc and gcc")
+def test_operators_argument_checks_and_sizes_under_sanitizers():
+    """The operators' checks, and the host code that sizes the attention calls' launches and workspaces
+    (tests/sanitize_operators.c)."""
+    os.makedirs(OUT, exist_ok=True)
+    names = [os.path.splitext(s)[0] for s in lib_build.SOURCES]
+    objs = {n: os.path.join(lib_build.BUILD, n + ".o") for n in names}
+    if not all(os.path.exists(o) for o in objs.values()):
+        lib_build.build()
+    sources = ["w4a16_api.cpp", "attention.hip", "attention_tokens.hip"]
+
+    def instrumented(src):
+        obj = os.path.join(OUT, os.path.splitext(src)[0] + "_operators.o")
+        _run([lib_build.HIPCC, "-x", "hip", *lib_build.FLAGS, "-O1", "-g", "-Xarch_host", "-fsanitize=address",
+              "-Xarch_host", "-fsanitize=undefined", "-Xarch_host", "-fno-sanitize-recover=all", "-c",
+              os.path.join(lib_build.CSRC, src), "-o", obj])
+        return obj
+
+    with concurrent.futures.ThreadPoolExecutor(max_workers=len(sources)) as ex:
+        checked = list(ex.map(instrumented, sources))
+    drv = os.path.join(OUT, "operators_driver.o")
+    _run(["gcc", "-std=c99", "-O1", "-g", "-Wall", "-Werror", "-fsanitize=address,undefined", "-fno-sanitize-recover=all",
+          "-D__HIP_PLATFORM_AMD__", "-I", os.path.join(ROOT, "include"), "-I", "/opt/rocm/include", "-c",
+          os.path.join(ROOT, "tests", "sanitize_operators.c"), "-o", drv])
+    exe = os.path.join(OUT, "operators_driver")
+    others = [o for n, o in objs.items() if n + ".cpp" not in sources and n + ".hip" not in sources]
+    _run([lib_build.HIPCC, f"--offload-arch={lib_build.ARCH}", "-Xarch_host", "-fsanitize=address", "-Xarch_host",
+          "-fsanitize=undefined", "-o", exe, drv, *checked, *others, "-L/opt/rocm/lib", "-lhipblaslt"])
     res = _run([exe], env=ENV)
     assert res.stdout.strip().endswith("ok")
