@@ -217,8 +217,7 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(SampleArgs a) {
             row.load(step + kAtOnce, next);
             if (step != 0) {
                 // 2^15 logits raise a count by as much at most: taken out of the
-                // counts that have reached it, the next ones fit too. Only values
-                // that may be drawn are listed: NaNs lie in +infinity's block too.
+                // counts that have reached it, the next ones fit too.
                 static_assert(kAtOnce * 8 * kThreads <= (int)kCarry, "counts of 16 bits");
                 __syncthreads();
                 for (int i = 0; i < 32; ++i) {
@@ -226,8 +225,8 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(SampleArgs a) {
                     if ((n & 0x80008000u) == 0) continue;
                     const uint32_t k = 2 * (32 * tid + i);
                     s.counts[word] = n & 0x7FFF7FFFu;
-                    if ((n & 0x8000u) && drawn(k)) s.carried[atomicAdd(&s.carries, 1)] = (uint16_t)k;
-                    if (n >> 31 && drawn(k + 1)) s.carried[atomicAdd(&s.carries, 1)] = (uint16_t)(k + 1 == K::kZero - 1 ? K::kZero : k + 1);
+                    if (n & 0x8000u) s.carried[atomicAdd(&s.carries, 1)] = (uint16_t)k;
+                    if (n >> 31) s.carried[atomicAdd(&s.carries, 1)] = (uint16_t)(k + 1 == K::kZero - 1 ? K::kZero : k + 1);
                 }
                 __syncthreads();
             }
@@ -258,6 +257,11 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(SampleArgs a) {
         // Block b holds the keys kKeys - 1 - 64 b - i, i = 0 .. 63, so that blocks
         // and i go down the order. Thread b holds block b's counts.
         const int carries = s.carries;
+        if (carries > 0) {  // NaNs among them, which lie in +infinity's block too: 0 is no value that may be drawn
+            for (int i = tid; i < carries; i += kThreads)
+                if (!drawn(s.carried[i])) s.carried[i] = 0;
+            __syncthreads();
+        }
         auto carried = [&](uint32_t k) {
             uint32_t n = 0;
             for (int i = 0; i < carries; ++i) n += s.carried[i] == k ? kCarry : 0u;
