@@ -304,7 +304,8 @@ struct Attend {
                     }
                 // Never 0, which times an unseen score's -infinity is NaN: the least number in its
                 // place moves a score by less than 2^-21, since products are below 2^128.
-                factor[h] = fmaxf(__builtin_ldexpf(factor[h], -up), 0x1p-149f);
+                factor[h] = __builtin_ldexpf(factor[h], -up);
+                if (factor[h] == 0.0f) factor[h] = 0x1p-149f;
             }
         }
     }
