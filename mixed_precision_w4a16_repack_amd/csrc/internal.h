@@ -2,8 +2,10 @@
 // of libw4a16.so (not installed, not part of the ABI).
 #pragma once
 
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
+#include <mutex>
 
 #include <hip/hip_runtime.h>
 
@@ -59,15 +61,24 @@ struct MfmaPlan {
     size_t partial_bytes = 0;  // fp32 partial tiles in the workspace
 };
 
-// Raises a kernel's dynamic-LDS limit (needed above 64 KB); cached per kernel
-// (the template parameter is the kernel itself, so each has its own cache).
+// Raises a kernel's dynamic-LDS limit (needed above 64 KB) on the current
+// device: each device has its own. Cached per kernel (the template parameter is
+// the kernel itself) and device; the limit is never lowered.
+constexpr int kLdsDevices = 64;
 template <auto Kernel>
 inline hipError_t allow_lds(size_t bytes) {
-    static size_t granted = 64 * 1024;
-    if (bytes <= granted) return hipSuccess;
-    hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(Kernel),
-                                       hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-    if (e == hipSuccess) granted = bytes;
+    static std::atomic<size_t> granted[kLdsDevices];
+    static std::mutex raising;
+    if (bytes <= 64 * 1024) return hipSuccess;
+    int device = 0;
+    hipError_t e = hipGetDevice(&device);
+    if (e != hipSuccess) return e;
+    if (device < 0 || device >= kLdsDevices) return hipErrorInvalidDevice;
+    if (bytes <= granted[device].load(std::memory_order_acquire)) return hipSuccess;
+    std::lock_guard<std::mutex> lock(raising);
+    if (bytes <= granted[device].load(std::memory_order_relaxed)) return hipSuccess;
+    e = hipFuncSetAttribute(reinterpret_cast<const void*>(Kernel), hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e == hipSuccess) granted[device].store(bytes, std::memory_order_release);
     return e;
 }
 

@@ -6,6 +6,8 @@ from __future__ import annotations
 
 import ctypes
 import os
+import shutil
+import subprocess
 
 import numpy as np
 import pytest
@@ -308,3 +310,15 @@ def test_calls_run_with_their_tensors_device_current(monkeypatch):
     with pytest.raises(RuntimeError, match="w4a16 status 1"):
         w4._call(2, entry, 1)
     assert ran == [0, 1, 2] and current == [0]
+
+
+@pytest.mark.skipif(shutil.which("g++") is None, reason="needs g++")
+def test_lds_limits_are_raised_on_each_device(tmp_path):
+    """A kernel's limit is the device's: a call on another device raises its own, and calls at once never lower one."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    exe = str(tmp_path / "lds_limit")
+    subprocess.run(["g++", "-std=c++17", "-O1", "-pthread", "-D__HIP_PLATFORM_AMD__", "-I", os.path.join(root, "include"),
+                    "-I", os.path.join(root, "mixed_precision_w4a16_repack_amd", "csrc"), "-isystem", "/opt/rocm/include",
+                    os.path.join(root, "tests", "lds_limit.cpp"), "-o", exe], check=True, capture_output=True, text=True)
+    res = subprocess.run([exe], capture_output=True, text=True)
+    assert res.returncode == 0 and res.stdout.strip() == "ok", res.stdout
