@@ -31,10 +31,11 @@
 // exponentials) and 68 scalar ones; the matrix cores are busy for 42 % of the time and the
 // other vector instructions take as much again, and the two waves of a SIMD overlap little of it:
 // without the products, the exponentials or the loads the time falls by about that part's own.
-// Four prompts of 2048 tokens, 32 heads of 128 over 8, bf16: 228 us, 605 TFLOP/s
-// (the two-operand products counted once); 24 trees of 32 tokens over 3000 on average: 79 us;
-// two trees of 80 tokens over 50000 of int8, 64 heads: 435 us, 602 TFLOP/s; one tree of 16
-// tokens over 700: 20 us, of which 4 find the share and 4 join.
+// Four prompts of 2048 tokens, 32 heads of 128 over 8, bf16: 229 us a call, 601 TFLOP/s
+// (the two-operand products counted once; 222 to 237 between boxes and ways of timing); 24
+// trees of 32 tokens over up to 6000: 80 us; two trees of 80 tokens over 50000 of int8, 64
+// heads: 432 us, 606 TFLOP/s; one tree of 16 tokens over 700: 20 us, of which 4 find the
+// share and 4 join.
 // Columns of 64 rows a wave with one workgroup a CU: 702 us for the 255 of then.
 #include <cmath>
 
@@ -957,7 +958,11 @@ template <int KIND>
 Shape plan(const TokensArgs& a) {
     Shape s{};
     const int64_t group = a.Hq / a.H;
-    s.ht = a.D <= kMostWide<KIND> && a.T * group > 64 * a.B ? 2 : 1;  // where sequences have more than 64 rows on average
+    // Where sequences have more than 64 rows on average. 64 of them over 2000 tokens, heads of 128, us with
+    // blocks of 64 and 128: 64 rows each 108 and 112 (int8 91 and 112), 80 rows 200 and 114 (161 and 118).
+    // With few sequences 64 stays ahead for longer (4 of 128 rows: 28 and 36). Of steps that mix, 60 single
+    // tokens and a prompt of 900 have 64 by this rule (118 and 123), with 8 parts of 512 tokens 128 (344 and 304).
+    s.ht = a.D <= kMostWide<KIND> && a.T * group > 64 * a.B ? 2 : 1;
     by_shape<KIND>(a.D, s.ht, [&](auto d, auto ht) {
         using A = Attend<0, KIND, decltype(d)::value, decltype(ht)::value>;
         s.wgs = kCUs * A::kPerCU;

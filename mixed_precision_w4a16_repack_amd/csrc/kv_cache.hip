@@ -357,7 +357,7 @@ __device__ __forceinline__ void turn(const Angle& w, float& x, float& y) {
 
 // One wave per (token, query or key or value head); a lane holds pairs. For few
 // tokens, which are bound by the chain of waits from the slot to the store:
-// 8 tokens of int8 4 us, 384 of 16 bits 7.1 us.
+// 8 tokens of int8 4.1 us, 128 of 16 bits 4.6 us (32 query and 8 key and value heads of 128).
 template <int DT, int KIND>
 __global__ __launch_bounds__(256) void kv_append_rows_kernel(KvAppendArgs a) {
     using L = KvPlace<KIND>;
@@ -423,8 +423,9 @@ __global__ __launch_bounds__(256) void kv_append_rows_kernel(KvAppendArgs a) {
 // of its heads, and so their sines once.
 //
 // Bound by bytes: 8000 tokens of 32 query and 8 key and value heads of 128,
-// 197 MB read and written, 47.7 us (4.1 TB/s; a copy reaches 5.3). About 4096
-// workgroups turn (3 heads each here): with 1024, 2048 and 8192 it is 55, 50 and 52 us.
+// 197 MB read and written, 44.1 us (4.5 TB/s; a copy reaches 5.3); 384 tokens 6.7 us.
+// About 4096 workgroups turn (3 heads each here): calls of the 8000 tokens took 51.5 us
+// with that, and 55, 50 and 52 with 1024, 2048 and 8192.
 template <int DT, int KIND, int D>
 __global__ __launch_bounds__(2 * D) void kv_append_tile_kernel(KvAppendArgs a) {
     using L = KvPlace<KIND>;
@@ -723,7 +724,10 @@ hipError_t run(KvArgs a, bool write, int kind, int dtype, hipStream_t stream) {
     return hipGetLastError();
 }
 
-// Up to this many (token, head) of queries, keys and values, a wave for each.
+// Up to this many (token, head) of queries, keys and values, a wave for each. Of
+// 48 rows a token, heads of 128: 3072 rows 3.9 us against 4.2 with tiles (int8 4.2
+// and 4.5), 6144 4.6 and 4.2 (int8 4.8 and 4.6; in scattered slots 4.7 and 5.5), 8160
+// 5.2 and 4.3 (5.6 and 5.1; 5.4 and 5.6), 12288 6.5 and 4.7 (7.2 and 5.2; 6.7 and 5.8).
 constexpr int64_t kAppendRowsMost = 8192;
 
 template <int DT, int KIND>
