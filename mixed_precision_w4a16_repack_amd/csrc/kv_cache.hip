@@ -725,9 +725,9 @@ hipError_t run(KvArgs a, bool write, int kind, int dtype, hipStream_t stream) {
 }
 
 // Up to this many (token, head) of queries, keys and values, a wave for each. Of
-// 48 rows a token, heads of 128: 3072 rows 3.9 us against 4.2 with tiles (int8 4.2
-// and 4.5), 6144 4.6 and 4.2 (int8 4.8 and 4.6; in scattered slots 4.7 and 5.5), 8160
-// 5.2 and 4.3 (5.6 and 5.1; 5.4 and 5.6), 12288 6.5 and 4.7 (7.2 and 5.2; 6.7 and 5.8).
+// tokens of 48 of them, heads of 128: 64 tokens 3.9 us against 4.2 with tiles (int8
+// 4.2 and 4.5), 128 4.6 and 4.2 (int8 4.8 and 4.6; in scattered slots 4.7 and 5.5),
+// 170 5.2 and 4.3 (5.6 and 5.1; 5.4 and 5.6), 256 6.5 and 4.7 (7.2 and 5.2; 6.7 and 5.8).
 constexpr int64_t kAppendRowsMost = 8192;
 
 template <int DT, int KIND>
